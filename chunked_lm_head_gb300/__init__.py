@@ -9,3 +9,5 @@ from .api import (IGNORE_INDEX, DistillLoss, GRPOLoss, LinearCrossEntropy,  # no
                   backward, distill_loss, forward, forward_backward, grpo_loss, grpo_token_loss,
                   jsd_backward, jsd_forward, kd_backward, kd_forward, linear_cross_entropy,
                   scale_grads, selective_log_softmax, workspace_bytes)
+from .norm import (RMSNorm, RMSNormFunction, rms_norm, rms_norm_backward, rms_norm_e4m3,  # noqa: F401
+                   rms_norm_forward)

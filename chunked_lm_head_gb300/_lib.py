@@ -93,6 +93,16 @@ SIGNATURES = {
                                              _c_vp, _c_vp, _c_vp, ctypes.c_float, ctypes.c_float, _c_vp,
                                              _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp,
                                              ctypes.c_size_t, _c_vp]),
+    "flce_rms_norm": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, ctypes.c_int32, _c_vp, ctypes.c_int32,
+                                     ctypes.c_float, ctypes.c_float, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp,
+                                     _c_vp]),
+    "flce_rms_norm_e4m3": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, ctypes.c_int32, _c_vp, ctypes.c_int32,
+                                          ctypes.c_float, ctypes.c_float, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp,
+                                          _c_vp, _c_vp]),
+    "flce_rms_norm_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_i64, ctypes.c_int32, _c_vp, _c_vp,
+                                              ctypes.c_int32, ctypes.c_float, _c_vp, _c_i64, _c_i64, _c_vp,
+                                              _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
+    "flce_rms_norm_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64]),
     "flce_scale_grads": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp]),
     "flce_set_option": (ctypes.c_int, [ctypes.c_int, _c_i64]),
     "flce_get_option": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_int64)]),
@@ -105,6 +115,10 @@ SIGNATURES = {
     "flce_profile_read": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_double),
                                          ctypes.POINTER(ctypes.c_int64)]),
 }
+
+# flce_dtype
+DTYPES = {"bf16": 0, "f32": 1, "f16": 2, "i32": 3, "i64": 4}
+
 
 class LogitTransform(ctypes.Structure):
     """flce_logit_transform: multiply, divide, soft-cap, temperature (0/0/0/1 = identity)."""
@@ -414,6 +428,34 @@ def flce_forward_backward(h, W, targets, weights, N, H, V, chunk_rows, ignore_in
                                      _ptr(out_lse), _ptr(out_loss), _ptr(out_n_valid), _ptr(dH),
                                      _ptr(dW), _ptr(workspace), workspace_bytes,
                                      _stream_handle(stream))
+
+
+def flce_rms_norm(x, ldx, residual, ldr, residual_type, weight, weight_type, weight_offset, eps, N, H, out_y,
+                  out_residual, out_rstd, stream=None) -> int:
+    """Raw C call of the residual addition and RMS norm (bf16 output)."""
+    return load().flce_rms_norm(_ptr(x), ldx, _ptr(residual), ldr, residual_type, _ptr(weight), weight_type,
+                                weight_offset, eps, N, H, _ptr(out_y), _ptr(out_residual), _ptr(out_rstd),
+                                _stream_handle(stream))
+
+
+def flce_rms_norm_e4m3(x, ldx, residual, ldr, residual_type, weight, weight_type, weight_offset, eps, N, H,
+                       out_q, out_scale, out_residual, out_rstd, stream=None) -> int:
+    """Raw C call of the residual addition and RMS norm with e4m3 rows and scales."""
+    return load().flce_rms_norm_e4m3(_ptr(x), ldx, _ptr(residual), ldr, residual_type, _ptr(weight), weight_type,
+                                     weight_offset, eps, N, H, _ptr(out_q), _ptr(out_scale), _ptr(out_residual),
+                                     _ptr(out_rstd), _stream_handle(stream))
+
+
+def flce_rms_norm_backward(dy, s, lds, s_type, ds, weight, weight_type, weight_offset, rstd, N, H, dx, dr,
+                           dweight, workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Raw C call of the RMS norm's gradients."""
+    return load().flce_rms_norm_backward(_ptr(dy), _ptr(s), lds, s_type, _ptr(ds), _ptr(weight), weight_type,
+                                         weight_offset, _ptr(rstd), N, H, _ptr(dx), _ptr(dr), _ptr(dweight),
+                                         _ptr(workspace), workspace_bytes, _stream_handle(stream))
+
+
+def flce_rms_norm_backward_workspace_bytes(N, H) -> int:
+    return int(load().flce_rms_norm_backward_workspace_bytes(N, H))
 
 
 def flce_quantize_e4m3_rows(x, rows, cols, q, scale, stream=None) -> int:

@@ -23,6 +23,7 @@
 #include "host_common.cuh"
 #include "plan.cuh"
 #include "launch.cuh"
+#include "norm_api.cuh"
 
 namespace {
 using namespace flce;

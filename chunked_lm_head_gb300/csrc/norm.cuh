@@ -1,0 +1,306 @@
+// libflce: the root-mean-square norm in front of the LM head, with the
+// residual's addition, in bf16 or in e4m3 with one scale per row, and its
+// backward.
+//
+// Per row, with s the residual stream as it is stored:
+//   s    = round(x + r)            (r's type; s = x without a residual)
+//   rstd = 1 / sqrt(sum_j s_j^2 / H + eps)
+//   y_j  = s_j rstd gain_j,        gain_j = weight_j + offset
+// bf16: y rounded once.  e4m3: scale = max_j |y_j| / 448, q_j = e4m3(y_j / scale)
+// straight from the 32-bit y.  Backward, with g_j = dy_j gain_j:
+//   ds_j = up_j + rstd (g_j - s_j rstd^2 (sum_k g_k s_k) / H)
+//   dweight_j = sum_rows dy_j s_j rstd
+// (up: the gradient that reaches the stream past the norm).  Every sum is in
+// fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "gemm.cuh"
+
+namespace flce {
+
+struct NoResidual {};  // kernel residual type of a call without one
+
+// 8 consecutive elements, as fp32.
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+// 8 values rounded to the element type; v becomes what was stored.
+__device__ __forceinline__ void store8(uint16_t* p, float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    v[2 * k] = __uint_as_float(w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// 8 gains from column c on: weight (fp32 or bf16) + offset.
+__device__ __forceinline__ void gain8(const void* w, int f32, float offset, int c, float (&v)[8]) {
+  if (f32)
+    load8(static_cast<const float*>(w) + c, v);
+  else
+    load8(static_cast<const uint16_t*>(w) + c, v);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] += offset;
+}
+
+// Sum and maximum over the TPR threads of one row (TPR a multiple of 32; the
+// whole CTA when it is more), in a fixed order.  smem: 2 * TPR / 32 floats.
+template <int TPR, bool kMax>
+__device__ __forceinline__ void row_reduce(float& sum, float& top, float* smem) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if constexpr (kMax) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  }
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) {
+      smem[warp] = sum;
+      if constexpr (kMax) smem[W + warp] = top;
+    }
+    __syncthreads();
+    sum = lane < W ? smem[lane] : 0.f;
+    if constexpr (kMax) top = lane < W ? smem[W + lane] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if constexpr (kMax) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    }
+  }
+}
+
+struct NormParams {
+  const uint16_t* x;
+  const void* r;       // residual, R
+  const void* weight;  // bf16, or fp32 with w_f32
+  long long ldx, ldr;  // row strides of x and r, in elements
+  int N, H, w_f32;
+  float offset, eps;
+  uint16_t* y;         // bf16 [N][H]
+  uint8_t* q;          // e4m3 [N][H] and
+  float* scale;        // its row scales [N]
+  void* s;             // the stream [N][H], R
+  float* rstd;         // [N], or null
+};
+
+// One row on TPR threads, VPT vectors of 8 elements to a thread in registers
+// (H <= 8 TPR VPT): the row is read once.  TPR 32: 8 rows to a CTA.
+template <class R, bool kQ, int TPR, int VPT>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+    rms_norm_kernel(const __grid_constant__ NormParams p) {
+  constexpr bool kRes = !std::is_same<R, NoResidual>::value;
+  constexpr int CTA = TPR < 256 ? 256 : TPR;
+  constexpr int ROWS = CTA / TPR;
+  static_assert(TPR == 32 || ROWS == 1, "a row is a warp's or a CTA's");
+  __shared__ float red[2 * CTA / 32];
+  const int t = threadIdx.x % TPR;
+  const int row = blockIdx.x * ROWS + threadIdx.x / TPR;
+  if (row >= p.N) return;  // whole warps (TPR 32), or no row at all
+  const uint16_t* x = p.x + row * p.ldx;
+  const long long o = static_cast<long long>(row) * p.H;
+  const int nv = p.H / 8;
+
+  // 8 elements of the stream from column c on, stored when there is a residual
+  auto stream8 = [&](int c, float (&v)[8]) {
+    load8(x + c, v);
+    if constexpr (kRes) {
+      float r8[8];
+      load8(static_cast<const R*>(p.r) + row * p.ldr + c, r8);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += r8[k];
+      store8(static_cast<R*>(p.s) + o + c, v);
+    }
+  };
+  float sum = 0.f, top = 0.f;
+  float s[VPT][8];
+  // one vector's share of the sum of squares; with kQ v becomes s gain and
+  // its largest magnitude counts (max_j |y_j| = rstd max_j |s_j gain_j|)
+  auto take8 = [&](int c, float (&v)[8]) {
+    float g8[8];
+    if constexpr (kQ) gain8(p.weight, p.w_f32, p.offset, c, g8);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      sum = fmaf(v[k], v[k], sum);
+      if constexpr (kQ) {
+        v[k] *= g8[k];
+        top = fmaxf(top, fabsf(v[k]));
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if (t + i * TPR < nv) stream8((t + i * TPR) * 8, s[i]);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if (t + i * TPR < nv) take8((t + i * TPR) * 8, s[i]);
+  row_reduce<TPR, kQ>(sum, top, red);
+  const float rstd = 1.f / sqrtf(sum / static_cast<float>(p.H) + p.eps);
+  float f = rstd;
+  if constexpr (kQ) {
+    const float amax = rstd * top;
+    // an all-zero row, and one that holds a NaN or an infinity, has scale 1
+    const float sc = amax > 0.f ? amax / 448.f : 1.f;
+    if (t == 0) p.scale[row] = sc;
+    f = rstd / sc;
+  }
+  if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+  auto put8 = [&](int c, float (&v)[8]) {
+    if constexpr (kQ) {
+      uint32_t b[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * k] * f, v[4 * k + 1] * f),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * k + 2] * f, v[4 * k + 3] * f),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        b[k] = lo | (hi << 16);
+      }
+      *reinterpret_cast<uint2*>(p.q + o + c) = make_uint2(b[0], b[1]);
+    } else {
+      float g8[8];
+      gain8(p.weight, p.w_f32, p.offset, c, g8);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = v[k] * f * g8[k];
+      store8(p.y + o + c, v);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if (t + i * TPR < nv) put8((t + i * TPR) * 8, s[i]);
+}
+
+struct NormBwdParams {
+  const uint16_t* dy;  // [N][H] bf16
+  const void* s;       // the stream, S, row stride lds
+  const void* up;      // [N][H] S: gradient of the stream, or null
+  const void* weight;  // bf16, or fp32 with w_f32
+  const float* rstd;
+  long long lds;
+  int N, H, w_f32;
+  float offset;
+  uint16_t* dx;        // bf16 [N][H]
+  float* dr;           // fp32 [N][H] (S fp32), or null
+  float* part;         // dweight partials [gridDim.x * rows per CTA][H], or null
+};
+
+// Backward rows, dealt to the row slots (a warp, or a CTA of TPR threads) in
+// turn; each slot keeps its rows' dweight in registers and stores them once.
+template <class S, int TPR, int VPT>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+    rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+  constexpr int CTA = TPR < 256 ? 256 : TPR;
+  constexpr int ROWS = CTA / TPR;
+  __shared__ float red[2][2 * CTA / 32];
+  const int t = threadIdx.x % TPR;
+  const int slot = blockIdx.x * ROWS + threadIdx.x / TPR;
+  const int slots = gridDim.x * ROWS;
+  const int nv = p.H / 8;
+  float dw[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[i][k] = 0.f;
+  int phase = 0;
+  for (int row = slot; row < p.N; row += slots, phase ^= 1) {
+    const S* s = static_cast<const S*>(p.s) + row * p.lds;
+    const long long o = static_cast<long long>(row) * p.H;
+    const float rstd = p.rstd[row];
+    float sv[VPT][8], g[VPT][8];
+    float dot = 0.f, none = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (t + i * TPR) * 8;
+      if (t + i * TPR < nv) {
+        load8(s + c, sv[i]);
+        load8(p.dy + o + c, g[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (t + i * TPR) * 8;
+      if (t + i * TPR < nv) {
+        float w8[8];
+        gain8(p.weight, p.w_f32, p.offset, c, w8);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          dw[i][k] = fmaf(g[i][k], sv[i][k] * rstd, dw[i][k]);
+          g[i][k] *= w8[k];
+          dot = fmaf(g[i][k], sv[i][k], dot);
+        }
+      }
+    }
+    row_reduce<TPR, false>(dot, none, red[phase]);
+    const float k2 = dot / static_cast<float>(p.H) * rstd * rstd;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (t + i * TPR) * 8;
+      if (t + i * TPR < nv) {
+        float d[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = rstd * (g[i][k] - sv[i][k] * k2);
+        if (p.up != nullptr) {
+          float u8[8];
+          load8(static_cast<const S*>(p.up) + o + c, u8);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) d[k] += u8[k];
+        }
+        if (p.dr != nullptr) store8(p.dr + o + c, d);
+        if (p.dx != nullptr) store8(p.dx + o + c, d);
+      }
+    }
+  }
+  if (p.part != nullptr) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (t + i * TPR < nv) store8(p.part + static_cast<long long>(slot) * p.H + (t + i * TPR) * 8, dw[i]);
+  }
+}
+
+// dweight = the partials' sum over the slots, in slot order (32 columns to a
+// CTA, 8 runs of slots joined at the end).
+template <class W>
+__global__ void norm_dweight_kernel(const float* __restrict__ part, int slots, int H, W* __restrict__ dw) {
+  __shared__ float sh[8][33];
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float a = 0.f;
+  if (c < H)
+    for (int i = run; i < slots; i += 8) a += part[static_cast<long long>(i) * H + c];
+  sh[run][lane] = a;
+  __syncthreads();
+  if (run == 0 && c < H) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) a += sh[k][lane];
+    if constexpr (std::is_same<W, float>::value)
+      dw[c] = a;
+    else
+      dw[c] = static_cast<uint16_t>(pack_bf16x2(a, 0.f) & 0xffffu);
+  }
+}
+
+}  // namespace flce

@@ -75,6 +75,15 @@ typedef enum {
   FLCE_ERR_TIMEOUT = 6       /* a kernel's bounded wait ran out (device error word) */
 } flce_status;
 
+/* Element types of the arrays that may have one of several. */
+typedef enum {
+  FLCE_BF16 = 0,
+  FLCE_F32 = 1,
+  FLCE_F16 = 2,
+  FLCE_I32 = 3,
+  FLCE_I64 = 4
+} flce_dtype;
+
 /*
  * Logit transforms applied elementwise to z before the log-softmax, in this
  * order: multiply, divide, soft-cap, temperature.  Source: Unsloth,
@@ -527,6 +536,62 @@ FLCE_API flce_status flce_forward_e4m3(const uint8_t* h8, const float* h_scale, 
                                        const flce_logit_transform* transform, float* out_logp,
                                        float* out_lse, float* out_loss, int64_t* out_n_valid,
                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Root-mean-square norm in front of the LM head, with the residual's
+ * addition (an addition of this library: the pages start at the hidden
+ * states).  Per row, with s the residual stream as it is stored,
+ *   s    = round(x + residual)      (residual's type; s = x without one)
+ *   rstd = 1 / sqrt(mean_j s_j^2 + eps)
+ *   y_j  = s_j * rstd * (weight_j + weight_offset).
+ *   x        [N,H] bf16, rows ldx elements apart.
+ *   residual [N,H] bf16 or fp32 (residual_type), rows ldr elements apart, or
+ *            NULL; out_residual [N,H] of its type, contiguous: NULL exactly
+ *            when residual is.  No output may overlap an input.
+ *   weight   [H] bf16 or fp32 (weight_type); weight_offset 1 for a gain stored
+ *            as its distance from one.
+ *   eps      >= 0.
+ *   out_y    [N,H] bf16, contiguous.  out_rstd [N] fp32 or NULL
+ *            (flce_rms_norm_backward needs it).
+ * H <= 32,768 and a multiple of 8 (e4m3: of 16), arrays 16-byte aligned, row
+ * strides of whole 16 bytes, else FLCE_ERR_UNSUPPORTED.
+ *
+ * flce_rms_norm_e4m3 gives the operands of flce_forward_e4m3 instead of y:
+ * out_scale[i] = max_j |y_ij| / 448 (1 for an all-zero row and for one that
+ * holds a NaN or an infinity) and out_q = e4m3(y / scale), round to nearest
+ * even, saturating, from the 32-bit y (not through bf16).
+ */
+FLCE_API flce_status flce_rms_norm(const flce_bf16* x, int64_t ldx, const void* residual, int64_t ldr,
+                                   int32_t residual_type, const void* weight, int32_t weight_type,
+                                   float weight_offset, float eps, int64_t N, int64_t H,
+                                   flce_bf16* out_y, void* out_residual, float* out_rstd, void* stream);
+FLCE_API flce_status flce_rms_norm_e4m3(const flce_bf16* x, int64_t ldx, const void* residual, int64_t ldr,
+                                        int32_t residual_type, const void* weight, int32_t weight_type,
+                                        float weight_offset, float eps, int64_t N, int64_t H,
+                                        uint8_t* out_q, float* out_scale, void* out_residual,
+                                        float* out_rstd, void* stream);
+
+/*
+ * Gradients of flce_rms_norm, with g_j = dy_j (weight_j + weight_offset):
+ *   d_j       = ds_j + rstd (g_j - s_j rstd^2 mean_k(g_k s_k))
+ *   dweight_j = sum_rows dy_j s_j rstd
+ *   dy  [N,H] bf16; s [N,H] the stream that was normed (x, or out_residual),
+ *       of s_type, rows lds elements apart; ds [N,H] of s_type, the gradient
+ *       that reaches the stream past the norm, or NULL; rstd [N] from the
+ *       forward.
+ *   dx  [N,H] bf16 = d; dr [N,H] fp32 = d (the residual's gradient where the
+ *       stream is fp32); dweight [H] of weight_type.  Each may be NULL, not
+ *       all.  Arrays contiguous but for s.
+ * The sums are fp32 in a fixed order: same inputs, same bits.  Workspace (for
+ * dweight): flce_rms_norm_backward_workspace_bytes, or NULL (stream-ordered
+ * allocation).
+ */
+FLCE_API flce_status flce_rms_norm_backward(const flce_bf16* dy, const void* s, int64_t lds,
+                                            int32_t s_type, const void* ds, const void* weight,
+                                            int32_t weight_type, float weight_offset, const float* rstd,
+                                            int64_t N, int64_t H, flce_bf16* dx, float* dr, void* dweight,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+FLCE_API size_t flce_rms_norm_backward_workspace_bytes(int64_t N, int64_t H);
 
 /*
  * Forward that allocates nothing (no counterpart on the source pages: the
