@@ -67,25 +67,26 @@ __device__ __forceinline__ void gain8(const void* w, int f32, float offset, int 
   for (int k = 0; k < 8; ++k) v[k] += offset;
 }
 
-// Sum and maximum over the TPR threads of one row (TPR a multiple of 32; the
-// whole CTA when it is more), in a fixed order.  smem: 2 * TPR / 32 floats.
-template <int TPR, bool kMax>
-__device__ __forceinline__ void row_reduce(float& sum, float& top, float* smem) {
+// A CTA holds `groups` rows at a time, each on its own group of T threads (a
+// multiple of 32): sum (and maximum) over the group, in a fixed order, joined
+// through the group's 2 x 32 floats of shared memory behind a named barrier
+// (id 1 + group, at most 15 of them).  A group of one warp needs neither.
+template <bool kMax>
+__device__ __forceinline__ void group_reduce(float& sum, float& top, int T, int group, int t, float* smem) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if constexpr (kMax) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   }
-  if constexpr (TPR > 32) {
-    constexpr int W = TPR / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (T > 32) {
+    const int warp = t >> 5, lane = t & 31, warps = T >> 5;
     if (lane == 0) {
       smem[warp] = sum;
-      if constexpr (kMax) smem[W + warp] = top;
+      if constexpr (kMax) smem[32 + warp] = top;
     }
-    __syncthreads();
-    sum = lane < W ? smem[lane] : 0.f;
-    if constexpr (kMax) top = lane < W ? smem[W + lane] : 0.f;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(T) : "memory");
+    sum = lane < warps ? smem[lane] : 0.f;
+    if constexpr (kMax) top = lane < warps ? smem[32 + lane] : 0.f;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -100,6 +101,7 @@ struct NormParams {
   const void* weight;  // bf16, or fp32 with w_f32
   long long ldx, ldr;  // row strides of x and r, in elements
   int N, H, w_f32;
+  int T;               // threads of a row's group
   float offset, eps;
   uint16_t* y;         // bf16 [N][H]
   uint8_t* q;          // e4m3 [N][H] and
@@ -108,19 +110,18 @@ struct NormParams {
   float* rstd;         // [N], or null
 };
 
-// One row on TPR threads, VPT vectors of 8 elements to a thread in registers
-// (H <= 8 TPR VPT): the row is read once.  TPR 32: 8 rows to a CTA.
-template <class R, bool kQ, int TPR, int VPT>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
-    rms_norm_kernel(const __grid_constant__ NormParams p) {
+// One row on a group of T threads, VPT vectors of 8 elements to a thread in
+// registers (H <= 8 T VPT): the row is read once.
+constexpr int kNormGroups = 8;  // groups of a CTA at most
+
+template <class R, bool kQ, int VPT>
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ NormParams p) {
   constexpr bool kRes = !std::is_same<R, NoResidual>::value;
-  constexpr int CTA = TPR < 256 ? 256 : TPR;
-  constexpr int ROWS = CTA / TPR;
-  static_assert(TPR == 32 || ROWS == 1, "a row is a warp's or a CTA's");
-  __shared__ float red[2 * CTA / 32];
-  const int t = threadIdx.x % TPR;
-  const int row = blockIdx.x * ROWS + threadIdx.x / TPR;
-  if (row >= p.N) return;  // whole warps (TPR 32), or no row at all
+  __shared__ float red[kNormGroups][64];
+  const int T = p.T;
+  const int group = threadIdx.x / T, t = threadIdx.x - group * T;
+  const int row = blockIdx.x * (blockDim.x / T) + group;
+  if (row >= p.N) return;  // whole groups
   const uint16_t* x = p.x + row * p.ldx;
   const long long o = static_cast<long long>(row) * p.H;
   const int nv = p.H / 8;
@@ -154,11 +155,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   };
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if (t + i * TPR < nv) stream8((t + i * TPR) * 8, s[i]);
+    if (t + i * T < nv) stream8((t + i * T) * 8, s[i]);
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if (t + i * TPR < nv) take8((t + i * TPR) * 8, s[i]);
-  row_reduce<TPR, kQ>(sum, top, red);
+    if (t + i * T < nv) take8((t + i * T) * 8, s[i]);
+  group_reduce<kQ>(sum, top, T, group, t, red[group]);
   const float rstd = 1.f / sqrtf(sum / static_cast<float>(p.H) + p.eps);
   float f = rstd;
   if constexpr (kQ) {
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   };
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if (t + i * TPR < nv) put8((t + i * TPR) * 8, s[i]);
+    if (t + i * T < nv) put8((t + i * T) * 8, s[i]);
 }
 
 struct NormBwdParams {
@@ -202,100 +203,166 @@ struct NormBwdParams {
   const float* rstd;
   long long lds;
   int N, H, w_f32;
+  int T;               // threads of a row's group
   float offset;
-  uint16_t* dx;        // bf16 [N][H]
-  float* dr;           // fp32 [N][H] (S fp32), or null
-  float* part;         // dweight partials [gridDim.x * rows per CTA][H], or null
+  uint16_t* dx;        // bf16 [N][H], or null
+  float* dr;           // fp32 [N][H], or null
+  float* part;         // dweight partials [gridDim.x][H], or null
 };
 
-// Backward rows, dealt to the row slots (a warp, or a CTA of TPR threads) in
-// turn; each slot keeps its rows' dweight in registers and stores them once.
-template <class S, int TPR, int VPT>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
-    rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
-  constexpr int CTA = TPR < 256 ? 256 : TPR;
-  constexpr int ROWS = CTA / TPR;
-  __shared__ float red[2][2 * CTA / 32];
-  const int t = threadIdx.x % TPR;
-  const int slot = blockIdx.x * ROWS + threadIdx.x / TPR;
-  const int slots = gridDim.x * ROWS;
+// 8 elements as they lie in memory.
+template <class S>
+struct Raw8 {
+  uint4 q[sizeof(S) / 2];
+  __device__ __forceinline__ void load(const S* p) {
+#pragma unroll
+    for (int k = 0; k < static_cast<int>(sizeof(S) / 2); ++k) q[k] = reinterpret_cast<const uint4*>(p)[k];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < static_cast<int>(sizeof(S) / 2); ++k) q[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ float at(int k) const {
+    if constexpr (sizeof(S) == 4) {
+      const uint4& u = q[k / 4];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      return __uint_as_float(w[k % 4]);
+    } else {
+      const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+      return __uint_as_float((k & 1) ? (w[k / 2] & 0xffff0000u) : (w[k / 2] << 16));
+    }
+  }
+};
+
+// Backward rows, dealt to the grid's groups in turn.  A group's loads of its
+// next row are in flight while it reduces and writes the present one (kAhead);
+// each thread keeps its columns' dweight in registers over all its rows, the
+// groups of a CTA are joined in shared memory at the end, in group order.
+template <class S, int VPT, int MAXT, bool kAhead>
+__global__ void __launch_bounds__(MAXT, 1) rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+  __shared__ float red[2][kNormGroups][64];
+  extern __shared__ float dw_groups[];  // [groups - 1][H]
+  const int T = p.T;
+  const int group = threadIdx.x / T, t = threadIdx.x - group * T;
+  const int groups = blockDim.x / T;
   const int nv = p.H / 8;
-  float dw[VPT][8];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) dw[i][k] = 0.f;
-  int phase = 0;
-  for (int row = slot; row < p.N; row += slots, phase ^= 1) {
+  const int step = gridDim.x * groups;
+  struct Vec {
+    Raw8<S> s, up;
+    Raw8<uint16_t> dy;
+  };
+  auto load_row = [&](int row, Vec (&v)[VPT], float& rstd) {
+    rstd = p.rstd[row];
     const S* s = static_cast<const S*>(p.s) + row * p.lds;
     const long long o = static_cast<long long>(row) * p.H;
-    const float rstd = p.rstd[row];
-    float sv[VPT][8], g[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (t + i * T) * 8;
+      if (t + i * T < nv) {
+        v[i].s.load(s + c);
+        v[i].dy.load(p.dy + o + c);
+        if (p.up != nullptr) v[i].up.load(static_cast<const S*>(p.up) + o + c);
+      }
+    }
+  };
+  float dw[VPT][8];
+  Vec cur[VPT], ahead[kAhead ? VPT : 1];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    cur[i].up.zero();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[i][k] = 0.f;
+  }
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) ahead[i].up.zero();
+  }
+  float rstd = 0.f, rstd_ahead = 0.f;
+  int row = blockIdx.x * groups + group, phase = 0;
+  if (row < p.N) load_row(row, cur, rstd);
+  for (; row < p.N; row += step, phase ^= 1) {
+    if constexpr (kAhead) {
+      if (row + step < p.N) load_row(row + step, ahead, rstd_ahead);
+    }
     float dot = 0.f, none = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (t + i * TPR) * 8;
-      if (t + i * TPR < nv) {
-        load8(s + c, sv[i]);
-        load8(p.dy + o + c, g[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (t + i * TPR) * 8;
-      if (t + i * TPR < nv) {
+      if (t + i * T < nv) {
         float w8[8];
-        gain8(p.weight, p.w_f32, p.offset, c, w8);
+        gain8(p.weight, p.w_f32, p.offset, (t + i * T) * 8, w8);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          dw[i][k] = fmaf(g[i][k], sv[i][k] * rstd, dw[i][k]);
-          g[i][k] *= w8[k];
-          dot = fmaf(g[i][k], sv[i][k], dot);
+          const float sv = cur[i].s.at(k), dy = cur[i].dy.at(k);
+          dw[i][k] = fmaf(dy, sv * rstd, dw[i][k]);
+          dot = fmaf(dy * w8[k], sv, dot);
         }
       }
     }
-    row_reduce<TPR, false>(dot, none, red[phase]);
+    group_reduce<false>(dot, none, T, group, t, red[phase][group]);
     const float k2 = dot / static_cast<float>(p.H) * rstd * rstd;
+    const long long o = static_cast<long long>(row) * p.H;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (t + i * TPR) * 8;
-      if (t + i * TPR < nv) {
-        float d[8];
+      const int c = (t + i * T) * 8;
+      if (t + i * T < nv) {
+        float w8[8], d[8];
+        gain8(p.weight, p.w_f32, p.offset, c, w8);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = rstd * (g[i][k] - sv[i][k] * k2);
-        if (p.up != nullptr) {
-          float u8[8];
-          load8(static_cast<const S*>(p.up) + o + c, u8);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) d[k] += u8[k];
-        }
+        for (int k = 0; k < 8; ++k)
+          d[k] = fmaf(rstd, cur[i].dy.at(k) * w8[k] - cur[i].s.at(k) * k2, cur[i].up.at(k));
         if (p.dr != nullptr) store8(p.dr + o + c, d);
         if (p.dx != nullptr) store8(p.dx + o + c, d);
       }
     }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) cur[i] = ahead[i];
+      rstd = rstd_ahead;
+    } else {
+      if (row + step < p.N) load_row(row + step, cur, rstd);
+    }
   }
   if (p.part != nullptr) {
+    if (groups > 1) {
+      if (group > 0) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+          if (t + i * T < nv) store8(dw_groups + static_cast<size_t>(group - 1) * p.H + (t + i * T) * 8, dw[i]);
+      }
+      __syncthreads();
+      if (group > 0) return;
+      for (int g = 0; g < groups - 1; ++g)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+          if (t + i * T < nv) {
+            float v[8];
+            load8(dw_groups + static_cast<size_t>(g) * p.H + (t + i * T) * 8, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dw[i][k] += v[k];
+          }
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (t + i * TPR < nv) store8(p.part + static_cast<long long>(slot) * p.H + (t + i * TPR) * 8, dw[i]);
+      if (t + i * T < nv) store8(p.part + static_cast<long long>(blockIdx.x) * p.H + (t + i * T) * 8, dw[i]);
   }
 }
 
-// dweight = the partials' sum over the slots, in slot order (32 columns to a
-// CTA, 8 runs of slots joined at the end).
+// dweight = the partials' sum over the CTAs, in their order (32 columns to a
+// CTA, 32 runs of partials joined at the end).
 template <class W>
-__global__ void norm_dweight_kernel(const float* __restrict__ part, int slots, int H, W* __restrict__ dw) {
-  __shared__ float sh[8][33];
+__global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* __restrict__ part, int slots, int H,
+                                                           W* __restrict__ dw) {
+  __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.f;
   if (c < H)
-    for (int i = run; i < slots; i += 8) a += part[static_cast<long long>(i) * H + c];
+    for (int i = run; i < slots; i += 32) a += part[static_cast<long long>(i) * H + c];
   sh[run][lane] = a;
   __syncthreads();
   if (run == 0 && c < H) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) a += sh[k][lane];
+    for (int k = 1; k < 32; ++k) a += sh[k][lane];
     if constexpr (std::is_same<W, float>::value)
       dw[c] = a;
     else

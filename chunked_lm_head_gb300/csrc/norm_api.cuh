@@ -14,42 +14,67 @@ constexpr int64_t kNormMaxH = 32768;
 bool norm_sizes_ok(int64_t N, int64_t H) { return N >= 0 && H > 0 && N < INT_MAX && H < INT_MAX; }
 bool norm_dtype_ok(int32_t t) { return t == FLCE_BF16 || t == FLCE_F32; }
 
-// Calls go(threads per row, vectors per thread) with the narrowest row that
-// holds H: a warp up to 1,024 elements (no CTA barrier), then a CTA whose
-// threads hold one or two vectors, so that several CTAs per SM keep loads in
-// flight while others reduce.
-template <class Go>
-cudaError_t norm_shape(int64_t H, Go go) {
-  using std::integral_constant;
-  const int64_t nv = H / 8;
-  if (nv <= 32) return go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  if (nv <= 128) return go(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-  if (nv <= 256) return go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  if (nv <= 512) return go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  if (nv <= 1024) return go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-  return go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+// Threads of a row's group for VPT vectors of 8 elements to a thread.
+int norm_group(int64_t H, int vpt) { return static_cast<int>(round_up(ceil_div(H / 8, vpt), 32)); }
+// Groups of a CTA of about `threads`.
+int norm_groups(int T, int threads) { return std::max(1, std::min(kNormGroups, threads / T)); }
+
+template <bool kQ, int VPT>
+cudaError_t launch_norm_v(NormParams p, bool res, bool res_f32, int threads, cudaStream_t st) {
+  p.T = norm_group(p.H, VPT);
+  const int groups = norm_groups(p.T, threads);
+  const unsigned grid = static_cast<unsigned>(ceil_div(p.N, groups));
+  if (!res)
+    rms_norm_kernel<NoResidual, kQ, VPT><<<grid, groups * p.T, 0, st>>>(p);
+  else if (res_f32)
+    rms_norm_kernel<float, kQ, VPT><<<grid, groups * p.T, 0, st>>>(p);
+  else
+    rms_norm_kernel<uint16_t, kQ, VPT><<<grid, groups * p.T, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
+// Two vectors to a thread in CTAs of about 512 threads (131,072 x 2,560 without
+// a residual: 257 us, against 387 with one vector and 362 with four; CTAs of
+// 256 threads 480); rows of a warp or less one vector in CTAs of 256 (262,144 x
+// 256: 102 against 104 us); past 8,192 elements four, so that a row fits a CTA.
 template <bool kQ>
 cudaError_t launch_norm(const NormParams& p, bool res, bool res_f32, cudaStream_t st) {
-  return norm_shape(p.H, [&](auto tpr, auto vpt) -> cudaError_t {
-    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
-    constexpr int CTA = TPR < 256 ? 256 : TPR;
-    const unsigned grid = static_cast<unsigned>(ceil_div(p.N, CTA / TPR));
-    if (!res)
-      rms_norm_kernel<NoResidual, kQ, TPR, VPT><<<grid, CTA, 0, st>>>(p);
-    else if (res_f32)
-      rms_norm_kernel<float, kQ, TPR, VPT><<<grid, CTA, 0, st>>>(p);
-    else
-      rms_norm_kernel<uint16_t, kQ, TPR, VPT><<<grid, CTA, 0, st>>>(p);
-    return cudaGetLastError();
-  });
+  if (p.H <= 256) return launch_norm_v<kQ, 1>(p, res, res_f32, 256, st);
+  if (p.H <= 8192) return launch_norm_v<kQ, 2>(p, res, res_f32, 512, st);
+  return launch_norm_v<kQ, 4>(p, res, res_f32, 512, st);
 }
 
-// Row slots of the backward: rows in flight, each with a dweight partial.
-int64_t norm_bwd_ctas(int64_t N, int64_t H, int* rows_per_cta) {
-  *rows_per_cta = H / 8 <= 128 ? 8 : 1;
-  return std::max<int64_t>(1, std::min<int64_t>(ceil_div(N, *rows_per_cta), 4LL * device_sms()));
+// How the backward runs rows of H: vectors per thread, the group and the CTA.
+struct NormBwdShape {
+  int vpt, T, groups, ctas;
+};
+// One CTA of 512 threads to an SM, two vectors to a thread (16,384 x 4,096 bf16
+// with the stream's gradient: 93 us, against 116 with one vector and 99 with
+// four; two CTAs to an SM 96, their dweight partials twice as many).  Rows of
+// a warp or less: one vector, three CTAs to an SM (262,144 x 256: 97 us
+// against 166 with one CTA).
+NormBwdShape norm_bwd_shape(int64_t N, int64_t H) {
+  NormBwdShape b;
+  b.vpt = H <= 256 ? 1 : H <= 8192 ? 2 : 4;
+  b.T = norm_group(H, b.vpt);
+  b.groups = norm_groups(b.T, 512);
+  const int64_t most = static_cast<int64_t>(H <= 256 ? 3 : 1) * device_sms();
+  b.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(N, b.groups), most)));
+  return b;
+}
+
+template <class S>
+cudaError_t launch_norm_bwd(const NormBwdParams& p, const NormBwdShape& b, cudaStream_t st) {
+  // the groups' dweight to be joined: at most 7 x 2,048 floats
+  const size_t smem = p.part ? static_cast<size_t>(b.groups - 1) * p.H * 4 : 0;
+  auto go = [&](auto kern) -> cudaError_t {
+    kern<<<b.ctas, b.groups * b.T, smem, st>>>(p);
+    return cudaGetLastError();
+  };
+  if (b.vpt == 1) return go(rms_norm_bwd_kernel<S, 1, 512, true>);
+  if (b.vpt == 2) return go(rms_norm_bwd_kernel<S, 2, 512, true>);
+  if (b.T <= 512) return go(rms_norm_bwd_kernel<S, 4, 512, false>);
+  return go(rms_norm_bwd_kernel<S, 4, 1024, false>);
 }
 
 }  // namespace
@@ -118,9 +143,7 @@ flce_status flce_rms_norm_e4m3(const flce_bf16* x, int64_t ldx, const void* resi
 
 size_t flce_rms_norm_backward_workspace_bytes(int64_t N, int64_t H) {
   if (!norm_sizes_ok(N, H)) return 0;
-  int rows = 1;
-  const int64_t ctas = norm_bwd_ctas(N, H, &rows);
-  return align256(static_cast<size_t>(ctas) * rows * H * 4);
+  return align256(static_cast<size_t>(norm_bwd_shape(N, H).ctas) * H * 4);
 }
 
 flce_status flce_rms_norm_backward(const flce_bf16* dy, const void* s, int64_t lds, int32_t s_type,
@@ -141,8 +164,7 @@ flce_status flce_rms_norm_backward(const flce_bf16* dy, const void* s, int64_t l
     if (dweight) FLCE_CUDA_TRY(cudaMemsetAsync(dweight, 0, H * (weight_type == FLCE_F32 ? 4 : 2), st));
     return FLCE_OK;
   }
-  int rows = 1;
-  const int64_t ctas = norm_bwd_ctas(N, H, &rows);
+  const NormBwdShape b = norm_bwd_shape(N, H);
   Workspace ws;
   if (dweight) {
     const flce_status g =
@@ -165,24 +187,16 @@ flce_status flce_rms_norm_backward(const flce_bf16* dy, const void* s, int64_t l
   p.part = dweight ? static_cast<float*>(ws.ptr) : nullptr;
   {
     ProfScope ps(K_NORM_BWD, st);
-    FLCE_CUDA_TRY(norm_shape(H, [&](auto tpr, auto vpt) -> cudaError_t {
-      constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
-      constexpr int CTA = TPR < 256 ? 256 : TPR;
-      if (s_type == FLCE_F32)
-        rms_norm_bwd_kernel<float, TPR, VPT><<<static_cast<unsigned>(ctas), CTA, 0, st>>>(p);
-      else
-        rms_norm_bwd_kernel<uint16_t, TPR, VPT><<<static_cast<unsigned>(ctas), CTA, 0, st>>>(p);
-      return cudaGetLastError();
-    }));
+    p.T = b.T;
+    FLCE_CUDA_TRY(s_type == FLCE_F32 ? launch_norm_bwd<float>(p, b, st) : launch_norm_bwd<uint16_t>(p, b, st));
   }
   if (dweight) {
     ProfScope ps(K_NORM_BWD, st);
     const unsigned grid = static_cast<unsigned>(ceil_div(H, 32));
-    const int slots = static_cast<int>(ctas * rows);
     if (weight_type == FLCE_F32)
-      norm_dweight_kernel<<<grid, 256, 0, st>>>(p.part, slots, p.H, static_cast<float*>(dweight));
+      norm_dweight_kernel<<<grid, 1024, 0, st>>>(p.part, b.ctas, p.H, static_cast<float*>(dweight));
     else
-      norm_dweight_kernel<<<grid, 256, 0, st>>>(p.part, slots, p.H, static_cast<uint16_t*>(dweight));
+      norm_dweight_kernel<<<grid, 1024, 0, st>>>(p.part, b.ctas, p.H, static_cast<uint16_t*>(dweight));
     FLCE_CUDA_TRY(cudaGetLastError());
   }
   return FLCE_OK;

@@ -98,6 +98,9 @@ def rms_norm_backward(dy, s, weight, rstd, ds=None, weight_offset: float = 0.0, 
     dr = torch.empty((N, H), dtype=torch.float32, device=s.device) if need_dr and wide else None
     dw = torch.empty_like(weight) if need_dweight else None
     if dx is not None or dr is not None or dw is not None:
+        if workspace is None and dw is not None:  # torch's allocator keeps it for the next call
+            workspace = torch.empty(_lib.flce_rms_norm_backward_workspace_bytes(N, H), dtype=torch.uint8,
+                                    device=s.device)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _lib.check("flce_rms_norm_backward", _lib.flce_rms_norm_backward(
             dy, s, lds, _TYPES[s.dtype], ds, weight, _TYPES[weight.dtype], weight_offset, rstd, N, H, dx, dr, dw,
