@@ -11,3 +11,5 @@ from .api import (IGNORE_INDEX, DistillLoss, GRPOLoss, LinearCrossEntropy,  # no
                   scale_grads, selective_log_softmax, workspace_bytes)
 from .norm import (RMSNorm, RMSNormFunction, rms_norm, rms_norm_backward, rms_norm_e4m3,  # noqa: F401
                    rms_norm_forward)
+from .topk import (TopkDistill, TopkDistillOneCall, topk_distill_loss, topk_kd_backward,  # noqa: F401
+                   topk_kd_forward, topk_kd_forward_backward)

@@ -93,6 +93,18 @@ SIGNATURES = {
                                              _c_vp, _c_vp, _c_vp, ctypes.c_float, ctypes.c_float, _c_vp,
                                              _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp,
                                              ctypes.c_size_t, _c_vp]),
+    "flce_topk_kd_forward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64,
+                                            _c_i64, _c_vp, ctypes.c_uint32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+                                            _c_vp, ctypes.c_size_t, _c_vp]),
+    "flce_topk_kd_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_i64,
+                                             _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, ctypes.c_size_t,
+                                             _c_vp]),
+    "flce_topk_kd_forward_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64,
+                                                     _c_i64, _c_i64, _c_vp, ctypes.c_float, _c_vp, _c_vp, _c_vp,
+                                                     _c_vp, _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
+    "flce_topk_kd_state_bytes": (ctypes.c_size_t, [_c_i64, _c_i64]),
+    "flce_topk_kd_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64]),
+    "flce_topk_kd_forward_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64]),
     "flce_rms_norm": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, ctypes.c_int32, _c_vp, ctypes.c_int32,
                                      ctypes.c_float, ctypes.c_float, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp,
                                      _c_vp]),
@@ -131,6 +143,14 @@ class DeviceScale(ctypes.Structure):
     """flce_device_scale: a device fp32 scale and a device int64 count (each may be NULL)."""
 
     _fields_ = [("scale", ctypes.c_void_p), ("count", ctypes.c_void_p)]
+
+
+class TopLogits(ctypes.Structure):
+    """flce_top_logits: a teacher's stored top logits (device pointers)."""
+
+    _fields_ = [("ids", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("ld_ids", ctypes.c_int64), ("ld_logits", ctypes.c_int64), ("ids_type", ctypes.c_int32),
+                ("logits_type", ctypes.c_int32), ("k", ctypes.c_int32), ("tail", ctypes.c_int32)]
 
 
 def _dscale_ptr(scale, count):
@@ -428,6 +448,56 @@ def flce_forward_backward(h, W, targets, weights, N, H, V, chunk_rows, ignore_in
                                      _ptr(out_lse), _ptr(out_loss), _ptr(out_n_valid), _ptr(dH),
                                      _ptr(dW), _ptr(workspace), workspace_bytes,
                                      _stream_handle(stream))
+
+
+def _teacher_ptr(teacher):
+    return None if teacher is None else ctypes.addressof(teacher)
+
+
+def flce_topk_kd_forward(h, W, teacher, targets, weights, N, H, V, chunk_rows, ignore_index, transform, flags,
+                         out_kl, out_lse, out_loss, out_n_valid, state=None, workspace=None, workspace_bytes=0,
+                         stream=None) -> int:
+    """Raw C call of the distillation from top logits (teacher: a TopLogits)."""
+    lib = load()
+    tp, keep = _tf_ptr(transform)
+    return lib.flce_topk_kd_forward(_ptr(h), _ptr(W), _teacher_ptr(teacher), _ptr(targets), _ptr(weights), N, H, V,
+                                    chunk_rows, ignore_index, tp, int(flags), _ptr(out_kl), _ptr(out_lse),
+                                    _ptr(out_loss), _ptr(out_n_valid), _ptr(state), _ptr(workspace),
+                                    workspace_bytes, _stream_handle(stream))
+
+
+def flce_topk_kd_backward(h, W, state, grad_scale, scale, count, dH, dW, N, H, V, k, chunk_rows, transform,
+                          workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Raw C call of its gradients from the forward's state, with a device-side scale."""
+    lib = load()
+    tp, keep = _tf_ptr(transform)
+    dp, keep_d = _dscale_ptr(scale, count)
+    return lib.flce_topk_kd_backward(_ptr(h), _ptr(W), _ptr(state), float(grad_scale), dp, _ptr(dH), _ptr(dW), N, H,
+                                     V, k, chunk_rows, tp, _ptr(workspace), workspace_bytes, _stream_handle(stream))
+
+
+def flce_topk_kd_forward_backward(h, W, teacher, targets, weights, N, H, V, chunk_rows, ignore_index, transform,
+                                  grad_scale, out_kl, out_lse, out_loss, out_n_valid, dH, dW, workspace=None,
+                                  workspace_bytes=0, stream=None) -> int:
+    """Raw C call of the loss and gradients in one call."""
+    lib = load()
+    tp, keep = _tf_ptr(transform)
+    return lib.flce_topk_kd_forward_backward(_ptr(h), _ptr(W), _teacher_ptr(teacher), _ptr(targets), _ptr(weights),
+                                             N, H, V, chunk_rows, ignore_index, tp, float(grad_scale), _ptr(out_kl),
+                                             _ptr(out_lse), _ptr(out_loss), _ptr(out_n_valid), _ptr(dH), _ptr(dW),
+                                             _ptr(workspace), workspace_bytes, _stream_handle(stream))
+
+
+def flce_topk_kd_state_bytes(N, k) -> int:
+    return int(load().flce_topk_kd_state_bytes(N, k))
+
+
+def flce_topk_kd_workspace_bytes(N, H, V, k, chunk_rows) -> int:
+    return int(load().flce_topk_kd_workspace_bytes(N, H, V, k, chunk_rows))
+
+
+def flce_topk_kd_forward_backward_workspace_bytes(N, H, V, k, chunk_rows) -> int:
+    return int(load().flce_topk_kd_forward_backward_workspace_bytes(N, H, V, k, chunk_rows))
 
 
 def flce_rms_norm(x, ldx, residual, ldr, residual_type, weight, weight_type, weight_offset, eps, N, H, out_y,

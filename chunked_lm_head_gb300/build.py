@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libflce.so")
 SOURCES = ["flce.cu"]
 HEADERS = ["ptx.cuh", "gemm.cuh", "small_kernels.cuh", "host_common.cuh", "options.cuh", "plan.cuh",
-           "launch.cuh", "norm.cuh", "norm_api.cuh"]
+           "launch.cuh", "norm.cuh", "norm_api.cuh", "topk.cuh", "topk_api.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

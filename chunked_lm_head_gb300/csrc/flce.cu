@@ -1,7 +1,9 @@
 // libflce: the C-ABI entry points.  The tensor-core GEMM engine lives in
 // gemm.cuh, the CUDA-core kernels in small_kernels.cuh, the launch plans and
 // workspace layouts in plan.cuh, tensor maps, launches and shared stages in
-// launch.cuh.  include/flce.h states the contract of every entry point.
+// launch.cuh, the norm in norm.cuh and norm_api.cuh, the distillation from top
+// logits in topk.cuh and topk_api.cuh.  include/flce.h states the contract of
+// every entry point.
 #include <cuda.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -79,11 +81,12 @@ static flce_status forward_impl(const flce_bf16* h, const flce_bf16* W, const in
                                 int64_t ignore_index, const flce_logit_transform* transform,
                                 float* out_logp, float* out_lse, float* out_loss,
                                 int64_t* out_n_valid, void* workspace, size_t workspace_bytes,
-                                void* stream, size_t partials_cap, bool skip_ignored = false) {
+                                void* stream, size_t partials_cap, bool skip_ignored = false,
+                                const TopkCall* topk = nullptr) {
   if (!sizes_ok(N, H, V)) return FLCE_ERR_INVALID_ARG;
   GemmParams tfp{};
   if (!transform_params(transform, tfp)) return FLCE_ERR_INVALID_ARG;
-  if (!out_logp && !out_lse && !out_loss && !out_n_valid) return FLCE_ERR_INVALID_ARG;
+  if (!topk && !out_logp && !out_lse && !out_loss && !out_n_valid) return FLCE_ERR_INVALID_ARG;
   if (N > 0 && (!h || !W || !targets)) return FLCE_ERR_INVALID_ARG;
   if (H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
   if (!aligned(h, 16) || !aligned(W, 16) || !aligned(targets, 8) || !aligned(weights, 4) ||
@@ -105,12 +108,12 @@ static flce_status forward_impl(const flce_bf16* h, const flce_bf16* W, const in
   double* bsum = reinterpret_cast<double*>(wb + L.bsum);
   long long* bcnt = reinterpret_cast<long long*>(wb + L.bcnt);
   int* bad = reinterpret_cast<int*>(wb + L.bad);
-  const bool validate = validate_on();
+  const bool validate = validate_on() && !topk;  // a list's marks are no targets
   const int Ni = static_cast<int>(N);
 
   if (N > 0) {
     if (validate) FLCE_CUDA_TRY(cudaMemsetAsync(bad, 0, sizeof(int), st));
-    {
+    if (!topk) {
       ProfScope ps(K_PREP, st);
       prep_kernel<<<static_cast<int>(ceil_div(N, SMALL_THREADS)), SMALL_THREADS, 0, st>>>(
           targets, Ni, static_cast<int>(V), ignore_index, zt, validate ? bad : nullptr);
@@ -162,6 +165,11 @@ static flce_status forward_impl(const flce_bf16* h, const flce_bf16* W, const in
     p.ignore_index = ignore_index;
     p.partials = part;
     p.zt = zt;
+    if (topk) {
+      p.sp_ids = topk->rows.ids;
+      p.sp_val = topk->rows.val;
+      p.sp_k = topk->K;
+    }
     p.tf_softcap = tfp.tf_softcap;
     p.tf_a = tfp.tf_a;
     p.tf_b = tfp.tf_b;
@@ -188,12 +196,19 @@ static flce_status forward_impl(const flce_bf16* h, const flce_bf16* W, const in
         if (sg != FLCE_OK) return sg;
       }
       ProfScope ps(K_FWD, st);
-      FLCE_CUDA_TRY(launch_gemm<MODE_FWD>(cg, kLong, tA, tB, tB, q, std::min(q.num_units, workers), st));
+      const int w = std::min(q.num_units, workers);
+      FLCE_CUDA_TRY(topk ? launch_fwd_listed<MODE_FWD>(cg, kLong, tA, tB, q, w, st)
+                         : launch_gemm<MODE_FWD>(cg, kLong, tA, tB, tB, q, w, st));
+    }
+    if (topk) {
+      const flce_status sr = topk_rows(*topk, kLong, f, p, Ni, 0, Ni, nullptr, part, skip_ignored, 0, st);
+      if (sr != FLCE_OK) return sr;
+      return loss_sums(out_loss, out_n_valid, topk->bsum, topk->bcnt, ceil_div(N, TOPK_ROWS), st);
     }
     return ce_forward_tail(kLong, f, Ni, part, zt, targets, weights, ignore_index, out_logp, out_lse,
                            out_loss, out_n_valid, bsum, bcnt, st, skip_ignored);
   }
-  return loss_tail(f, out_loss, out_n_valid, bsum, bcnt, st);
+  return loss_sums(out_loss, out_n_valid, bsum, bcnt, topk ? 0 : f.nblk, st);
 }
 
 flce_status flce_forward_ex(const flce_bf16* h, const flce_bf16* W, const int64_t* targets,
@@ -240,7 +255,8 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
                                  int64_t chunk_rows, int64_t ignore_index,
                                  const flce_logit_transform* transform, void* workspace,
                                  size_t workspace_bytes, void* stream,
-                                 const long long* count_scale, const float* scale_dev = nullptr) {
+                                 const long long* count_scale, const float* scale_dev = nullptr,
+                                 const TopkCall* topk = nullptr) {
   if (!sizes_ok(N, H, V)) return FLCE_ERR_INVALID_ARG;
   GemmParams tfp{};
   if (!transform_params(transform, tfp)) return FLCE_ERR_INVALID_ARG;
@@ -259,7 +275,9 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   const int cg = cta_group();
   const int workers = device_workers(cg);
   const int tm = BM * cg;
-  const BwdPlan b = plan_backward_call(N, H, V, chunk_rows, workers, tm, dH != nullptr && dW != nullptr);
+  // (a list's columns are written over each slab's dlogits, between its launches)
+  const BwdPlan b = topk ? plan_backward(N, H, V, chunk_rows, workers, tm)
+                         : plan_backward_call(N, H, V, chunk_rows, workers, tm, dH != nullptr && dW != nullptr);
   const BwdLayout L = bwd_layout(N, H, b);
   Workspace ws;
   flce_status s = get_workspace(ws, workspace, workspace_bytes, L.total, st);
@@ -268,7 +286,7 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   uint16_t* Dbuf = reinterpret_cast<uint16_t*>(wb + L.D);
   float* dh_part = b.dh_f32 ? reinterpret_cast<float*>(wb + L.dh_part) : nullptr;
 
-  if (validate_on()) {
+  if (validate_on() && !topk) {
     int* bad = reinterpret_cast<int*>(wb + L.bad);
     FLCE_CUDA_TRY(cudaMemsetAsync(bad, 0, sizeof(int), st));
     prep_kernel<<<static_cast<int>(ceil_div(N, SMALL_THREADS)), SMALL_THREADS, 0, st>>>(
@@ -410,6 +428,12 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
         FLCE_CUDA_TRY(launch_gemm<MODE_DLOGITS>(cg, kLong, A_dl, W_k, q.d_tma ? D_st : W_k, q,
                                                 std::min(q.num_units, workers), st));
       }
+      if (topk) {
+        const flce_status sc = topk_scatter(*topk, kLong, p, Dbuf, v0, width, static_cast<int>(row0), rows,
+                                            compact ? cidx : nullptr, compact ? ccount : nullptr,
+                                            static_cast<int>(row0), count_scale, nullptr, st);
+        if (sc != FLCE_OK) return sc;
+      }
       // (2) dH[rows] (+)= D W[slab], (3) dW[slab] (+)= D^T h[rows]
       const flce_status s2 = slab_dh_dw(dhdw, p, rows, block, slab, v0, width, D_k, D_mn, B_dw, st);
       if (s2 != FLCE_OK) return s2;
@@ -512,7 +536,8 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
                                          const flce_logit_transform* transform, float grad_scale,
                                          float* out_logp, float* out_lse, float* out_loss,
                                          int64_t* out_n_valid, flce_bf16* dH, float* dW, void* workspace,
-                                         size_t workspace_bytes, void* stream, const GrpoArgs* grpo) {
+                                         size_t workspace_bytes, void* stream, const GrpoArgs* grpo,
+                                         const TopkCall* topk = nullptr) {
   if (!sizes_ok(N, H, V)) return FLCE_ERR_INVALID_ARG;
   GemmParams tfp{};
   if (!transform_params(transform, tfp)) return FLCE_ERR_INVALID_ARG;
@@ -539,6 +564,14 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
     uint8_t* wb = static_cast<uint8_t*>(ws.ptr);
     float* lse = out_lse ? out_lse : reinterpret_cast<float*>(wb + FL.lse);
     int64_t* nv = out_n_valid ? out_n_valid : reinterpret_cast<int64_t*>(wb + FL.nv);
+    if (topk) {
+      s = forward_impl(h, W, targets, nullptr, N, H, V, ignore_index, transform, nullptr, nullptr, out_loss, nv, wb,
+                       FL.inner, stream, kFwdPartialsCap, false, topk);
+      if (s != FLCE_OK) return s;
+      return backward_impl(h, W, targets, topk->rows.coef, topk->rows.lse_rest, grad_scale, dH, dW, N, H, V,
+                           chunk_rows, ignore_index, transform, wb, FL.inner, stream,
+                           reinterpret_cast<const long long*>(nv), nullptr, topk);
+    }
     if (grpo == nullptr) {
       s = forward_impl(h, W, targets, weights, N, H, V, ignore_index, transform, out_logp, lse, out_loss, nv,
                        wb, FL.inner, stream, kFwdPartialsCap);
@@ -597,9 +630,10 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
   // GRPO: the block's log-probs feed its token losses and backward weights
   float* lp = out_logp ? out_logp : (grpo ? reinterpret_cast<float*>(wb + L.lp) : nullptr);
   float* wg = reinterpret_cast<float*>(wb + L.wg);
-  const float* dl_weights = grpo ? wg : weights;
+  const float* dl_weights = topk ? topk->rows.coef : grpo ? wg : weights;
+  const float* dl_lse = topk ? topk->rows.lse_rest : lse;
   const int Ni = static_cast<int>(N);
-  const bool validate = validate_on();
+  const bool validate = validate_on() && !topk;  // a list's marks are no targets
   // Row compaction: the blocks run over a permutation of the rows with the
   // non-ignored ones first.  A block's forward covers all its rows when the
   // caller asks for lse (defined for ignored rows too), else only the
@@ -607,10 +641,10 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
   // only the non-ignored rows.
   // (one row tile gains nothing from compaction: see backward_impl)
   const bool compact = compact_on() && N > tm;
-  const bool fwd_valid_only = compact && out_lse == nullptr;
+  const bool fwd_valid_only = compact && out_lse == nullptr && !(topk && topk->out_lse);
 
   if (validate) FLCE_CUDA_TRY(cudaMemsetAsync(bad, 0, sizeof(int), st));
-  {
+  if (!topk) {
     ProfScope ps(K_PREP, st);
     prep_kernel<<<static_cast<int>(ceil_div(N, SMALL_THREADS)), SMALL_THREADS, 0, st>>>(
         targets, Ni, static_cast<int>(V), ignore_index, zt, validate ? bad : nullptr);
@@ -671,9 +705,18 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
   base.tf_a = tfp.tf_a;
   base.tf_b = tfp.tf_b;
   base.tf_d = tfp.tf_d;
+  if (topk) {
+    base.grad_scale = grad_scale;
+    base.sp_ids = topk->rows.ids;
+    base.sp_val = topk->rows.val;
+    base.sp_k = topk->K;
+    bsum = topk->bsum;
+    bcnt = topk->bcnt;
+  }
   const DhDwStage dhdw{cg, workers, tm, kLong, &fp.b, H, V, dh_part, dH, dW, &W_mn, &dW_map, &dhp_map};
+  // loss block sums: a segment per row block
+  const long long per = ceil_div(fp.R, topk ? TOPK_ROWS : SMALL_THREADS);
   {  // the last block's segment may be shorter than the others: zero it whole
-    const long long per = ceil_div(fp.R, SMALL_THREADS);
     const long long last = (ceil_div(N, fp.R) - 1) * per;
     FLCE_CUDA_TRY(cudaMemsetAsync(bsum + last, 0, per * 8, st));
     FLCE_CUDA_TRY(cudaMemsetAsync(bcnt + last, 0, per * 8, st));
@@ -708,13 +751,19 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
       // (their partials stay unwritten; the combine gives them logp 0)
       if (fwd_valid_only) q.dyn_count = ccount;
       ProfScope ps(K_FWD, st);
-      FLCE_CUDA_TRY(launch_gemm<MODE_FUSED_FWD>(cg, kLong, compact ? hc_k : h_k, W_k, W_k, q,
-                                                std::min(q.num_units, workers), st));
+      const CUtensorMap& A = compact ? hc_k : h_k;
+      const int nw = std::min(q.num_units, workers);
+      FLCE_CUDA_TRY(topk ? launch_fwd_listed<MODE_FUSED_FWD>(cg, kLong, A, W_k, q, nw, st)
+                         : launch_gemm<MODE_FUSED_FWD>(cg, kLong, A, W_k, W_k, q, nw, st));
     }
-    {  // (2) the block's lse, logp and loss partials
+    if (topk) {  // (2) the block's lse, kl, loss partials and dlogits coefficients
+      s = topk_rows(*topk, kLong, fp.f, p, Ni, static_cast<int>(row0), rows, compact ? cidx + row0 : nullptr, part,
+                    fwd_valid_only, block * per, st);
+      if (s != FLCE_OK) return s;
+    } else {  // (2) the block's lse, logp and loss partials
       ProfScope ps(K_COMBINE, st);
       const int nb = static_cast<int>(ceil_div(rows, SMALL_THREADS));
-      const long long b0 = block * ceil_div(fp.R, SMALL_THREADS);  // this block's segment
+      const long long b0 = block * per;  // this block's segment
       // the block's rows: row0 + j, or cidx[row0 + j] (arrays not offset)
       const long long off = compact ? 0 : row0;
       const int* ri = compact ? cidx + row0 : nullptr;
@@ -747,12 +796,18 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
       if (kLong)
         fused_dlogits_kernel<true><<<grid, SMALL_THREADS, 0, st>>>(
             E, mx, static_cast<int>(fp.ldD), static_cast<int>(V), static_cast<int>(row0), ri, targets,
-            dl_weights, lse, zt, ignore_index, ccount, grad_scale, tfp.tf_softcap, tfp.tf_a, tfp.tf_b, tfp.tf_d);
+            dl_weights, dl_lse, zt, ignore_index, ccount, grad_scale, tfp.tf_softcap, tfp.tf_a, tfp.tf_b, tfp.tf_d);
       else
         fused_dlogits_kernel<false><<<grid, SMALL_THREADS, 0, st>>>(
             E, mx, static_cast<int>(fp.ldD), static_cast<int>(V), static_cast<int>(row0), ri, targets,
-            dl_weights, lse, zt, ignore_index, ccount, grad_scale, tfp.tf_softcap, tfp.tf_a, tfp.tf_b, tfp.tf_d);
+            dl_weights, dl_lse, zt, ignore_index, ccount, grad_scale, tfp.tf_softcap, tfp.tf_a, tfp.tf_b, tfp.tf_d);
       FLCE_CUDA_TRY(cudaGetLastError());
+    }
+    if (topk) {
+      s = topk_scatter(*topk, kLong, p, E, 0, static_cast<int>(V), static_cast<int>(row0), rows,
+                       compact ? cidx : nullptr, compact ? ccount : nullptr, static_cast<int>(row0), nullptr, ccount,
+                       st);
+      if (s != FLCE_OK) return s;
     }
     // (4) dH[rows] = D W, dW (+)= D^T h[rows]; compacted: the block's
     // non-ignored rows, min(n_valid - row0, rows) read on the device
@@ -766,16 +821,9 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
                         static_cast<int>(row0), st);
     if (s != FLCE_OK) return s;
   }
-  if (out_loss || out_n_valid) {
-    ProfScope ps(K_FINAL, st);
-    // every segment entry was written: full blocks fill theirs, and the last
-    // block's unused entries were zeroed before the loop
-    final_kernel<<<1, SMALL_THREADS, 0, st>>>(bsum, bcnt,
-                                              static_cast<int>(ceil_div(N, fp.R) * ceil_div(fp.R, SMALL_THREADS)),
-                                              out_loss, reinterpret_cast<long long*>(out_n_valid));
-    FLCE_CUDA_TRY(cudaGetLastError());
-  }
-  return FLCE_OK;
+  // every segment entry was written: full blocks fill theirs, and the last
+  // block's unused entries were zeroed before the loop
+  return loss_sums(out_loss, out_n_valid, bsum, bcnt, ceil_div(N, fp.R) * per, st);
 }
 
 flce_status flce_forward_backward(const flce_bf16* h, const flce_bf16* W, const int64_t* targets,
@@ -1680,3 +1728,5 @@ extern "C" flce_status flce_forward_static_scratch(const flce_bf16* h, const flc
   return forward_impl(h, W, targets, weights, N, H, V, ignore_index, nullptr, out_logp, out_lse,
                       out_loss, out_n_valid, scratch, kStaticScratchBytes, stream, cap);
 }
+
+#include "topk_api.cuh"

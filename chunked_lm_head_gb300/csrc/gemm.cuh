@@ -36,6 +36,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <climits>
 #include <cstdint>
 #include <type_traits>
 
@@ -259,6 +260,12 @@ struct GemmParams {
   int pp_slabs, pp_vs, pp_kh, pp_dh_kbps, pp_dl_group, pp_dep_words, pp_lookahead;
   unsigned* pp_dep;
   unsigned* pp_dep_zero;
+  // listed columns (the kernel's kSp): each row's sp_k ids in ascending order
+  // ([N][sp_k], INT_MAX past the last); the forward writes their transformed
+  // logits to sp_val [N][sp_k] and leaves them out of its log-sum-exp
+  const int* sp_ids;
+  float* sp_val;
+  int sp_k;
 };
 
 // grad_scale of the dlogits modes with its device-side factors: / max(count, 1)
@@ -766,7 +773,20 @@ __device__ __forceinline__ void stage_bf16_half(uint32_t box, int lane, int half
                      pk[4 * g + 2], pk[4 * g + 3]);
 }
 
-template <int MODE, bool kLong, int CG, bool kF8 = false, int EW = EPI_WARPS>
+// First position of a row's ascending list (k ids) whose id is >= v.
+__device__ __forceinline__ int list_lower_bound(const int* ids, int k, int v) {
+  int lo = 0, hi = k;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ids[mid] < v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+template <int MODE, bool kLong, int CG, bool kF8 = false, int EW = EPI_WARPS, bool kSp = false>
 __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
     flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmA2,
@@ -1123,6 +1143,17 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
         }
       }
       const float scale_a = scale * lin_a;
+      // listed columns: this row's list from the unit's first column on
+      static_assert(!kSp || MODE == MODE_FWD || MODE == MODE_FUSED_FWD, "listed columns: the forwards");
+      const int* sp_row = nullptr;
+      int sp_at = 0, sp_next = INT_MAX;
+      if constexpr (kSp) {
+        if (row_ok) {
+          sp_row = p.sp_ids + static_cast<long long>(grow) * p.sp_k;
+          sp_at = list_lower_bound(sp_row, p.sp_k, t.n0 * BN);
+          sp_next = sp_at < p.sp_k ? sp_row[sp_at] : INT_MAX;
+        }
+      }
       for (int n = t.n0; n < t.n1; ++n) {
         int got = 0;
         if (lane == 0) got = wait_bar(tfull_bar(acc), acc_phase, abort_flag, p.err) ? 1 : 0;
@@ -1170,6 +1201,26 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
               for (int j = 0; j < 32; ++j)
                 if (col0 + j >= p.V) v[j] = -INFINITY;
             }
+            if constexpr (kSp) {
+              // the chunk's listed columns: their logits kept, the columns
+              // left out of the sum (and of the stored exponentials).  A row
+              // of 64 ids meets one chunk in 75 of 151,936 columns, so most
+              // warps pass with one vote
+              if (__any_sync(0xffffffffu, sp_next < col0 + 32)) {
+                uint32_t listed = 0u;
+                while (sp_next < col0 + 32) {
+                  const int j = sp_next - col0;
+                  p.sp_val[static_cast<long long>(grow) * p.sp_k + sp_at] = select32(v, j) * lin_a;
+                  listed |= 1u << j;
+                  ++sp_at;
+                  sp_next = sp_at < p.sp_k ? sp_row[sp_at] : INT_MAX;
+                }
+                __syncwarp();  // the next accumulator load is the whole warp's
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if ((listed >> j) & 1u) v[j] = -INFINITY;
+              }
+            }
             float cm = v[0];
 #pragma unroll
             for (int j = 1; j < 32; ++j) cm = fmaxf(cm, v[j]);
@@ -1203,10 +1254,12 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                 if (col0 < p.ldD) p.mx[static_cast<idx_t>(lr) * (p.ldD / 32) + col0 / 32] = cmL;
               }
             }
-            const long long tj = tgt - col0;
-            if (tj >= 0 && tj < 32 && tgt < p.V) {
-              const float z = select32(v, static_cast<int>(tj)) * lin_a;
-              if (row_ok) p.zt[grow] = z;
+            if constexpr (!kSp) {
+              const long long tj = tgt - col0;
+              if (tj >= 0 && tj < 32 && tgt < p.V) {
+                const float z = select32(v, static_cast<int>(tj)) * lin_a;
+                if (row_ok) p.zt[grow] = z;
+              }
             }
           } else if (unit_dl) {
             uint32_t pk[16];

@@ -12,6 +12,7 @@
 
 #include "flce.h"
 #include "plan.cuh"
+#include "topk.cuh"
 
 namespace {
 
@@ -208,6 +209,24 @@ cudaError_t launch_fwd_e4m3(int cg, bool kLong, const CUtensorMap& a, const CUte
                : go(flce_gemm_kernel<MODE_FWD, false, 1, true>, TileCfg<1>::SMEM, 1);
 }
 
+// A forward over rows with listed columns (the distillation from a teacher's
+// top logits): MODE_FWD or MODE_FUSED_FWD.
+template <int MODE>
+cudaError_t launch_fwd_listed(int cg, bool kLong, const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
+                              int workers, cudaStream_t st) {
+  auto go = [&](auto kern, int smem, int grid_mult) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_persistent(kern, grid_mult * grid_workers(workers), grid_mult, gemm_threads(EPI_WARPS), smem, st,
+                             a, b, b, a, b, b, a, b, b, p);
+  };
+  if (cg == 2)
+    return kLong ? go(flce_gemm_kernel<MODE, true, 2, false, EPI_WARPS, true>, TileCfg<2>::SMEM, 2)
+                 : go(flce_gemm_kernel<MODE, false, 2, false, EPI_WARPS, true>, TileCfg<2>::SMEM, 2);
+  return kLong ? go(flce_gemm_kernel<MODE, true, 1, false, EPI_WARPS, true>, TileCfg<1>::SMEM, 1)
+               : go(flce_gemm_kernel<MODE, false, 1, false, EPI_WARPS, true>, TileCfg<1>::SMEM, 1);
+}
+
 // CTA group of the GEMMs: 2 (SM pairs, 256-row tiles) unless
 // FLCE_OPT_CTA_GROUP = 1.
 int cta_group() { return opt(FLCE_OPT_CTA_GROUP) == 1 ? 1 : 2; }
@@ -360,15 +379,19 @@ flce_status gather_rows(const flce_bf16* h, long long H, const int* idx, const i
 }
 
 // Final deterministic reduction of the block partials into loss and count.
-flce_status loss_tail(const FwdPlan& f, float* out_loss, int64_t* out_n_valid, const double* bsum,
-                      const long long* bcnt, cudaStream_t st) {
+flce_status loss_sums(float* out_loss, int64_t* out_n_valid, const double* bsum, const long long* bcnt,
+                      long long nblk, cudaStream_t st) {
   if (out_loss || out_n_valid) {
     ProfScope ps(K_FINAL, st);
-    final_kernel<<<1, SMALL_THREADS, 0, st>>>(bsum, bcnt, f.nblk, out_loss,
+    final_kernel<<<1, SMALL_THREADS, 0, st>>>(bsum, bcnt, static_cast<int>(nblk), out_loss,
                                               reinterpret_cast<long long*>(out_n_valid));
     FLCE_CUDA_TRY(cudaGetLastError());
   }
   return FLCE_OK;
+}
+flce_status loss_tail(const FwdPlan& f, float* out_loss, int64_t* out_n_valid, const double* bsum,
+                      const long long* bcnt, cudaStream_t st) {
+  return loss_sums(out_loss, out_n_valid, bsum, bcnt, f.nblk, st);
 }
 
 // ---- stages shared by the entry points
@@ -530,6 +553,59 @@ flce_status ce_forward_tail(bool kLong, const FwdPlan& f, int N, const float2* p
     FLCE_CUDA_TRY(cudaGetLastError());
   }
   return loss_tail(f, out_loss, out_n_valid, bsum, bcnt, st);
+}
+
+// ---- distillation from a teacher's top logits: what its calls add to the
+// forward, the one-call step and the tiled backward, whose targets are then
+// rows.mark (a counted row's lies past the vocabulary: no one-hot column),
+// with ignore index -1
+constexpr long long kMarkIgnored = -1;
+struct TopkCall {
+  TopkRows rows;
+  int K = 0, tail = 0;
+  const float* weights = nullptr;
+  float* out_kl = nullptr;
+  float* out_lse = nullptr;
+  double* bsum = nullptr;  // block sums of the row kernel
+  long long* bcnt = nullptr;
+};
+
+// The row kernel over `rows` rows (row0 + j, or ri[j]); its block sums at
+// bsum / bcnt + block0.
+flce_status topk_rows(const TopkCall& c, bool kLong, const FwdPlan& f, const GemmParams& p, int N, int row0, int rows,
+                      const int* ri, const float2* part, bool skipped, long long block0, cudaStream_t st) {
+  ProfScope ps(K_TOPK, st);
+  const unsigned grid = static_cast<unsigned>(ceil_div(rows, TOPK_ROWS));
+  auto go = [&](auto kern) {
+    kern<<<grid, SMALL_THREADS, 0, st>>>(part, f.S, N, row0, rows, ri, c.K, c.tail, c.weights, c.rows, p.tf_softcap,
+                                         p.tf_a, p.tf_b, p.tf_d, skipped ? 1 : 0, c.out_kl, c.out_lse,
+                                         c.bsum + block0, c.bcnt + block0);
+  };
+  if (kLong)
+    go(topk_row_kernel<true>);
+  else
+    go(topk_row_kernel<false>);
+  FLCE_CUDA_TRY(cudaGetLastError());
+  return FLCE_OK;
+}
+
+// The listed columns of the dlogits block D (local columns of slab v0).
+flce_status topk_scatter(const TopkCall& c, bool kLong, const GemmParams& p, uint16_t* D, int v0, int width, int row0,
+                         int rows, const int* ri, const int* dyn_count, int first, const long long* count,
+                         const int* count32, cudaStream_t st) {
+  ProfScope ps(K_TOPK, st);
+  const unsigned grid = static_cast<unsigned>(std::max<long long>(
+      1, std::min<long long>(ceil_div(static_cast<long long>(rows) * c.K, SMALL_THREADS), 8LL * device_sms())));
+  auto go = [&](auto kern) {
+    kern<<<grid, SMALL_THREADS, 0, st>>>(D, p.ldD, v0, width, row0, rows, ri, dyn_count, first, c.K, c.rows.ids,
+                                         c.rows.val, p.grad_scale, count, count32, p.scale_dev);
+  };
+  if (kLong)
+    go(topk_scatter_kernel<true>);
+  else
+    go(topk_scatter_kernel<false>);
+  FLCE_CUDA_TRY(cudaGetLastError());
+  return FLCE_OK;
 }
 
 }  // namespace

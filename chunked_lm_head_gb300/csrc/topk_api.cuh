@@ -1,0 +1,203 @@
+// libflce host side: the entry points of the distillation from a teacher's
+// top logits (row kernels in topk.cuh; the forward, the one-call step and the
+// tiled backward are those of the cross-entropy, in flce.cu, with the listed
+// columns taken apart).
+#pragma once
+
+namespace {
+
+bool topk_teacher_ok(const flce_top_logits* t) {
+  if (t == nullptr || t->k < 1) return false;
+  if (t->ids_type != FLCE_I32 && t->ids_type != FLCE_I64) return false;
+  if (t->logits_type != FLCE_F32 && t->logits_type != FLCE_BF16 && t->logits_type != FLCE_F16) return false;
+  if (t->tail != 0 && t->tail != 1) return false;
+  return !(t->tail && t->lse == nullptr);  // the mass outside the list needs the teacher's whole sum
+}
+
+// The call's row arrays and block sums.  The first five are the state that
+// the backward reads, laid out alike in a caller's state buffer.
+struct TopkLayout {
+  size_t ids = 0, val = 0, mark = 0, lse_rest = 0, coef = 0, state = 0;
+  size_t mass = 0, stat = 0, bsum = 0, bcnt = 0, nv = 0, total = 0;
+};
+TopkLayout topk_layout(int64_t N, int64_t K) {
+  TopkLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  const size_t n = static_cast<size_t>(std::max<int64_t>(N, 1)), nk = n * static_cast<size_t>(K);
+  L.ids = take(nk * 4);
+  L.val = take(nk * 4);
+  L.mark = take(n * 8);
+  L.lse_rest = take(n * 4);
+  L.coef = take(n * 4);
+  L.state = o;
+  L.mass = take(nk * 4);
+  L.stat = take(n * 16);
+  // one-call: ceil(N / R) segments of R / TOPK_ROWS block sums, R a multiple of
+  // 128 and at most N rounded up to one
+  const size_t blocks = (2 * n + 256) / TOPK_ROWS + 1;
+  L.bsum = take(blocks * 8);
+  L.bcnt = take(blocks * 8);
+  L.nv = take(8);
+  L.total = o;
+  return L;
+}
+
+TopkRows topk_rows_at(const TopkLayout& L, uint8_t* state, uint8_t* scratch) {
+  TopkRows r{};
+  r.ids = reinterpret_cast<int*>(state + L.ids);
+  r.val = reinterpret_cast<float*>(state + L.val);
+  r.mark = reinterpret_cast<long long*>(state + L.mark);
+  r.lse_rest = reinterpret_cast<float*>(state + L.lse_rest);
+  r.coef = reinterpret_cast<float*>(state + L.coef);
+  r.mass = reinterpret_cast<float*>(scratch + L.mass);
+  r.stat = reinterpret_cast<double2*>(scratch + L.stat);
+  return r;
+}
+
+// The checks of a call that takes a teacher.
+flce_status topk_check(const flce_top_logits* t, const int64_t* targets, const float* weights, int64_t N, int64_t H,
+                       int64_t V) {
+  if (!sizes_ok(N, H, V) || !topk_teacher_ok(t)) return FLCE_ERR_INVALID_ARG;
+  if (N > 0 && (!t->ids || !t->logits || t->ld_ids < t->k || t->ld_logits < t->k)) return FLCE_ERR_INVALID_ARG;
+  if (t->k > TOPK_MAX_K) return FLCE_ERR_UNSUPPORTED;
+  if (!aligned(t->ids, t->ids_type == FLCE_I64 ? 8 : 4) || !aligned(t->logits, t->logits_type == FLCE_F32 ? 4 : 2) ||
+      !aligned(t->lse, 4) || !aligned(targets, 8) || !aligned(weights, 4))
+    return FLCE_ERR_UNSUPPORTED;
+  return FLCE_OK;
+}
+
+flce_status topk_lists(const flce_top_logits* t, const int64_t* targets, int64_t ignore_index, int64_t N, int64_t V,
+                       const TopkRows& rows, cudaStream_t st) {
+  if (N == 0) return FLCE_OK;
+  const TopkTeacher d{t->ids,     t->logits,   t->lse,         t->ld_ids, t->ld_logits,
+                      t->ids_type, t->logits_type, t->k, t->tail};
+  ProfScope ps(K_TOPK, st);
+  topk_list_kernel<<<static_cast<unsigned>(ceil_div(N, TOPK_WARPS)), 32 * TOPK_WARPS,
+                     static_cast<size_t>(TOPK_WARPS) * 2 * t->k * 4, st>>>(
+      d, targets, ignore_index, static_cast<int>(N), static_cast<int>(V), rows);
+  FLCE_CUDA_TRY(cudaGetLastError());
+  return FLCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t flce_topk_kd_state_bytes(int64_t N, int64_t k) {
+  if (N < 0 || N >= INT_MAX || k < 1 || k > TOPK_MAX_K) return 0;
+  return topk_layout(N, k).state;
+}
+
+size_t flce_topk_kd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k, int64_t chunk_rows) {
+  if (!sizes_ok(N, H, V) || k < 1 || k > TOPK_MAX_K) return 0;
+  return align256(flce_workspace_bytes(N, H, V, chunk_rows)) + topk_layout(N, k).total;
+}
+
+size_t flce_topk_kd_forward_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k,
+                                                     int64_t chunk_rows) {
+  if (!sizes_ok(N, H, V) || k < 1 || k > TOPK_MAX_K) return 0;
+  return align256(flce_forward_backward_workspace_bytes(N, H, V, chunk_rows)) + topk_layout(N, k).total;
+}
+
+flce_status flce_topk_kd_forward(const flce_bf16* h, const flce_bf16* W, const flce_top_logits* teacher,
+                                 const int64_t* targets, const float* weights, int64_t N, int64_t H, int64_t V,
+                                 int64_t chunk_rows, int64_t ignore_index, const flce_logit_transform* transform,
+                                 uint32_t flags, float* out_kl, float* out_lse, float* out_loss,
+                                 int64_t* out_n_valid, void* state, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  if ((flags & ~static_cast<uint32_t>(FLCE_FORWARD_SKIP_IGNORED)) != 0) return FLCE_ERR_INVALID_ARG;
+  if (!out_kl && !out_lse && !out_loss && !out_n_valid && !state) return FLCE_ERR_INVALID_ARG;
+  flce_status s = topk_check(teacher, targets, weights, N, H, V);
+  if (s != FLCE_OK) return s;
+  if (N > 0 && (!h || !W)) return FLCE_ERR_INVALID_ARG;
+  if (!aligned(out_kl, 4) || !aligned(out_lse, 4) || !aligned(state, 256)) return FLCE_ERR_UNSUPPORTED;
+  const TopkLayout L = topk_layout(N, teacher->k);
+  const size_t inner = align256(flce_workspace_bytes(N, H, V, chunk_rows));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  GemmParams tfp{};
+  if (!transform_params(transform, tfp)) return FLCE_ERR_INVALID_ARG;
+  if (H % 8 != 0 || !aligned(h, 16) || !aligned(W, 16) || !aligned(out_loss, 4) || !aligned(out_n_valid, 8))
+    return FLCE_ERR_UNSUPPORTED;
+  Workspace ws;
+  s = get_workspace(ws, workspace, workspace_bytes, inner + L.total, st);
+  if (s != FLCE_OK) return s;
+  uint8_t* wb = static_cast<uint8_t*>(ws.ptr);
+  TopkCall c;
+  c.rows = topk_rows_at(L, state ? static_cast<uint8_t*>(state) : wb + inner, wb + inner);
+  c.K = teacher->k;
+  c.tail = teacher->tail;
+  c.weights = weights;
+  c.out_kl = out_kl;
+  c.out_lse = out_lse;
+  c.bsum = reinterpret_cast<double*>(wb + inner + L.bsum);
+  c.bcnt = reinterpret_cast<long long*>(wb + inner + L.bcnt);
+  s = topk_lists(teacher, targets, ignore_index, N, V, c.rows, st);
+  if (s != FLCE_OK) return s;
+  const bool skip = (flags & FLCE_FORWARD_SKIP_IGNORED) != 0 && compact_on() && N >= skip_min_rows();
+  return forward_impl(h, W, reinterpret_cast<const int64_t*>(c.rows.mark), nullptr, N, H, V, kMarkIgnored, transform,
+                      nullptr, nullptr, out_loss, out_n_valid, wb, inner, stream, kFwdPartialsCap, skip, &c);
+}
+
+flce_status flce_topk_kd_backward(const flce_bf16* h, const flce_bf16* W, const void* state, float grad_scale,
+                                  const flce_device_scale* device_scale, flce_bf16* dH, float* dW, int64_t N,
+                                  int64_t H, int64_t V, int64_t k, int64_t chunk_rows,
+                                  const flce_logit_transform* transform, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  if (!sizes_ok(N, H, V) || k < 1 || (N > 0 && !state)) return FLCE_ERR_INVALID_ARG;
+  if (k > TOPK_MAX_K || !aligned(state, 256)) return FLCE_ERR_UNSUPPORTED;
+  const TopkLayout L = topk_layout(N, k);
+  TopkCall c;
+  // read only by the tiled backward
+  uint8_t* sb = static_cast<uint8_t*>(const_cast<void*>(state));
+  c.rows = topk_rows_at(L, sb, sb);
+  c.K = static_cast<int>(k);
+  const long long* count = device_scale ? reinterpret_cast<const long long*>(device_scale->count) : nullptr;
+  const float* scale = device_scale ? device_scale->scale : nullptr;
+  return backward_impl(h, W, reinterpret_cast<const int64_t*>(c.rows.mark), c.rows.coef, c.rows.lse_rest, grad_scale,
+                       dH, dW, N, H, V, chunk_rows, kMarkIgnored, transform, workspace, workspace_bytes, stream, count,
+                       scale, &c);
+}
+
+flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W, const flce_top_logits* teacher,
+                                          const int64_t* targets, const float* weights, int64_t N, int64_t H,
+                                          int64_t V, int64_t chunk_rows, int64_t ignore_index,
+                                          const flce_logit_transform* transform, float grad_scale, float* out_kl,
+                                          float* out_lse, float* out_loss, int64_t* out_n_valid, flce_bf16* dH,
+                                          float* dW, void* workspace, size_t workspace_bytes, void* stream) {
+  flce_status s = topk_check(teacher, targets, weights, N, H, V);
+  if (s != FLCE_OK) return s;
+  GemmParams tfp{};
+  if (!transform_params(transform, tfp) || !std::isfinite(grad_scale)) return FLCE_ERR_INVALID_ARG;
+  if ((!dH && !dW) || (N > 0 && (!h || !W))) return FLCE_ERR_INVALID_ARG;
+  if (H % 8 != 0 || !aligned(h, 16) || !aligned(W, 16) || !aligned(dH, 16) || !aligned(dW, 16) ||
+      !aligned(out_kl, 4) || !aligned(out_lse, 4) || !aligned(out_loss, 4) || !aligned(out_n_valid, 8))
+    return FLCE_ERR_UNSUPPORTED;
+  const TopkLayout L = topk_layout(N, teacher->k);
+  const size_t inner = align256(flce_forward_backward_workspace_bytes(N, H, V, chunk_rows));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Workspace ws;
+  s = get_workspace(ws, workspace, workspace_bytes, inner + L.total, st);
+  if (s != FLCE_OK) return s;
+  uint8_t* wb = static_cast<uint8_t*>(ws.ptr);
+  TopkCall c;
+  c.rows = topk_rows_at(L, wb + inner, wb + inner);
+  c.K = teacher->k;
+  c.tail = teacher->tail;
+  c.weights = weights;
+  c.out_kl = out_kl;
+  c.out_lse = out_lse;
+  c.bsum = reinterpret_cast<double*>(wb + inner + L.bsum);
+  c.bcnt = reinterpret_cast<long long*>(wb + inner + L.bcnt);
+  s = topk_lists(teacher, targets, ignore_index, N, V, c.rows, st);
+  if (s != FLCE_OK) return s;
+  return forward_backward_impl(h, W, reinterpret_cast<const int64_t*>(c.rows.mark), nullptr, N, H, V, chunk_rows,
+                               kMarkIgnored, transform, grad_scale, nullptr, nullptr, out_loss, out_n_valid, dH, dW,
+                               wb, inner, stream, nullptr, &c);
+}
+
+}  // extern "C"

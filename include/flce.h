@@ -440,6 +440,102 @@ FLCE_API flce_status flce_jsd_backward_ex2(const flce_bf16* h_s, const flce_bf16
                                            size_t workspace_bytes, void* stream);
 
 /*
+ * Distillation from a teacher's stored top logits: the teacher's head does
+ * not run, its best k logits per token were kept (an addition of this
+ * library; the pages' distillation runs both heads).  Per row i, with u the
+ * student's transformed logits, S the row's distinct listed ids and
+ *   p_k  = exp(t_k - lse_t), entries of the same id added up,
+ *   P    = sum_k p_k,  T = max(0, 1 - P) with tail (else 0),
+ *   R    = sum_{v not in S} softmax(u)_v,
+ *   kl   = m (sum_k p_k (log p_k - log softmax(u)_k) + T (log T - log R)),
+ *   loss = sum_i m w kl / sum_i m,
+ * with 0 log 0 = 0, and no tail term where the list holds the whole
+ * vocabulary.  m is 0 where targets[i] == ignore_index (targets NULL: nowhere)
+ * and where the list is empty.
+ *   ids     [N, ld_ids] int32 or int64 (ids_type); a negative id is no entry
+ *           (lists of unequal length), the order is free.  An id >= V makes
+ *           the row's kl, and the loss, NaN; it takes part in no gradient and
+ *           nothing is read out of bounds.
+ *   logits  [N, ld_logits] fp32, bf16 or fp16 (logits_type): the teacher's
+ *           logits after its own transform and temperature, or log-probs.
+ *   lse     [N] fp32, the log-sum-exp of the teacher's whole row (0 for
+ *           log-probs), or NULL: the list's mass is scaled to one.
+ *   k       1..1,024 entries per row (ld_ids, ld_logits >= k).
+ *   tail    1: the mass outside the list is one more outcome, for teacher and
+ *           student alike (needs lse); 0: it takes no part.
+ */
+typedef struct flce_top_logits {
+  const void* ids;
+  const void* logits;
+  const float* lse;
+  int64_t ld_ids, ld_logits;
+  int32_t ids_type, logits_type;
+  int32_t k;
+  int32_t tail;
+} flce_top_logits;
+
+/*
+ * The loss.  Outputs (each may be NULL, not all): out_kl [N] (0 on rows
+ * without loss), out_lse [N] fp32 of every row (with FLCE_FORWARD_SKIP_IGNORED
+ * NaN on rows without loss, which the GEMM then skips as in
+ * flce_forward_ex2), out_loss, out_n_valid; and state, what
+ * flce_topk_kd_backward reads (flce_topk_kd_state_bytes, 256-byte aligned), or
+ * NULL.  No N x V array is stored: the GEMM's epilogue keeps the listed
+ * columns' logits and leaves them out of its online sum.  Workspace:
+ * flce_topk_kd_workspace_bytes, or NULL.  Other arguments as flce_forward_ex2.
+ */
+FLCE_API flce_status flce_topk_kd_forward(const flce_bf16* h, const flce_bf16* W,
+                                          const flce_top_logits* teacher, const int64_t* targets,
+                                          const float* weights, int64_t N, int64_t H, int64_t V,
+                                          int64_t chunk_rows, int64_t ignore_index,
+                                          const flce_logit_transform* transform, uint32_t flags,
+                                          float* out_kl, float* out_lse, float* out_loss,
+                                          int64_t* out_n_valid, void* state, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, the logits recomputed chunk by chunk:
+ *   D_v = m w g f'(z) ((P + T) softmax(u)_v - p_v)                   v in S
+ *       = m w g f'(z) ((P + T) R - T) softmax(u)_v / R               v not in S
+ *   dH = D W, dW = D^T h,  g = grad_scale * (*scale) / max(*count, 1)
+ * (device_scale as flce_backward_ex2, or NULL).  Same h, W, k and transform
+ * as the forward that wrote state.  chunk_rows, dH and dW as flce_backward;
+ * workspace flce_topk_kd_workspace_bytes, or NULL.
+ */
+FLCE_API flce_status flce_topk_kd_backward(const flce_bf16* h, const flce_bf16* W, const void* state,
+                                           float grad_scale, const flce_device_scale* device_scale,
+                                           flce_bf16* dH, float* dW, int64_t N, int64_t H, int64_t V,
+                                           int64_t k, int64_t chunk_rows,
+                                           const flce_logit_transform* transform, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/*
+ * Loss and gradients in one call without the logits recompute (blocks,
+ * budget and fallback as flce_forward_backward):
+ *   dH, dW = grad_scale * d(loss) / d(h, W).
+ * Workspace: flce_topk_kd_forward_backward_workspace_bytes, or NULL.
+ */
+FLCE_API flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W,
+                                                   const flce_top_logits* teacher,
+                                                   const int64_t* targets, const float* weights,
+                                                   int64_t N, int64_t H, int64_t V, int64_t chunk_rows,
+                                                   int64_t ignore_index,
+                                                   const flce_logit_transform* transform,
+                                                   float grad_scale, float* out_kl, float* out_lse,
+                                                   float* out_loss, int64_t* out_n_valid,
+                                                   flce_bf16* dH, float* dW, void* workspace,
+                                                   size_t workspace_bytes, void* stream);
+
+/* Bytes of flce_topk_kd_forward's state; of the workspace of
+ * flce_topk_kd_forward and flce_topk_kd_backward; and of
+ * flce_topk_kd_forward_backward's (0 on invalid sizes). */
+FLCE_API size_t flce_topk_kd_state_bytes(int64_t N, int64_t k);
+FLCE_API size_t flce_topk_kd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k,
+                                             int64_t chunk_rows);
+FLCE_API size_t flce_topk_kd_forward_backward_workspace_bytes(int64_t N, int64_t H, int64_t V,
+                                                              int64_t k, int64_t chunk_rows);
+
+/*
  * GRPO per-token objective on the sampled tokens' log-probs.  Source: TRL
  * v1.13 article, section "Other changes in v1.13": a fused linear GRPO loss is
  * among TRL's fused losses; the page gives no formula.  Reading taken (the
