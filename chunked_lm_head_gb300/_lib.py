@@ -96,15 +96,18 @@ SIGNATURES = {
     "flce_topk_kd_forward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64,
                                             _c_i64, _c_vp, ctypes.c_uint32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
                                             _c_vp, ctypes.c_size_t, _c_vp]),
-    "flce_topk_kd_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_i64,
-                                             _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, ctypes.c_size_t,
-                                             _c_vp]),
+    "flce_topk_kd_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, ctypes.c_float, _c_vp, _c_vp, _c_vp,
+                                             ctypes.c_int32, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp,
+                                             ctypes.c_size_t, _c_vp]),
+    "flce_topk_kd_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int32]),
     "flce_topk_kd_forward_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64,
                                                      _c_i64, _c_i64, _c_vp, ctypes.c_float, _c_vp, _c_vp, _c_vp,
-                                                     _c_vp, _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
+                                                     _c_vp, _c_vp, _c_vp, ctypes.c_int32, _c_vp, ctypes.c_size_t,
+                                                     _c_vp]),
     "flce_topk_kd_state_bytes": (ctypes.c_size_t, [_c_i64, _c_i64]),
     "flce_topk_kd_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64]),
-    "flce_topk_kd_forward_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64]),
+    "flce_topk_kd_forward_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
+                                                                        ctypes.c_int32]),
     "flce_rms_norm": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, ctypes.c_int32, _c_vp, ctypes.c_int32,
                                      ctypes.c_float, ctypes.c_float, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp,
                                      _c_vp]),
@@ -466,26 +469,27 @@ def flce_topk_kd_forward(h, W, teacher, targets, weights, N, H, V, chunk_rows, i
                                     workspace_bytes, _stream_handle(stream))
 
 
-def flce_topk_kd_backward(h, W, state, grad_scale, scale, count, dH, dW, N, H, V, k, chunk_rows, transform,
+def flce_topk_kd_backward(h, W, state, grad_scale, scale, count, dH, dW, dW_type, N, H, V, k, chunk_rows, transform,
                           workspace=None, workspace_bytes=0, stream=None) -> int:
     """Raw C call of its gradients from the forward's state, with a device-side scale."""
     lib = load()
     tp, keep = _tf_ptr(transform)
     dp, keep_d = _dscale_ptr(scale, count)
-    return lib.flce_topk_kd_backward(_ptr(h), _ptr(W), _ptr(state), float(grad_scale), dp, _ptr(dH), _ptr(dW), N, H,
-                                     V, k, chunk_rows, tp, _ptr(workspace), workspace_bytes, _stream_handle(stream))
+    return lib.flce_topk_kd_backward(_ptr(h), _ptr(W), _ptr(state), float(grad_scale), dp, _ptr(dH), _ptr(dW),
+                                     dW_type, N, H, V, k, chunk_rows, tp, _ptr(workspace), workspace_bytes,
+                                     _stream_handle(stream))
 
 
 def flce_topk_kd_forward_backward(h, W, teacher, targets, weights, N, H, V, chunk_rows, ignore_index, transform,
-                                  grad_scale, out_kl, out_lse, out_loss, out_n_valid, dH, dW, workspace=None,
-                                  workspace_bytes=0, stream=None) -> int:
+                                  grad_scale, out_kl, out_lse, out_loss, out_n_valid, dH, dW, dW_type,
+                                  workspace=None, workspace_bytes=0, stream=None) -> int:
     """Raw C call of the loss and gradients in one call."""
     lib = load()
     tp, keep = _tf_ptr(transform)
     return lib.flce_topk_kd_forward_backward(_ptr(h), _ptr(W), _teacher_ptr(teacher), _ptr(targets), _ptr(weights),
                                              N, H, V, chunk_rows, ignore_index, tp, float(grad_scale), _ptr(out_kl),
                                              _ptr(out_lse), _ptr(out_loss), _ptr(out_n_valid), _ptr(dH), _ptr(dW),
-                                             _ptr(workspace), workspace_bytes, _stream_handle(stream))
+                                             dW_type, _ptr(workspace), workspace_bytes, _stream_handle(stream))
 
 
 def flce_topk_kd_state_bytes(N, k) -> int:
@@ -496,8 +500,12 @@ def flce_topk_kd_workspace_bytes(N, H, V, k, chunk_rows) -> int:
     return int(load().flce_topk_kd_workspace_bytes(N, H, V, k, chunk_rows))
 
 
-def flce_topk_kd_forward_backward_workspace_bytes(N, H, V, k, chunk_rows) -> int:
-    return int(load().flce_topk_kd_forward_backward_workspace_bytes(N, H, V, k, chunk_rows))
+def flce_topk_kd_backward_workspace_bytes(N, H, V, chunk_rows, dW_type) -> int:
+    return int(load().flce_topk_kd_backward_workspace_bytes(N, H, V, chunk_rows, dW_type))
+
+
+def flce_topk_kd_forward_backward_workspace_bytes(N, H, V, k, chunk_rows, dW_type) -> int:
+    return int(load().flce_topk_kd_forward_backward_workspace_bytes(N, H, V, k, chunk_rows, dW_type))
 
 
 def flce_rms_norm(x, ldx, residual, ldr, residual_type, weight, weight_type, weight_offset, eps, N, H, out_y,

@@ -165,15 +165,16 @@ static flce_status forward_impl(const flce_bf16* h, const flce_bf16* W, const in
     p.ignore_index = ignore_index;
     p.partials = part;
     p.zt = zt;
-    if (topk) {
-      p.sp_ids = topk->rows.ids;
-      p.sp_val = topk->rows.val;
-      p.sp_k = topk->K;
-    }
     p.tf_softcap = tfp.tf_softcap;
     p.tf_a = tfp.tf_a;
     p.tf_b = tfp.tf_b;
     p.tf_d = tfp.tf_d;
+    if (topk) {
+      p.sp_ids = topk->rows.ids;
+      p.sp_val = topk->rows.val;
+      p.sp_k = topk->K;
+      p.tf_a *= 1.f + mma_cut(H);
+    }
     int* err = nullptr;
     FLCE_CUDA_TRY(cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_device_error));
     p.err = err;
@@ -260,7 +261,8 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   if (!sizes_ok(N, H, V)) return FLCE_ERR_INVALID_ARG;
   GemmParams tfp{};
   if (!transform_params(transform, tfp)) return FLCE_ERR_INVALID_ARG;
-  if (!dH && !dW) return FLCE_ERR_INVALID_ARG;
+  flce_bf16* dW16 = topk ? topk->dW16 : nullptr;
+  if (!dH && !dW && !dW16) return FLCE_ERR_INVALID_ARG;
   if (N > 0 && (!h || !W || !targets || !lse)) return FLCE_ERR_INVALID_ARG;
   if (H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
   if (!aligned(h, 16) || !aligned(W, 16) || !aligned(dH, 16) || !aligned(dW, 16) ||
@@ -270,6 +272,7 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (N == 0) {
     if (dW) FLCE_CUDA_TRY(cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * H * 4, st));
+    if (dW16) FLCE_CUDA_TRY(cudaMemsetAsync(dW16, 0, static_cast<size_t>(V) * H * 2, st));
     return FLCE_OK;
   }
   const int cg = cta_group();
@@ -306,6 +309,7 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
     return FLCE_ERR_CUDA;
   if (dW && !make_map_t(&dW_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dW, H, V, H, 32, 32))
     return FLCE_ERR_CUDA;
+  if (dW16 && (dW || N > b.R || !make_map(&dW_map, dW16, H, V, H, 64, 32))) return FLCE_ERR_CUDA;
   const bool kLong = static_cast<long long>(N) * V >= INT_MAX ||
                      b.R * b.ldD >= INT_MAX || static_cast<long long>(N) * H >= INT_MAX ||
                      static_cast<long long>(V) * H >= INT_MAX ||
@@ -363,7 +367,7 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   if (dH && b.dh_f32 &&
       !make_map_t(&dhp_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dh_part, H, b.dh_splits * b.R, H, 32, 32))
     return FLCE_ERR_CUDA;
-  const DhDwStage dhdw{cg, workers, tm, kLong, &b, H, V, dh_part, dH, dW, &W_mn, &dW_map, &dhp_map};
+  const DhDwStage dhdw{cg, workers, tm, kLong, &b, H, V, dh_part, dH, dW, &W_mn, &dW_map, &dhp_map, dW16 != nullptr};
   // a pipelined plan: each row block in one launch whose units wait on one
   // another through counters in the workspace (two sets, alternate blocks),
   // D in two buffers of R rows (maps over both)
@@ -541,7 +545,8 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
   if (!sizes_ok(N, H, V)) return FLCE_ERR_INVALID_ARG;
   GemmParams tfp{};
   if (!transform_params(transform, tfp)) return FLCE_ERR_INVALID_ARG;
-  if (!dH && !dW) return FLCE_ERR_INVALID_ARG;
+  flce_bf16* dW16 = topk ? topk->dW16 : nullptr;
+  if (!dH && !dW && !dW16) return FLCE_ERR_INVALID_ARG;
   if (N > 0 && (!h || !W || !targets)) return FLCE_ERR_INVALID_ARG;
   if (!std::isfinite(grad_scale)) return FLCE_ERR_INVALID_ARG;
   if (H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
@@ -675,6 +680,7 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
     return FLCE_ERR_CUDA;
   if (dW && !make_map_t(&dW_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dW, H, V, H, 32, 32))
     return FLCE_ERR_CUDA;
+  if (dW16 && (dW || N > fp.R || !make_map(&dW_map, dW16, H, V, H, 64, 32))) return FLCE_ERR_CUDA;
   if (dH && fp.b.dh_f32 &&
       !make_map_t(&dhp_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dh_part, H, fp.b.dh_splits * fp.R, H, 32, 32))
     return FLCE_ERR_CUDA;
@@ -710,10 +716,12 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
     base.sp_ids = topk->rows.ids;
     base.sp_val = topk->rows.val;
     base.sp_k = topk->K;
+    base.tf_a *= 1.f + mma_cut(H);
     bsum = topk->bsum;
     bcnt = topk->bcnt;
   }
-  const DhDwStage dhdw{cg, workers, tm, kLong, &fp.b, H, V, dh_part, dH, dW, &W_mn, &dW_map, &dhp_map};
+  const DhDwStage dhdw{cg, workers, tm, kLong, &fp.b, H, V, dh_part, dH, dW, &W_mn, &dW_map, &dhp_map,
+                       dW16 != nullptr};
   // loss block sums: a segment per row block
   const long long per = ceil_div(fp.R, topk ? TOPK_ROWS : SMALL_THREADS);
   {  // the last block's segment may be shorter than the others: zero it whole

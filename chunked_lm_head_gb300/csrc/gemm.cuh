@@ -786,7 +786,8 @@ __device__ __forceinline__ int list_lower_bound(const int* ids, int k, int v) {
   return lo;
 }
 
-template <int MODE, bool kLong, int CG, bool kF8 = false, int EW = EPI_WARPS, bool kSp = false>
+// kSp: the forwards with listed columns; kOut16: the DW mode with a bf16 dW.
+template <int MODE, bool kLong, int CG, bool kF8 = false, int EW = EPI_WARPS, bool kSp = false, bool kOut16 = false>
 __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
     flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmA2,
@@ -1507,6 +1508,34 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                   *reinterpret_cast<uint4*>(dst + 8 * g) = make_uint4(
                       pack_bf16x2(v[8 * g], v[8 * g + 1]), pack_bf16x2(v[8 * g + 2], v[8 * g + 3]),
                       pack_bf16x2(v[8 * g + 4], v[8 * g + 5]), pack_bf16x2(v[8 * g + 6], v[8 * g + 7]));
+            }
+          } else if constexpr (kOut16) {
+            // dW rounded to bf16 once (its only row block): two chunks fill a
+            // 32-row x 64-column box, which TMA stores; columns past H and
+            // rows past V are clipped.  Half the bytes of the fp32 gradient,
+            // and none are read back to be rounded (256 x 2,048 x 248,320: see
+            // the launch in launch.cuh)
+            static_assert(MODE == MODE_DW, "bf16 output: the dW mode");
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) pk[j / 2] = pack_bf16x2(v[j], v[j + 1]);
+            const int half = c & 1;
+            const uint32_t box =
+                out_stage + (warp - 2) * (kBoxes * OUT_BOX_BYTES) + ((c >> 1) % kBoxes) * OUT_BOX_BYTES;
+            if (half == 0) {
+              if (lane == 0) bulk_wait_read<kBoxes - 1>();  // the copy that last used this box has read it
+              __syncwarp();
+            }
+            stage_bf16_half(box, lane, half, pk);
+            if (half == 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                const int x = col0 - 32;  // first column of the box
+                const int oy = uv0 + t.m * C::TM + rank * BM + q * 32;
+                if (x < p.H && oy < p.V) tma_store_2d(&tmC, box, x, oy);
+                bulk_commit();
+              }
             }
           } else {  // MODE_DW, or MODE_DH into fp32 partials (DHDW: either unit kind)
             // stage this warp's 32 x 32 box (row = lane) in 128B-swizzled

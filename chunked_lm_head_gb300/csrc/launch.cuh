@@ -227,6 +227,26 @@ cudaError_t launch_fwd_listed(int cg, bool kLong, const CUtensorMap& a, const CU
                : go(flce_gemm_kernel<MODE, false, 1, false, EPI_WARPS, true>, TileCfg<1>::SMEM, 1);
 }
 
+// The dW GEMM with a bf16 result.
+template <int EW>
+cudaError_t launch_dw16_t(int cg, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const GemmParams& p,
+                          int workers, cudaStream_t st) {
+  auto go = [&](auto kern, int smem, int grid_mult) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_persistent(kern, grid_mult * grid_workers(workers), grid_mult, gemm_threads(EW), smem, st, a, b, c, a,
+                             b, c, a, b, c, p);
+  };
+  return cg == 2 ? go(flce_gemm_kernel<MODE_DW, false, 2, false, EW, false, true>, KernelCfg<MODE_DW, 2, EW>::SMEM, 2)
+                 : go(flce_gemm_kernel<MODE_DW, false, 1, false, EW, false, true>, KernelCfg<MODE_DW, 1, EW>::SMEM, 1);
+}
+cudaError_t launch_dw16(int cg, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const GemmParams& p,
+                        int workers, cudaStream_t st) {
+  // 16 epilogue warps at short K, as the fp32 dW
+  return p.k_blocks <= kDwWideEpilogueMaxKBlocks ? launch_dw16_t<4 * EPI_WARPS>(cg, a, b, c, p, workers, st)
+                                                 : launch_dw16_t<EPI_WARPS>(cg, a, b, c, p, workers, st);
+}
+
 // CTA group of the GEMMs: 2 (SM pairs, 256-row tiles) unless
 // FLCE_OPT_CTA_GROUP = 1.
 int cta_group() { return opt(FLCE_OPT_CTA_GROUP) == 1 ? 1 : 2; }
@@ -414,13 +434,14 @@ struct DhDwStage {
   const CUtensorMap* W_mn;
   const CUtensorMap* dW_map;
   const CUtensorMap* dhp_map;  // fp32 dH partials [dh_splits * R][H]
+  bool dw16 = false;           // one row block: dW in bf16, dW_map 64 x 32 boxes of it
 };
 
 flce_status slab_dh_dw(const DhDwStage& a, const GemmParams& p, int rows, int block, int slab, int v0,
                        int width, const CUtensorMap& D_k, const CUtensorMap& D_mn,
                        const CUtensorMap& B_dw, cudaStream_t st) {
   const BwdPlan& b = *a.plan;
-  if (a.dH && a.dW && fuse_dh_dw_on() && b.n_slabs > 1) {
+  if (a.dH && a.dW && !a.dw16 && fuse_dh_dw_on() && b.n_slabs > 1) {
     // both in one launch: the DH units (as below), then the DW units.  Only
     // for plans of several vocabulary slabs, whose short launches pay their
     // fixed cost twice per slab otherwise (131,072 x 2,560 x 151,936 at
@@ -475,7 +496,7 @@ flce_status slab_dh_dw(const DhDwStage& a, const GemmParams& p, int rows, int bl
       FLCE_CUDA_TRY(launch_gemm<MODE_DH>(a.cg, a.kLong, D_k, *a.W_mn, b.dh_f32 ? *a.dhp_map : *a.W_mn, q,
                                          std::min(q.num_units, a.workers), st));
   }
-  if (a.dW) {  // dW[slab] (+)= D[:, slab]^T h[rows]
+  if (a.dW || a.dw16) {  // dW[slab] (+)= D[:, slab]^T h[rows]
     GemmParams q = p;
     q.v0 = v0;
     q.m_tiles = static_cast<int>(ceil_div(width, a.tm));
@@ -489,8 +510,9 @@ flce_status slab_dh_dw(const DhDwStage& a, const GemmParams& p, int rows, int bl
     q.group_m = dw_group(q.k_blocks, q.m_tiles);
     q.dW_accumulate = block > 0 ? 1 : 0;
     ProfScope ps(K_DW, st);
-    FLCE_CUDA_TRY(launch_gemm<MODE_DW>(a.cg, a.kLong, D_mn, B_dw, *a.dW_map, q,
-                                       std::min(q.num_units, a.workers), st));
+    const int nw = std::min(q.num_units, a.workers);
+    FLCE_CUDA_TRY(a.dw16 ? launch_dw16(a.cg, D_mn, B_dw, *a.dW_map, q, nw, st)
+                         : launch_gemm<MODE_DW>(a.cg, a.kLong, D_mn, B_dw, *a.dW_map, q, nw, st));
   }
   return FLCE_OK;
 }
@@ -568,7 +590,18 @@ struct TopkCall {
   float* out_lse = nullptr;
   double* bsum = nullptr;  // block sums of the row kernel
   long long* bcnt = nullptr;
+  flce_bf16* dW16 = nullptr;  // dW in bf16 straight from the GEMM (one row block), instead of dW
 };
+
+// What the tensor cores' sums lack, relative to the sum.  tcgen05 cuts its
+// running fp32 sum to 24 bits at every step of 16 products instead of rounding
+// it, so a logit of size |z| comes out short: measured over the largest
+// logits, by 0.26 x 2^-24 |z| per step (0.22 at 16 steps, 0.264 at 512; a
+// partial sum is half the logit on average and a cut loses half a unit, which
+// bounds it by 0.5).  Left alone it biases a log-sum-exp of 4,096 products by
+// -4e-6, thirty times a rounded sum's error; the forward with listed columns
+// puts it back in the factor that every logit is multiplied by anyway.
+float mma_cut(int64_t H) { return static_cast<float>(0.26 * static_cast<double>(ceil_div(H, UMMA_K)) / 16777216.0); }
 
 // The row kernel over `rows` rows (row0 + j, or ri[j]); its block sums at
 // bsum / bcnt + block0.

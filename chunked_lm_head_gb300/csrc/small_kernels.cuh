@@ -571,6 +571,17 @@ __global__ void scale_bf16_kernel(__nv_bfloat16* __restrict__ x, long long n, co
     x[i] = __float2bfloat16_rn(__bfloat162float(x[i]) * s);
 }
 
+// bf16 of n fp32 values (n a multiple of 8), each rounded once.
+__global__ void round_bf16_kernel(const float* __restrict__ x, long long n, uint16_t* __restrict__ y) {
+  const long long nv = n / 8;
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < nv; i += stride) {
+    const float4 a = reinterpret_cast<const float4*>(x)[2 * i], b = reinterpret_cast<const float4*>(x)[2 * i + 1];
+    reinterpret_cast<uint4*>(y)[i] =
+        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+  }
+}
+
 __global__ void scale_f32_kernel(float* __restrict__ x, long long n, const float* __restrict__ scale) {
   const float s = *scale;
   if (s == 1.f) return;

@@ -84,6 +84,37 @@ flce_status topk_lists(const flce_top_logits* t, const int64_t* targets, int64_t
   return FLCE_OK;
 }
 
+// dW in the caller's type.  bf16 comes straight from the dW GEMM where one row
+// block holds every row; else it is summed over the blocks in fp32 scratch and
+// rounded once at the end.
+struct TopkGrad {
+  bool scratch = false;
+  size_t bytes = 0;  // of the scratch
+};
+TopkGrad topk_grad(int32_t dW_type, int64_t N, int64_t H, int64_t V, long long block_rows) {
+  TopkGrad g;
+  g.scratch = dW_type == FLCE_BF16 && N > block_rows;
+  if (g.scratch) g.bytes = align256(static_cast<size_t>(V) * H * 4);
+  return g;
+}
+long long topk_bwd_rows(int64_t N, int64_t H, int64_t V, int64_t chunk_rows) {
+  const int cg = cta_group();
+  return plan_backward(N, H, V, chunk_rows, device_workers(cg), BM * cg).R;
+}
+long long topk_one_call_rows(int64_t N, int64_t H, int64_t V, int64_t chunk_rows) {
+  const int cg = cta_group();
+  const FusedPlan fp = plan_fused(N, H, V, chunk_rows, device_workers(cg), BM * cg);
+  return fp.fused && N > 0 ? fp.R : topk_bwd_rows(N, H, V, chunk_rows);
+}
+bool topk_dw_ok(const void* dW, int32_t dW_type) { return dW == nullptr || dW_type == FLCE_BF16 || dW_type == FLCE_F32; }
+
+flce_status topk_round_dw(const float* x, int64_t n, void* dW, cudaStream_t st) {
+  ProfScope ps(K_DH_REDUCE, st);
+  round_bf16_kernel<<<8 * device_sms(), SMALL_THREADS, 0, st>>>(x, n, static_cast<uint16_t*>(dW));
+  FLCE_CUDA_TRY(cudaGetLastError());
+  return FLCE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -98,10 +129,17 @@ size_t flce_topk_kd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k, 
   return align256(flce_workspace_bytes(N, H, V, chunk_rows)) + topk_layout(N, k).total;
 }
 
-size_t flce_topk_kd_forward_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k,
-                                                     int64_t chunk_rows) {
+size_t flce_topk_kd_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t chunk_rows, int32_t dW_type) {
+  if (!sizes_ok(N, H, V)) return 0;
+  return align256(flce_workspace_bytes(N, H, V, chunk_rows)) +
+         topk_grad(dW_type, N, H, V, topk_bwd_rows(N, H, V, chunk_rows)).bytes;
+}
+
+size_t flce_topk_kd_forward_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k, int64_t chunk_rows,
+                                                     int32_t dW_type) {
   if (!sizes_ok(N, H, V) || k < 1 || k > TOPK_MAX_K) return 0;
-  return align256(flce_forward_backward_workspace_bytes(N, H, V, chunk_rows)) + topk_layout(N, k).total;
+  return align256(flce_forward_backward_workspace_bytes(N, H, V, chunk_rows)) + topk_layout(N, k).total +
+         topk_grad(dW_type, N, H, V, topk_one_call_rows(N, H, V, chunk_rows)).bytes;
 }
 
 flce_status flce_topk_kd_forward(const flce_bf16* h, const flce_bf16* W, const flce_top_logits* teacher,
@@ -144,12 +182,16 @@ flce_status flce_topk_kd_forward(const flce_bf16* h, const flce_bf16* W, const f
 }
 
 flce_status flce_topk_kd_backward(const flce_bf16* h, const flce_bf16* W, const void* state, float grad_scale,
-                                  const flce_device_scale* device_scale, flce_bf16* dH, float* dW, int64_t N,
-                                  int64_t H, int64_t V, int64_t k, int64_t chunk_rows,
+                                  const flce_device_scale* device_scale, flce_bf16* dH, void* dW, int32_t dW_type,
+                                  int64_t N, int64_t H, int64_t V, int64_t k, int64_t chunk_rows,
                                   const flce_logit_transform* transform, void* workspace, size_t workspace_bytes,
                                   void* stream) {
-  if (!sizes_ok(N, H, V) || k < 1 || (N > 0 && !state)) return FLCE_ERR_INVALID_ARG;
-  if (k > TOPK_MAX_K || !aligned(state, 256)) return FLCE_ERR_UNSUPPORTED;
+  if (!sizes_ok(N, H, V) || k < 1 || (N > 0 && !state) || !topk_dw_ok(dW, dW_type)) return FLCE_ERR_INVALID_ARG;
+  GemmParams tfp{};
+  if (!transform_params(transform, tfp) || (!dH && !dW) || (N > 0 && (!h || !W))) return FLCE_ERR_INVALID_ARG;
+  if (k > TOPK_MAX_K || H % 8 != 0 || !aligned(state, 256) || !aligned(dW, 16) || !aligned(dH, 16) || !aligned(h, 16) ||
+      !aligned(W, 16))
+    return FLCE_ERR_UNSUPPORTED;
   const TopkLayout L = topk_layout(N, k);
   TopkCall c;
   // read only by the tiled backward
@@ -158,9 +200,20 @@ flce_status flce_topk_kd_backward(const flce_bf16* h, const flce_bf16* W, const 
   c.K = static_cast<int>(k);
   const long long* count = device_scale ? reinterpret_cast<const long long*>(device_scale->count) : nullptr;
   const float* scale = device_scale ? device_scale->scale : nullptr;
-  return backward_impl(h, W, reinterpret_cast<const int64_t*>(c.rows.mark), c.rows.coef, c.rows.lse_rest, grad_scale,
-                       dH, dW, N, H, V, chunk_rows, kMarkIgnored, transform, workspace, workspace_bytes, stream, count,
-                       scale, &c);
+  const bool bf16 = dW != nullptr && dW_type == FLCE_BF16;
+  const TopkGrad tg = topk_grad(dW ? dW_type : FLCE_F32, N, H, V, topk_bwd_rows(N, H, V, chunk_rows));
+  if (bf16 && !tg.scratch) c.dW16 = static_cast<flce_bf16*>(dW);
+  const size_t inner = align256(flce_workspace_bytes(N, H, V, chunk_rows));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Workspace ws;
+  flce_status s = get_workspace(ws, workspace, workspace_bytes, inner + tg.bytes, st);
+  if (s != FLCE_OK) return s;
+  float* sum = tg.scratch ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws.ptr) + inner)
+                          : bf16 ? nullptr : static_cast<float*>(dW);
+  s = backward_impl(h, W, reinterpret_cast<const int64_t*>(c.rows.mark), c.rows.coef, c.rows.lse_rest, grad_scale, dH,
+                    sum, N, H, V, chunk_rows, kMarkIgnored, transform, ws.ptr, inner, stream, count, scale, &c);
+  if (s != FLCE_OK || !tg.scratch) return s;
+  return topk_round_dw(sum, V * H, dW, st);
 }
 
 flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W, const flce_top_logits* teacher,
@@ -168,12 +221,13 @@ flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W
                                           int64_t V, int64_t chunk_rows, int64_t ignore_index,
                                           const flce_logit_transform* transform, float grad_scale, float* out_kl,
                                           float* out_lse, float* out_loss, int64_t* out_n_valid, flce_bf16* dH,
-                                          float* dW, void* workspace, size_t workspace_bytes, void* stream) {
+                                          void* dW, int32_t dW_type, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
   flce_status s = topk_check(teacher, targets, weights, N, H, V);
   if (s != FLCE_OK) return s;
   GemmParams tfp{};
   if (!transform_params(transform, tfp) || !std::isfinite(grad_scale)) return FLCE_ERR_INVALID_ARG;
-  if ((!dH && !dW) || (N > 0 && (!h || !W))) return FLCE_ERR_INVALID_ARG;
+  if ((!dH && !dW) || (N > 0 && (!h || !W)) || !topk_dw_ok(dW, dW_type)) return FLCE_ERR_INVALID_ARG;
   if (H % 8 != 0 || !aligned(h, 16) || !aligned(W, 16) || !aligned(dH, 16) || !aligned(dW, 16) ||
       !aligned(out_kl, 4) || !aligned(out_lse, 4) || !aligned(out_loss, 4) || !aligned(out_n_valid, 8))
     return FLCE_ERR_UNSUPPORTED;
@@ -181,10 +235,14 @@ flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W
   const size_t inner = align256(flce_forward_backward_workspace_bytes(N, H, V, chunk_rows));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Workspace ws;
-  s = get_workspace(ws, workspace, workspace_bytes, inner + L.total, st);
+  const bool bf16 = dW != nullptr && dW_type == FLCE_BF16;
+  const TopkGrad tg = topk_grad(dW ? dW_type : FLCE_F32, N, H, V, topk_one_call_rows(N, H, V, chunk_rows));
+  s = get_workspace(ws, workspace, workspace_bytes, inner + L.total + tg.bytes, st);
   if (s != FLCE_OK) return s;
   uint8_t* wb = static_cast<uint8_t*>(ws.ptr);
+  float* sum = tg.scratch ? reinterpret_cast<float*>(wb + inner + L.total) : bf16 ? nullptr : static_cast<float*>(dW);
   TopkCall c;
+  if (bf16 && !tg.scratch) c.dW16 = static_cast<flce_bf16*>(dW);
   c.rows = topk_rows_at(L, wb + inner, wb + inner);
   c.K = teacher->k;
   c.tail = teacher->tail;
@@ -195,9 +253,11 @@ flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W
   c.bcnt = reinterpret_cast<long long*>(wb + inner + L.bcnt);
   s = topk_lists(teacher, targets, ignore_index, N, V, c.rows, st);
   if (s != FLCE_OK) return s;
-  return forward_backward_impl(h, W, reinterpret_cast<const int64_t*>(c.rows.mark), nullptr, N, H, V, chunk_rows,
-                               kMarkIgnored, transform, grad_scale, nullptr, nullptr, out_loss, out_n_valid, dH, dW,
-                               wb, inner, stream, nullptr, &c);
+  s = forward_backward_impl(h, W, reinterpret_cast<const int64_t*>(c.rows.mark), nullptr, N, H, V, chunk_rows,
+                            kMarkIgnored, transform, grad_scale, nullptr, nullptr, out_loss, out_n_valid, dH, sum, wb,
+                            inner, stream, nullptr, &c);
+  if (s != FLCE_OK || !tg.scratch) return s;
+  return topk_round_dw(sum, V * H, dW, st);
 }
 
 }  // extern "C"

@@ -18,6 +18,9 @@ _IDS = {torch.int32: _lib.DTYPES["i32"], torch.int64: _lib.DTYPES["i64"]}
 _LOGITS = {torch.float32: _lib.DTYPES["f32"], torch.bfloat16: _lib.DTYPES["bf16"], torch.float16: _lib.DTYPES["f16"]}
 
 
+_DW = {torch.float32: _lib.DTYPES["f32"], torch.bfloat16: _lib.DTYPES["bf16"]}
+
+
 def _workspace(workspace, nbytes, stream, device):
     """(workspace, bytes): the caller's, or one from torch's allocator, which
     orders its reuse on the current stream; with a stream of the caller's the
@@ -86,22 +89,25 @@ def topk_kd_forward(h, W, ids, logits, lse_t=None, targets=None, weights=None, t
 
 def topk_kd_backward(h, W, state, k: int, grad_scale: float, chunk_rows: int = 256, transform=None,
                      need_dH: bool = True, need_dW: bool = True, workspace: torch.Tensor | None = None, stream=None,
-                     scale=None, count=None):
-    """(dH[N,H] bf16 or None, dW[V,H] f32 or None) from the forward's state
-    (same h, W, k and transform).  scale / count: device-side factors of
-    grad_scale, as in backward()."""
+                     scale=None, count=None, dW_dtype=torch.float32):
+    """(dH[N,H] bf16 or None, dW[V,H] of dW_dtype (float32 or bfloat16) or None)
+    from the forward's state (same h, W, k and transform).  scale / count:
+    device-side factors of grad_scale, as in backward()."""
+    if dW_dtype not in _DW:
+        raise ValueError("dW_dtype must be float32 or bfloat16")
     (N, H), V, dev = h.shape, W.shape[0], h.device
     if W.shape[1] != H or any(not x.is_cuda or x.dtype != torch.bfloat16 or not x.is_contiguous() for x in (h, W)):
         raise ValueError("h[N,H] and W[V,H] must be contiguous bfloat16 CUDA tensors")
     if state is None or state.numel() * state.element_size() != _lib.flce_topk_kd_state_bytes(N, k):
         raise ValueError("state must come from topk_kd_forward(for_backward=True) of the same N and k")
     dH = torch.empty_like(h) if need_dH else None
-    dW = torch.empty((V, H), dtype=torch.float32, device=dev) if need_dW else None
+    dW = torch.empty((V, H), dtype=dW_dtype, device=dev) if need_dW else None
     scale = _device_scalar(scale, torch.float32, dev)
     count = _device_scalar(count, torch.int64, dev)
-    ws, ws_bytes = _workspace(workspace, _lib.flce_topk_kd_workspace_bytes(N, H, V, k, chunk_rows), stream, dev)
-    st = _lib.flce_topk_kd_backward(h, W, state, grad_scale, scale, count, dH, dW, N, H, V, k, chunk_rows, transform,
-                                    ws, ws_bytes, stream)
+    ws, ws_bytes = _workspace(workspace, _lib.flce_topk_kd_backward_workspace_bytes(N, H, V, chunk_rows, _DW[dW_dtype]),
+                              stream, dev)
+    st = _lib.flce_topk_kd_backward(h, W, state, grad_scale, scale, count, dH, dW, _DW[dW_dtype], N, H, V, k,
+                                    chunk_rows, transform, ws, ws_bytes, stream)
     _lib.check("flce_topk_kd_backward", st)
     return dH, dW
 
@@ -109,10 +115,13 @@ def topk_kd_backward(h, W, state, k: int, grad_scale: float, chunk_rows: int = 2
 def topk_kd_forward_backward(h, W, ids, logits, lse_t=None, targets=None, weights=None, tail: bool = False,
                              chunk_rows: int = 4096, ignore_index: int = IGNORE_INDEX, grad_scale: float = 1.0,
                              need_dH: bool = True, need_dW: bool = True, workspace: torch.Tensor | None = None,
-                             stream=None, transform=None, need_lse: bool = True):
+                             stream=None, transform=None, need_lse: bool = True, dW_dtype=torch.float32):
     """Loss and its gradients in one call without the logits recompute:
-    dict(kl, lse, loss, n_valid, dH, dW).  need_lse=False returns lse None and
-    lets the call skip the rows without loss."""
+    dict(kl, lse, loss, n_valid, dH, dW), dW of dW_dtype (float32 or bfloat16).
+    need_lse=False returns lse None and lets the call skip the rows without
+    loss."""
+    if dW_dtype not in _DW:
+        raise ValueError("dW_dtype must be float32 or bfloat16")
     t = _check(h, W, ids, logits, lse_t, targets, weights, tail)
     (N, H), V, dev = h.shape, W.shape[0], h.device
     kl = torch.empty(N, dtype=torch.float32, device=dev)
@@ -120,11 +129,13 @@ def topk_kd_forward_backward(h, W, ids, logits, lse_t=None, targets=None, weight
     loss = torch.empty((), dtype=torch.float32, device=dev)
     n_valid = torch.empty((), dtype=torch.int64, device=dev)
     dH = torch.empty_like(h) if need_dH else None
-    dW = torch.empty((V, H), dtype=torch.float32, device=dev) if need_dW else None
-    ws, ws_bytes = _workspace(workspace, _lib.flce_topk_kd_forward_backward_workspace_bytes(N, H, V, t.k, chunk_rows),
+    dW = torch.empty((V, H), dtype=dW_dtype, device=dev) if need_dW else None
+    ws, ws_bytes = _workspace(workspace, _lib.flce_topk_kd_forward_backward_workspace_bytes(N, H, V, t.k, chunk_rows,
+                                                                                            _DW[dW_dtype]),
                               stream, dev)
     st = _lib.flce_topk_kd_forward_backward(h, W, t, targets, weights, N, H, V, chunk_rows, ignore_index, transform,
-                                            grad_scale, kl, lse, loss, n_valid, dH, dW, ws, ws_bytes, stream)
+                                            grad_scale, kl, lse, loss, n_valid, dH, dW, _DW[dW_dtype], ws, ws_bytes,
+                                            stream)
     _lib.check("flce_topk_kd_forward_backward", st)
     return {"kl": kl, "lse": lse, "loss": loss, "n_valid": n_valid, "dH": dH, "dW": dW}
 
@@ -145,7 +156,7 @@ class TopkDistill(torch.autograd.Function):
     def backward(ctx, grad_loss, grad_kl, grad_n):
         h, W, state, n_valid = ctx.saved_tensors
         dH, dW = topk_kd_backward(h, W, state, ctx.k, 1.0, ctx.chunk_rows, ctx.transform, ctx.needs_input_grad[0],
-                                  ctx.needs_input_grad[1], scale=grad_loss, count=n_valid)
+                                  ctx.needs_input_grad[1], scale=grad_loss, count=n_valid, dW_dtype=W.dtype)
         return (dH, dW) + (None,) * 9
 
 
@@ -157,7 +168,7 @@ class TopkDistillOneCall(torch.autograd.Function):
     def forward(ctx, h, W, ids, logits, lse_t, targets, weights, tail, chunk_rows, ignore_index, transform):
         out = topk_kd_forward_backward(h, W, ids, logits, lse_t, targets, weights, tail, chunk_rows, ignore_index,
                                        1.0, ctx.needs_input_grad[0], ctx.needs_input_grad[1], transform=transform,
-                                       need_lse=False)
+                                       need_lse=False, dW_dtype=W.dtype)
         ctx.grads = (out["dH"], out["dW"])
         ctx.mark_non_differentiable(out["kl"], out["n_valid"])
         return out["loss"], out["kl"], out["n_valid"]
@@ -168,8 +179,9 @@ class TopkDistillOneCall(torch.autograd.Function):
             raise RuntimeError("the one-call loss can be differentiated once: its gradients are scaled in place")
         dH, dW = ctx.grads
         ctx.grads = None
-        if dH is not None or dW is not None:
-            scale_grads(dH, dW, grad_loss)
+        for d in (dH, dW):  # both bf16
+            if d is not None:
+                scale_grads(d, None, grad_loss)
         return (dH, dW) + (None,) * 9
 
 

@@ -499,13 +499,15 @@ FLCE_API flce_status flce_topk_kd_forward(const flce_bf16* h, const flce_bf16* W
  *       = m w g f'(z) ((P + T) R - T) softmax(u)_v / R               v not in S
  *   dH = D W, dW = D^T h,  g = grad_scale * (*scale) / max(*count, 1)
  * (device_scale as flce_backward_ex2, or NULL).  Same h, W, k and transform
- * as the forward that wrote state.  chunk_rows, dH and dW as flce_backward;
- * workspace flce_topk_kd_workspace_bytes, or NULL.
+ * as the forward that wrote state.  chunk_rows and dH as flce_backward; dW
+ * [V,H] of dW_type, FLCE_F32 or FLCE_BF16 (rounded once: by the dW GEMM itself
+ * where one row block holds every row, else from fp32 sums in the workspace).
+ * Workspace flce_topk_kd_backward_workspace_bytes, or NULL.
  */
 FLCE_API flce_status flce_topk_kd_backward(const flce_bf16* h, const flce_bf16* W, const void* state,
                                            float grad_scale, const flce_device_scale* device_scale,
-                                           flce_bf16* dH, float* dW, int64_t N, int64_t H, int64_t V,
-                                           int64_t k, int64_t chunk_rows,
+                                           flce_bf16* dH, void* dW, int32_t dW_type, int64_t N,
+                                           int64_t H, int64_t V, int64_t k, int64_t chunk_rows,
                                            const flce_logit_transform* transform, void* workspace,
                                            size_t workspace_bytes, void* stream);
 
@@ -523,17 +525,20 @@ FLCE_API flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flc
                                                    const flce_logit_transform* transform,
                                                    float grad_scale, float* out_kl, float* out_lse,
                                                    float* out_loss, int64_t* out_n_valid,
-                                                   flce_bf16* dH, float* dW, void* workspace,
-                                                   size_t workspace_bytes, void* stream);
+                                                   flce_bf16* dH, void* dW, int32_t dW_type,
+                                                   void* workspace, size_t workspace_bytes,
+                                                   void* stream);
 
-/* Bytes of flce_topk_kd_forward's state; of the workspace of
- * flce_topk_kd_forward and flce_topk_kd_backward; and of
- * flce_topk_kd_forward_backward's (0 on invalid sizes). */
+/* Bytes of flce_topk_kd_forward's state and workspace, and of the other two
+ * calls' workspaces for a dW of dW_type (0 on invalid sizes). */
 FLCE_API size_t flce_topk_kd_state_bytes(int64_t N, int64_t k);
 FLCE_API size_t flce_topk_kd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k,
                                              int64_t chunk_rows);
+FLCE_API size_t flce_topk_kd_backward_workspace_bytes(int64_t N, int64_t H, int64_t V,
+                                                      int64_t chunk_rows, int32_t dW_type);
 FLCE_API size_t flce_topk_kd_forward_backward_workspace_bytes(int64_t N, int64_t H, int64_t V,
-                                                              int64_t k, int64_t chunk_rows);
+                                                              int64_t k, int64_t chunk_rows,
+                                                              int32_t dW_type);
 
 /*
  * GRPO per-token objective on the sampled tokens' log-probs.  Source: TRL

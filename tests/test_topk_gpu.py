@@ -52,6 +52,16 @@ def run_all(c, tail=False, tf=None, chunk=256, one_call_chunk=4096, what=""):
     lean = flce.topk_kd_forward_backward(*args, chunk_rows=one_call_chunk, transform=tf, need_lse=False)
     R.check(lean, ref, roundings=2, what=what + "one call without lse")
     assert lean["lse"] is None
+    # dW in bf16: straight from the GEMM, or from sums over row blocks
+    half = flce.topk_kd_forward_backward(*args, chunk_rows=one_call_chunk, transform=tf, dW_dtype=torch.bfloat16)
+    assert torch.equal(half["dW"], one["dW"].bfloat16()) and torch.equal(half["dH"], one["dH"])
+    dH16, dW16 = flce.topk_kd_backward(c["h"], c["W"], out["state"], K, 1.0, chunk, tf, count=out["n_valid"],
+                                       dW_dtype=torch.bfloat16)
+    assert torch.equal(dW16, dW.bfloat16()) and torch.equal(dH16, dH)
+    _, only = flce.topk_kd_backward(c["h"], c["W"], out["state"], K, 1.0, chunk, tf, count=out["n_valid"],
+                                    dW_dtype=torch.bfloat16, need_dH=False)
+    assert float((only.double() - dW.double()).norm()) <= 1e-2 * float(dW.double().norm())
+    assert _lib.flce_device_status() == 0
     return ref, out, one
 
 
@@ -286,7 +296,11 @@ def test_workspace_of_the_caller_is_enough():
     a = flce.topk_kd_forward(c["h"], c["W"], c["ids"], c["logits"], workspace=ws, for_backward=True)
     b = flce.topk_kd_forward(c["h"], c["W"], c["ids"], c["logits"])
     assert torch.equal(a["kl"], b["kl"])
-    flce.topk_kd_backward(c["h"], c["W"], a["state"], K, 1.0, workspace=ws)
+    bws = torch.empty(_lib.flce_topk_kd_backward_workspace_bytes(500, 64, 1500, 256, _lib.DTYPES["bf16"]),
+                      dtype=torch.uint8, device="cuda")
+    flce.topk_kd_backward(c["h"], c["W"], a["state"], K, 1.0, workspace=bws, dW_dtype=torch.bfloat16)
+    with pytest.raises(_lib.FlceError):
+        flce.topk_kd_backward(c["h"], c["W"], a["state"], K, 1.0, workspace=bws[:-256], dW_dtype=torch.bfloat16)
     with pytest.raises(_lib.FlceError):
         flce.topk_kd_forward(c["h"], c["W"], c["ids"], c["logits"], workspace=ws[:-256])
     with pytest.raises(ValueError, match="state"):

@@ -25,13 +25,13 @@ def fwd(t, h=P, W=P, targets=None, weights=None, N=4, H=64, V=100, tf=None, flag
                                      state, ws, wb, 0)
 
 
-def fb(t, h=P, W=P, N=4, H=64, V=100, tf=None, g=1.0, dH=P, dW=P, loss=None, ws=None, wb=0):
+def fb(t, h=P, W=P, N=4, H=64, V=100, tf=None, g=1.0, dH=P, dW=P, dt=D["f32"], loss=None, ws=None, wb=0):
     return _lib.flce_topk_kd_forward_backward(h, W, t, None, None, N, H, V, 256, -100, tf, g, None, None, loss, None,
-                                              dH, dW, ws, wb, 0)
+                                              dH, dW, dt, ws, wb, 0)
 
 
-def bwd(state=P, h=P, W=P, N=4, H=64, V=100, k=8, tf=None, dH=P, dW=P, ws=None, wb=0):
-    return _lib.flce_topk_kd_backward(h, W, state, 1.0, None, None, dH, dW, N, H, V, k, 256, tf, ws, wb, 0)
+def bwd(state=P, h=P, W=P, N=4, H=64, V=100, k=8, tf=None, dH=P, dW=P, dt=D["f32"], ws=None, wb=0):
+    return _lib.flce_topk_kd_backward(h, W, state, 1.0, None, None, dH, dW, dt, N, H, V, k, 256, tf, ws, wb, 0)
 
 
 BAD_TEACHERS = [
@@ -64,6 +64,7 @@ def test_forward_refusals(kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(dH=None, dW=None), INVALID), (dict(h=None), INVALID), (dict(g=float("inf")), INVALID),
     (dict(tf={"softcap": -1.0}), INVALID), (dict(ws=P, wb=64), INVALID), (dict(H=60), UNSUPPORTED),
+    (dict(dt=D["f16"]), INVALID),
     (dict(dW=P + 4), UNSUPPORTED), (dict(loss=P + 2), UNSUPPORTED),
 ])
 def test_one_call_refusals(kw, want):
@@ -73,6 +74,7 @@ def test_one_call_refusals(kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(state=None), INVALID), (dict(k=0), INVALID), (dict(dH=None, dW=None), INVALID), (dict(h=None), INVALID),
     (dict(tf={"temperature": -1.0}), INVALID), (dict(ws=P, wb=64), INVALID), (dict(k=1025), UNSUPPORTED),
+    (dict(dt=D["i64"]), INVALID), (dict(dW=P + 8), UNSUPPORTED),
     (dict(state=P + 8), UNSUPPORTED), (dict(H=12), UNSUPPORTED),
 ])
 def test_backward_refusals(kw, want):
@@ -87,6 +89,10 @@ def test_sizes():
     # beside the cross-entropy's workspace: 12 bytes per entry and a few per row
     extra = w(4096, 512, 20000, 64, 256) - _lib.flce_workspace_bytes(4096, 512, 20000, 256)
     assert extra <= 4096 * (64 * 12 + 64) + (1 << 16)
+    # a bf16 dW takes fp32 scratch only where several row blocks are summed
+    f = _lib.flce_topk_kd_forward_backward_workspace_bytes
+    assert f(4096, 512, 20000, 64, 4096, D["bf16"]) == f(4096, 512, 20000, 64, 4096, D["f32"])
+    assert f(4096, 512, 20000, 64, 2048, D["bf16"]) == f(4096, 512, 20000, 64, 2048, D["f32"]) + 20000 * 512 * 4
 
 
 def test_torch_checks():
