@@ -219,10 +219,17 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_raw_stream = None  # (current stream of a device as an integer, current device), without a Stream object
+
+
 def _stream_handle(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            torch.cuda.current_stream()  # initialises CUDA
+            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+        return _raw_stream[0](_raw_stream[1]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -180,6 +180,16 @@ static flce_status forward_impl(const flce_bf16* h, const flce_bf16* W, const in
     p.err = err;
     const bool kLong = static_cast<long long>(N) * V >= INT_MAX ||
                        static_cast<long long>(f.S) * N >= INT_MAX;
+    if (topk && topk_gemv_for(N, H)) {
+      p.tf_a = tfp.tf_a;  // its sums are rounded, not cut
+      flce_status sg = topk_gemv(*topk, p, h, W, topk->gemv, st);
+      if (sg != FLCE_OK) return sg;
+      FwdPlan g = f;
+      g.S = topk_gemv_ctas(V);
+      sg = topk_rows(*topk, kLong, g, p, Ni, 0, Ni, nullptr, topk->gemv, skip_ignored, 0, st);
+      if (sg != FLCE_OK) return sg;
+      return loss_sums(out_loss, out_n_valid, topk->bsum, topk->bcnt, ceil_div(N, TOPK_ROWS), st);
+    }
     for (long long row0 = 0; row0 < N; row0 += fb) {
       GemmParams q = p;
       q.row0 = static_cast<int>(row0);
@@ -435,7 +445,7 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
       if (topk) {
         const flce_status sc = topk_scatter(*topk, kLong, p, Dbuf, v0, width, static_cast<int>(row0), rows,
                                             compact ? cidx : nullptr, compact ? ccount : nullptr,
-                                            static_cast<int>(row0), count_scale, nullptr, st);
+                                            static_cast<int>(row0), count_scale, st);
         if (sc != FLCE_OK) return sc;
       }
       // (2) dH[rows] (+)= D W[slab], (3) dW[slab] (+)= D^T h[rows]
@@ -635,8 +645,7 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
   // GRPO: the block's log-probs feed its token losses and backward weights
   float* lp = out_logp ? out_logp : (grpo ? reinterpret_cast<float*>(wb + L.lp) : nullptr);
   float* wg = reinterpret_cast<float*>(wb + L.wg);
-  const float* dl_weights = topk ? topk->rows.coef : grpo ? wg : weights;
-  const float* dl_lse = topk ? topk->rows.lse_rest : lse;
+  const float* dl_weights = grpo ? wg : weights;
   const int Ni = static_cast<int>(N);
   const bool validate = validate_on() && !topk;  // a list's marks are no targets
   // Row compaction: the blocks run over a permutation of the rows with the
@@ -662,7 +671,8 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
     if (nbad != 0) return FLCE_ERR_BAD_TARGET;
   }
   {  // n_valid on the device, before any dlogits
-    const flce_status sl = list_valid_rows(targets, Ni, ignore_index, cblk, cidx, ccount, compact, st);
+    const flce_status sl = topk ? topk_index(*topk, Ni, cblk, compact || N > TOPK_INDEX_ROWS ? cidx : nullptr, ccount, st)
+                                : list_valid_rows(targets, Ni, ignore_index, cblk, cidx, ccount, compact, st);
     if (sl != FLCE_OK) return sl;
   }
   if (compact && dH) {  // the dH GEMM writes the non-ignored rows only
@@ -724,7 +734,7 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
                        dW16 != nullptr};
   // loss block sums: a segment per row block
   const long long per = ceil_div(fp.R, topk ? TOPK_ROWS : SMALL_THREADS);
-  {  // the last block's segment may be shorter than the others: zero it whole
+  if (!topk) {  // the last block's segment may be shorter than the others: zero it whole
     const long long last = (ceil_div(N, fp.R) - 1) * per;
     FLCE_CUDA_TRY(cudaMemsetAsync(bsum + last, 0, per * 8, st));
     FLCE_CUDA_TRY(cudaMemsetAsync(bcnt + last, 0, per * 8, st));
@@ -796,7 +806,11 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
         FLCE_CUDA_TRY(cudaGetLastError());
       }
     }
-    {  // (3) exponentials -> dlogits, in place
+    if (topk) {  // (3) exponentials -> dlogits, in place
+      s = topk_dlogits(*topk, kLong, p, E, mx, static_cast<int>(row0), rows, compact ? cidx + row0 : nullptr, ccount,
+                       st);
+      if (s != FLCE_OK) return s;
+    } else {
       ProfScope ps(K_DLOGITS, st);
       const dim3 grid(static_cast<unsigned>(ceil_div(fp.ldD, SMALL_THREADS * FUSED_COLS_PER_THREAD)),
                       static_cast<unsigned>(rows));
@@ -804,18 +818,12 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
       if (kLong)
         fused_dlogits_kernel<true><<<grid, SMALL_THREADS, 0, st>>>(
             E, mx, static_cast<int>(fp.ldD), static_cast<int>(V), static_cast<int>(row0), ri, targets,
-            dl_weights, dl_lse, zt, ignore_index, ccount, grad_scale, tfp.tf_softcap, tfp.tf_a, tfp.tf_b, tfp.tf_d);
+            dl_weights, lse, zt, ignore_index, ccount, grad_scale, tfp.tf_softcap, tfp.tf_a, tfp.tf_b, tfp.tf_d);
       else
         fused_dlogits_kernel<false><<<grid, SMALL_THREADS, 0, st>>>(
             E, mx, static_cast<int>(fp.ldD), static_cast<int>(V), static_cast<int>(row0), ri, targets,
-            dl_weights, dl_lse, zt, ignore_index, ccount, grad_scale, tfp.tf_softcap, tfp.tf_a, tfp.tf_b, tfp.tf_d);
+            dl_weights, lse, zt, ignore_index, ccount, grad_scale, tfp.tf_softcap, tfp.tf_a, tfp.tf_b, tfp.tf_d);
       FLCE_CUDA_TRY(cudaGetLastError());
-    }
-    if (topk) {
-      s = topk_scatter(*topk, kLong, p, E, 0, static_cast<int>(V), static_cast<int>(row0), rows,
-                       compact ? cidx : nullptr, compact ? ccount : nullptr, static_cast<int>(row0), nullptr, ccount,
-                       st);
-      if (s != FLCE_OK) return s;
     }
     // (4) dH[rows] = D W, dW (+)= D^T h[rows]; compacted: the block's
     // non-ignored rows, min(n_valid - row0, rows) read on the device
@@ -830,8 +838,9 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
     if (s != FLCE_OK) return s;
   }
   // every segment entry was written: full blocks fill theirs, and the last
-  // block's unused entries were zeroed before the loop
-  return loss_sums(out_loss, out_n_valid, bsum, bcnt, ceil_div(N, fp.R) * per, st);
+  // block's unused entries were zeroed before the loop (a list's row blocks
+  // are whole multiples of a segment entry's rows: its entries run through)
+  return loss_sums(out_loss, out_n_valid, bsum, bcnt, topk ? ceil_div(N, TOPK_ROWS) : ceil_div(N, fp.R) * per, st);
 }
 
 flce_status flce_forward_backward(const flce_bf16* h, const flce_bf16* W, const int64_t* targets,

@@ -590,6 +590,7 @@ struct TopkCall {
   float* out_lse = nullptr;
   double* bsum = nullptr;  // block sums of the row kernel
   long long* bcnt = nullptr;
+  float2* gemv = nullptr;  // [CTAs][N] partials of the few-row forward
   flce_bf16* dW16 = nullptr;  // dW in bf16 straight from the GEMM (one row block), instead of dW
 };
 
@@ -622,16 +623,70 @@ flce_status topk_rows(const TopkCall& c, bool kLong, const FwdPlan& f, const Gem
   return FLCE_OK;
 }
 
+// CTAs of the few-row forward: two per SM, fewer where the vocabulary runs out.
+constexpr size_t kGemvMaxSmem = 98304;  // h in shared memory, two CTAs to an SM
+int topk_gemv_ctas(long long V) {
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(ceil_div(V, 4 * TOPK_GEMV_WARPS), 2LL * device_sms())));
+}
+// Whether a forward of N rows runs it.
+bool topk_gemv_for(long long N, long long H) {
+  const long long nr = N <= 1 ? 1 : N <= 2 ? 2 : 4;
+  return N >= 1 && N <= TOPK_GEMV_ROWS && static_cast<size_t>(nr) * H * 4 <= kGemvMaxSmem;
+}
+flce_status topk_gemv(const TopkCall& c, const GemmParams& p, const flce_bf16* h, const flce_bf16* W, float2* part,
+                      cudaStream_t st) {
+  ProfScope ps(K_FWD, st);
+  auto go = [&](auto kern, int nr) -> cudaError_t {
+    const size_t smem = static_cast<size_t>(nr) * p.H * 4;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGemvMaxSmem));
+    if (e != cudaSuccess) return e;
+    kern<<<topk_gemv_ctas(p.V), 32 * TOPK_GEMV_WARPS, smem, st>>>(h, W, p.N, p.H, p.V, c.K, c.rows, p.tf_softcap,
+                                                                 p.tf_a, p.tf_b, part);
+    return cudaGetLastError();
+  };
+  FLCE_CUDA_TRY(p.N == 1 ? go(topk_gemv_kernel<1>, 1) : p.N == 2 ? go(topk_gemv_kernel<2>, 2) : go(topk_gemv_kernel<4>, 4));
+  return FLCE_OK;
+}
+
+// The dlogits of one row block of the one-call step, listed columns included.
+flce_status topk_dlogits(const TopkCall& c, bool kLong, const GemmParams& p, uint16_t* E, const float* mx, int row0,
+                         int rows, const int* ri, const int* n_valid, cudaStream_t st) {
+  ProfScope ps(K_DLOGITS, st);
+  const dim3 grid(static_cast<unsigned>(ceil_div(p.ldD, TOPK_DL_COLS)), static_cast<unsigned>(rows));
+  auto go = [&](auto kern) {
+    kern<<<grid, SMALL_THREADS, 0, st>>>(E, mx, p.ldD, row0, ri, c.rows, c.K, n_valid, p.grad_scale, p.tf_softcap,
+                                         p.tf_a, p.tf_b, p.tf_d);
+  };
+  if (kLong)
+    go(topk_dlogits_kernel<true>);
+  else
+    go(topk_dlogits_kernel<false>);
+  FLCE_CUDA_TRY(cudaGetLastError());
+  return FLCE_OK;
+}
+
+// The counted rows' number, and with idx a permutation that puts them first.
+flce_status topk_index(const TopkCall& c, int N, int* blk, int* idx, int* count, cudaStream_t st) {
+  // one CTA up to 32,768 rows: two launches fewer to wait for than the listing over many
+  if (N > TOPK_INDEX_ROWS)
+    return list_valid_rows(reinterpret_cast<const int64_t*>(c.rows.mark), N, kMarkIgnored, blk, idx, count,
+                           true, st);
+  ProfScope ps(K_COMPACT, st);
+  topk_index_kernel<<<1, 1024, 0, st>>>(c.rows.mark, N, idx, count);
+  FLCE_CUDA_TRY(cudaGetLastError());
+  return FLCE_OK;
+}
+
 // The listed columns of the dlogits block D (local columns of slab v0).
 flce_status topk_scatter(const TopkCall& c, bool kLong, const GemmParams& p, uint16_t* D, int v0, int width, int row0,
                          int rows, const int* ri, const int* dyn_count, int first, const long long* count,
-                         const int* count32, cudaStream_t st) {
+                         cudaStream_t st) {
   ProfScope ps(K_TOPK, st);
   const unsigned grid = static_cast<unsigned>(std::max<long long>(
       1, std::min<long long>(ceil_div(static_cast<long long>(rows) * c.K, SMALL_THREADS), 8LL * device_sms())));
   auto go = [&](auto kern) {
     kern<<<grid, SMALL_THREADS, 0, st>>>(D, p.ldD, v0, width, row0, rows, ri, dyn_count, first, c.K, c.rows.ids,
-                                         c.rows.val, p.grad_scale, count, count32, p.scale_dev);
+                                         c.rows.val, p.grad_scale, count, p.scale_dev);
   };
   if (kLong)
     go(topk_scatter_kernel<true>);

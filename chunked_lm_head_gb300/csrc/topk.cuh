@@ -19,6 +19,7 @@
 #include <climits>
 #include <cstdint>
 
+#include "norm.cuh"
 #include "small_kernels.cuh"
 
 namespace flce {
@@ -149,6 +150,119 @@ __global__ void __launch_bounds__(32 * TOPK_WARPS)
   }
 }
 
+// The forward of a few rows (at most TOPK_GEMV_ROWS): with so few, a 256-row
+// tensor-core tile is nearly empty and the work is reading W once, so warps
+// read it straight into fp32 multiply-adds.  A warp takes 4 vocabulary rows at
+// a time (a row of h, in shared memory as fp32, is read once for the four) and
+// 8 elements of each per lane and step; after the warp's sums, lane 4 r + c
+// keeps row r's online maximum and sum over the c-th of the 4, and walks r's
+// list, whose ids ascend with the warp's vocabulary rows.  One partial per CTA
+// and row.
+constexpr int TOPK_GEMV_ROWS = 4;
+constexpr int TOPK_GEMV_WARPS = 8;
+
+__device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <int NR>
+__global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS)
+    topk_gemv_kernel(const uint16_t* __restrict__ h, const uint16_t* __restrict__ W, int N, int H, int V, int K,
+                     const TopkRows rows, int tf_softcap, float tf_a, float tf_b, float2* __restrict__ part) {
+  extern __shared__ float4 gemv_h[];  // [NR][H / 4]
+  __shared__ float2 merged[TOPK_GEMV_WARPS][32];
+  float* hs = reinterpret_cast<float*>(gemv_h);
+  for (int e = threadIdx.x; e < NR * (H / 2); e += blockDim.x) {
+    const int r = e / (H / 2), c = (e - r * (H / 2)) * 2;
+    const uint32_t u = r < N ? *reinterpret_cast<const uint32_t*>(h + static_cast<long long>(r) * H + c) : 0u;
+    hs[r * H + c] = __uint_as_float(u << 16);
+    hs[r * H + c + 1] = __uint_as_float(u & 0xffff0000u);
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int my_r = lane >> 2, my_c = lane & 3;  // this lane's row and place among the 4
+  const bool mine = my_r < NR && my_r < N;
+  const int* ids = rows.ids + static_cast<long long>(mine ? my_r : 0) * K;
+  float* val = rows.val + static_cast<long long>(mine ? my_r : 0) * K;
+  int at = 0;
+  float m = -INFINITY, s = 0.f;
+  const int warps = gridDim.x * TOPK_GEMV_WARPS;
+  const int groups = (V + 3) / 4;
+  for (int g = blockIdx.x * TOPK_GEMV_WARPS + warp; g < groups; g += warps) {
+    const int v0 = 4 * g;
+    float acc[NR][4];
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+    const uint16_t* w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[c] = W + static_cast<long long>(min(v0 + c, V - 1)) * H + lane * 8;
+#pragma unroll 2
+    for (int k = lane * 8; k < H; k += 256) {
+      uint4 q[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        q[c] = ld_stream(w[c]);
+        w[c] += 256;
+      }
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float x[8];
+        load8(hs + r * H + k, x);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t u[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[r][c] = fmaf(__uint_as_float(u[e] << 16), x[2 * e], acc[r][c]);
+            acc[r][c] = fmaf(__uint_as_float(u[e] & 0xffff0000u), x[2 * e + 1], acc[r][c]);
+          }
+        }
+      }
+    }
+    float z = 0.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float a = acc[r][c];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+        if (lane == 4 * r + c) z = a;
+      }
+    const int v = v0 + my_c;
+    if (mine && v < V) {
+      const float u = tf_softcap ? tf_b * tanhf(tf_a * z) : tf_a * z;
+      while (at < K && ids[at] < v) ++at;
+      if (at < K && ids[at] == v) {
+        for (; at < K && ids[at] == v; ++at) val[at] = u;
+      } else {
+        const float u2 = u * kLog2e, nm = fmaxf(m, u2);
+        if (nm > -INFINITY) {
+          s = s * exp2f(m - nm) + exp2f(u2 - nm);
+          m = nm;
+        }
+      }
+    }
+  }
+  merged[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp == 0 && my_c == 0 && mine) {
+    float M = -INFINITY, S = 0.f;
+    for (int i = 0; i < TOPK_GEMV_WARPS; ++i)
+      for (int c = 0; c < 4; ++c) M = fmaxf(M, merged[i][lane + c].x);
+    if (M > -INFINITY)
+      for (int i = 0; i < TOPK_GEMV_WARPS; ++i)
+        for (int c = 0; c < 4; ++c) S += merged[i][lane + c].y * exp2f(merged[i][lane + c].x - M);
+    part[static_cast<long long>(blockIdx.x) * N + my_r] = make_float2(M, S);
+  }
+}
+
 // Rows of a launch: row0 + j, or ri[j] where ri is given.
 //   part [S][stride]: the forward's (max x log2 e, sum) over the columns that
 //   are not listed.  Writes kl, lse, the coefficients of the backward
@@ -239,6 +353,115 @@ __global__ void __launch_bounds__(SMALL_THREADS)
   block_sum_store(contrib, cnt, blk_sum, blk_cnt);
 }
 
+// dlogits of one row block of the one-call step, in place: the forward's
+// exponentials E = 2^(u log2 e - chunk max) (0 in the listed columns and past
+// the vocabulary) become
+//   D = E 2^(chunk max - lse_rest) coef g f'(z),  g = grad_scale / max(n_valid, 1),
+// then the listed columns get theirs.  A CTA takes TOPK_DL_COLS columns of a
+// row (blockIdx.y), a lane 8 neighbouring columns per step, so that a warp's
+// 16-byte accesses are contiguous.  Rows as fused_dlogits_kernel.
+constexpr int TOPK_DL_COLS = SMALL_THREADS * 32;
+
+template <bool kLong>
+__global__ void __launch_bounds__(SMALL_THREADS)
+    topk_dlogits_kernel(uint16_t* __restrict__ E, const float* __restrict__ mx, int ldD, int row0,
+                        const int* __restrict__ ri, const TopkRows rows, int K, const int* __restrict__ n_valid,
+                        float grad_scale, int tf_softcap, float tf_a, float tf_b, float tf_d) {
+  using idx_t = typename std::conditional<kLong, long long, int>::type;
+  const int r = blockIdx.y;
+  const int n = *n_valid;
+  if (ri != nullptr && r >= (n - row0 + 63) / 64 * 64) return;  // row0: the block's first position
+  const long long i = ri ? ri[r] : row0 + r;
+  const float g = grad_scale / fmaxf(1.f, static_cast<float>(n));
+  const bool live = rows.mark[i] >= 0;
+  const float scale = live ? rows.coef[i] * g : 0.f;
+  uint16_t* row = E + static_cast<idx_t>(r) * ldD;
+  const float* rmx = mx + static_cast<idx_t>(r) * (ldD / 32);
+  const int c0 = blockIdx.x * TOPK_DL_COLS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float nlse2 = -rows.lse_rest[i] * kLog2e;
+  uint4 q[4];
+  float base[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = c0 + warp * 1024 + k * 256 + lane * 8;
+    q[k] = make_uint4(0u, 0u, 0u, 0u);
+    base[k] = 0.f;
+    if (c < ldD && scale != 0.f) {
+      q[k] = *reinterpret_cast<const uint4*>(row + c);
+      base[k] = rmx[c / 32];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = c0 + warp * 1024 + k * 256 + lane * 8;
+    if (c >= ldD) continue;
+    uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+    if (scale != 0.f) {  // else zeros: a row without loss or weight, whose exponentials may never have been written
+      const float kf = ex2_approx(base[k] + nlse2) * scale;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
+        if (!tf_softcap) {
+          lo *= kf * tf_a;
+          hi *= kf * tf_a;
+        } else {  // u = ln(E) + chunk max, tanh(a z) = u / b
+          const float ul = (__log2f(lo) + base[k]) * kLn2 / tf_b, uh = (__log2f(hi) + base[k]) * kLn2 / tf_b;
+          lo = lo > 0.f ? lo * kf * tf_d * (1.f - ul * ul) : 0.f;
+          hi = hi > 0.f ? hi * kf * tf_d * (1.f - uh * uh) : 0.f;
+        }
+        w[e] = pack_bf16x2(lo, hi);
+      }
+    }
+    *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (!live) return;  // (the whole CTA)
+  __syncthreads();  // the listed columns after the CTA's own stores
+  for (int j = threadIdx.x; j < K; j += SMALL_THREADS) {
+    const int id = rows.ids[i * K + j];
+    if (id >= c0 && id - c0 < TOPK_DL_COLS && id != INT_MAX)
+      row[id] = static_cast<uint16_t>(pack_bf16x2(rows.val[i * K + j] * g, 0.f) & 0xffffu);
+  }
+}
+
+// The counted rows of up to TOPK_INDEX_ROWS rows in one CTA: their number,
+// and (idx given) a permutation with them first, each part in row order.
+constexpr int TOPK_INDEX_ROWS = 32768;
+__global__ void __launch_bounds__(1024)
+    topk_index_kernel(const long long* __restrict__ mark, int N, int* __restrict__ idx, int* __restrict__ total) {
+  __shared__ int wsum[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int live = 0;  // of all rows
+  for (int i = threadIdx.x; i < N; i += 1024) live += mark[i] >= 0 ? 1 : 0;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) live += __shfl_xor_sync(0xffffffffu, live, off);
+  if (lane == 0) wsum[warp] = live;
+  __syncthreads();
+  int all = 0;
+  for (int w = 0; w < 32; ++w) all += wsum[w];
+  if (threadIdx.x == 0) *total = all;
+  if (idx == nullptr) return;
+  int before = 0;  // counted rows of the tiles before this one
+  for (int t0 = 0; t0 < N; t0 += 1024) {
+    const int i = t0 + threadIdx.x;
+    const bool keep = i < N && mark[i] >= 0;
+    const unsigned ballot = __ballot_sync(0xffffffffu, keep);
+    __syncthreads();  // the last tile's sums have been read
+    if (lane == 0) wsum[warp] = __popc(ballot);
+    __syncthreads();
+    int pos = before + __popc(ballot & ((1u << lane) - 1u)), tile = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) pos += wsum[w];
+      tile += wsum[w];
+    }
+    if (keep)
+      idx[pos] = i;
+    else if (i < N)
+      idx[all + i - pos] = i;
+    before += tile;
+  }
+}
+
 // The listed columns of a dlogits block: D[r][id - v0] = val * scale, bf16,
 // for the ids inside [v0, v0 + width).  Local row r is row row0 + r, or
 // ri[first + r]; rows past the device-side count are left alone.
@@ -246,13 +469,11 @@ template <bool kLong>
 __global__ void topk_scatter_kernel(uint16_t* __restrict__ D, int ldD, int v0, int width, int row0, int rows,
                                     const int* __restrict__ ri, const int* __restrict__ dyn_count, int first, int K,
                                     const int* __restrict__ ids, const float* __restrict__ val, float grad_scale,
-                                    const long long* __restrict__ count, const int* __restrict__ count32,
-                                    const float* __restrict__ scale_dev) {
+                                    const long long* __restrict__ count, const float* __restrict__ scale_dev) {
   using idx_t = typename std::conditional<kLong, long long, int>::type;
   if (dyn_count != nullptr) rows = max(0, min(*dyn_count - first, rows));
   float g = grad_scale;
   if (count != nullptr) g *= 1.f / fmaxf(1.f, static_cast<float>(*count));
-  if (count32 != nullptr) g /= fmaxf(1.f, static_cast<float>(*count32));
   if (scale_dev != nullptr) g *= *scale_dev;
   const long long total = static_cast<long long>(rows) * K;
   for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < total;

@@ -18,7 +18,7 @@ bool topk_teacher_ok(const flce_top_logits* t) {
 // the backward reads, laid out alike in a caller's state buffer.
 struct TopkLayout {
   size_t ids = 0, val = 0, mark = 0, lse_rest = 0, coef = 0, state = 0;
-  size_t mass = 0, stat = 0, bsum = 0, bcnt = 0, nv = 0, total = 0;
+  size_t mass = 0, stat = 0, bsum = 0, bcnt = 0, gemv = 0, total = 0;
 };
 TopkLayout topk_layout(int64_t N, int64_t K) {
   TopkLayout L;
@@ -42,7 +42,7 @@ TopkLayout topk_layout(int64_t N, int64_t K) {
   const size_t blocks = (2 * n + 256) / TOPK_ROWS + 1;
   L.bsum = take(blocks * 8);
   L.bcnt = take(blocks * 8);
-  L.nv = take(8);
+  L.gemv = take(n <= TOPK_GEMV_ROWS ? static_cast<size_t>(2 * device_sms()) * n * 8 : 0);
   L.total = o;
   return L;
 }
@@ -174,6 +174,7 @@ flce_status flce_topk_kd_forward(const flce_bf16* h, const flce_bf16* W, const f
   c.out_lse = out_lse;
   c.bsum = reinterpret_cast<double*>(wb + inner + L.bsum);
   c.bcnt = reinterpret_cast<long long*>(wb + inner + L.bcnt);
+  c.gemv = reinterpret_cast<float2*>(wb + inner + L.gemv);
   s = topk_lists(teacher, targets, ignore_index, N, V, c.rows, st);
   if (s != FLCE_OK) return s;
   const bool skip = (flags & FLCE_FORWARD_SKIP_IGNORED) != 0 && compact_on() && N >= skip_min_rows();
@@ -251,6 +252,7 @@ flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W
   c.out_lse = out_lse;
   c.bsum = reinterpret_cast<double*>(wb + inner + L.bsum);
   c.bcnt = reinterpret_cast<long long*>(wb + inner + L.bcnt);
+  c.gemv = reinterpret_cast<float2*>(wb + inner + L.gemv);
   s = topk_lists(teacher, targets, ignore_index, N, V, c.rows, st);
   if (s != FLCE_OK) return s;
   s = forward_backward_impl(h, W, reinterpret_cast<const int64_t*>(c.rows.mark), nullptr, N, H, V, chunk_rows,

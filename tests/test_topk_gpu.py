@@ -121,6 +121,23 @@ def test_every_tiling_gives_the_definition(options):
     R.check({k: out[k] for k in ("kl", "loss", "n_valid")}, ref, what="skip")
 
 
+@pytest.mark.parametrize("N", [1, 2, 3, 4])
+@pytest.mark.parametrize("H,V,K", [(8, 3, 3), (264, 1001, 5), (1000, 2500, 64), (4096, 5000, 16), (24576, 300, 7)])
+def test_a_few_rows(N, H, V, K):
+    """The forward of up to 4 rows reads W by warps instead of tiles (but for
+    rows too long for its shared memory)."""
+    tf = {"softcap": 6.0, "temperature": 0.9} if V % 2 else None
+    c = make(N, H, V, K, seed=16, std=1.2 / H ** 0.5, pad=N > 2 and V > 5, whole=True, weights=True)
+    c["ids"][0, 0] = c["ids"][0, 1]  # listed twice
+    for tail in (False, True):
+        ref = R.reference(**c, tail=tail, tf=tf)
+        out = flce.topk_kd_forward(c["h"], c["W"], c["ids"], c["logits"], c["lse_t"], None, c["weights"], tail,
+                                   transform=tf, for_backward=True)
+        dH, dW = flce.topk_kd_backward(c["h"], c["W"], out["state"], K, 1.0, transform=tf, count=out["n_valid"])
+        R.check(dict(out, dH=dH, dW=dW), ref)
+    assert _lib.flce_device_status() == 0
+
+
 def test_several_row_blocks_of_the_one_call_step():
     c = make(5000, 64, 700, 9, seed=5, mask=True, whole=True)
     run_all(c, tail=True, one_call_chunk=2048)
