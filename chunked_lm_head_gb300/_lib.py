@@ -119,6 +119,7 @@ SIGNATURES = {
                                               _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
     "flce_rms_norm_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64]),
     "flce_scale_grads": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp]),
+    "flce_scale_grads_bf16": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp]),
     "flce_set_option": (ctypes.c_int, [ctypes.c_int, _c_i64]),
     "flce_get_option": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_int64)]),
     "flce_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -359,6 +360,11 @@ def flce_jsd_backward_ex2(h_s, W_s, H_s, h_t, W_t, H_t, targets, weights, lse_s,
 def flce_scale_grads(dH, n_dH, dW, n_dW, scale, stream=None) -> int:
     """Raw C call: dH, dW *= *scale in place (scale a [1] fp32 device tensor)."""
     return load().flce_scale_grads(_ptr(dH), n_dH, _ptr(dW), n_dW, _ptr(scale), _stream_handle(stream))
+
+
+def flce_scale_grads_bf16(dH, n_dH, dW, n_dW, scale, stream=None) -> int:
+    """Raw C call: bf16 dH, dW *= *scale in place, in one launch."""
+    return load().flce_scale_grads_bf16(_ptr(dH), n_dH, _ptr(dW), n_dW, _ptr(scale), _stream_handle(stream))
 
 
 def flce_kd_forward(h_s, W_s, H_s, h_t, W_t, H_t, targets, weights, N, V, chunk_rows, ignore_index,

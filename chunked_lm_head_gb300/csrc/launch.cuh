@@ -626,7 +626,7 @@ flce_status topk_rows(const TopkCall& c, bool kLong, const FwdPlan& f, const Gem
 // CTAs of the few-row forward: two per SM, fewer where the vocabulary runs out.
 constexpr size_t kGemvMaxSmem = 98304;  // h in shared memory, two CTAs to an SM
 int topk_gemv_ctas(long long V) {
-  return static_cast<int>(std::max<long long>(1, std::min<long long>(ceil_div(V, 4 * TOPK_GEMV_WARPS), 2LL * device_sms())));
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(ceil_div(V, 4 * TOPK_GEMV_WARPS), static_cast<long long>(TOPK_GEMV_CTAS) * device_sms())));
 }
 // Whether a forward of N rows runs it.
 bool topk_gemv_for(long long N, long long H) {

@@ -582,6 +582,29 @@ __global__ void round_bf16_kernel(const float* __restrict__ x, long long n, uint
   }
 }
 
+// The same for two bf16 arrays in one launch.
+__global__ void scale_bf16_pair_kernel(__nv_bfloat16* __restrict__ x, long long nx, __nv_bfloat16* __restrict__ y,
+                                       long long ny, const float* __restrict__ scale) {
+  const float s = *scale;
+  if (s == 1.f) return;
+  const long long vx = nx / 8, vy = ny / 8;
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  const long long t = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x;
+  for (long long i = t; i < vx + vy; i += stride) {
+    uint4* p = i < vx ? reinterpret_cast<uint4*>(x) + i : reinterpret_cast<uint4*>(y) + (i - vx);
+    uint4 u = *p;
+    __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __bfloat1622float2(b[j]);
+      b[j] = __floats2bfloat162_rn(f.x * s, f.y * s);
+    }
+    *p = u;
+  }
+  for (long long i = vx * 8 + t; i < nx; i += stride) x[i] = __float2bfloat16_rn(__bfloat162float(x[i]) * s);
+  for (long long i = vy * 8 + t; i < ny; i += stride) y[i] = __float2bfloat16_rn(__bfloat162float(y[i]) * s);
+}
+
 __global__ void scale_f32_kernel(float* __restrict__ x, long long n, const float* __restrict__ scale) {
   const float s = *scale;
   if (s == 1.f) return;

@@ -10,7 +10,9 @@
 //            = (M R - T) e^(u_v - lse_rest)     v not in S
 // The listed columns never enter the GEMM's sum, so R keeps its precision
 // when the listed ids hold nearly all of the student's mass, and no division
-// by it is needed.  The few sums over K are taken in 64 bits.
+// by it is needed.  All in fp32 (64-bit arithmetic took 10 us of latency per
+// row): every term of kl is small where the two distributions are near, and
+// logits are taken relative to the row's largest.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,6 +30,9 @@ constexpr int TOPK_WARPS = 4;      // rows per CTA of the list kernel, one warp 
 constexpr int TOPK_MAX_K = 1024;   // longest list (its shared memory: 8 bytes per entry and row)
 constexpr int TOPK_ROWS = SMALL_THREADS / 32;  // rows per CTA of the row kernel
 
+// ln 2 - kLn2
+constexpr float kLn2Low = static_cast<float>(0.69314718055994530942 - static_cast<double>(kLn2));
+
 struct TopkTeacher {
   const void* ids;     // int32 or int64 [N][ld_ids]
   const void* logits;  // fp32, bf16 or fp16 [N][ld_logits]
@@ -42,13 +47,13 @@ struct TopkRows {
   int* ids;          // [N][K] ascending, INT_MAX where there is no entry
   float* mass;       // [N][K] teacher mass of the id (of all its entries)
   float* val;        // [N][K] the student's u_k, then the gradient of its column
-  double2* stat;     // [N] sum p log p (NaN: an id outside the vocabulary), P
+  float2* stat;      // [N] P (NaN: an id outside the vocabulary), T = max(0, 1 - P)
   long long* mark;   // [N] V for a counted row, -1 for one without loss
   float* lse_rest;   // [N]
   float* coef;       // [N] w (M R - T)
 };
 
-__device__ __forceinline__ double warp_sum(double x) {
+__device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
   return x;
@@ -66,10 +71,18 @@ __device__ __forceinline__ float topk_logit(const TopkTeacher& t, long long row,
   return static_cast<const float*>(t.logits)[o];
 }
 
-// The row's list in ascending order of id with the teacher's masses (one warp
-// per row).  An entry's place is the number of entries before it (by id, then
-// by position), counted in one walk over the list that also adds up the mass
-// of equal ids: K^2 / 32 steps of a lane, no barrier.
+// x + y as a rounded sum and what the rounding left out.
+__device__ __forceinline__ float2 two_sum(float x, float y) {
+  const float s = x + y, b = s - x;
+  return make_float2(s, (x - (s - b)) + (y - b));
+}
+
+// The row's list in ascending order of id with the teacher's masses and their
+// logarithms (one warp per row).  An entry's place is the number of entries
+// before it (by id, then by position), counted in one walk over the list that
+// also adds up the mass of equal ids: K^2 / 32 steps of a lane, no barrier.
+// t - lse carries what its rounding leaves out; with the tail the masses and
+// their sum are taken in 64 bits, since T = 1 - P is small where they are not.
 __global__ void __launch_bounds__(32 * TOPK_WARPS)
     topk_list_kernel(const TopkTeacher t, const int64_t* __restrict__ targets, long long ignore, int N, int V,
                      const TopkRows out) {
@@ -96,56 +109,57 @@ __global__ void __launch_bounds__(32 * TOPK_WARPS)
   any = __any_sync(0xffffffffu, any);
   bad = __any_sync(0xffffffffu, bad);
   top = warp_max(top);
-  double lse = 0.0;
   bool live = any || bad;
+  // log p = (u - ref) - logsum: ref the teacher's log-sum-exp, or the list's
+  // largest logit and the logarithm of its exponentials' sum beside it
+  float ref = top, logsum = 0.f;
   if (t.lse != nullptr) {
-    lse = t.lse[i];
+    ref = t.lse[i];
   } else {
     live = live && (top > -INFINITY || bad);  // a list without mass sums to nothing
-    double s = 0.0;
+    float s = 0.f;
     for (int j = lane; j < K; j += 32) s += expf(sp[j] - top);
-    lse = top + log(warp_sum(s));
+    logsum = logf(warp_sum(s));
   }
   live = live && (targets == nullptr || targets[i] != ignore);
-  __syncwarp();
-  // masses in place of the logits; log p = u - lse is needed once more below
-  double own_h = 0.0, P = 0.0;
+  double P = 0.0;
   for (int j = lane; j < K; j += 32) {
-    const double lp = static_cast<double>(sp[j]) - lse;
-    const float p = sid[j] == INT_MAX ? 0.f : expf(static_cast<float>(lp));
-    P += p;
-    if (p > 0.f) own_h += p * lp;
+    float p = 0.f;
+    if (sid[j] != INT_MAX) {
+      if (t.tail) {
+        const double pd = exp(static_cast<double>(sp[j]) - static_cast<double>(ref));
+        P += pd;
+        p = static_cast<float>(pd);
+      } else {
+        const float2 d = two_sum(sp[j], -ref), e = two_sum(d.x, -logsum);
+        // (infinities and NaN make no rest of their own)
+        p = expf(e.x) * (1.f + (e.x - e.x == 0.f ? d.y + e.y : 0.f));
+        P += p;
+      }
+    }
     sp[j] = p;
   }
   __syncwarp();
   int* ids_out = out.ids + i * K;
   float* mass_out = out.mass + i * K;
-  double h_fix = 0.0;  // sum p log p of ids listed more than once, instead of their entries' own
   for (int j = lane; j < K; j += 32) {
     const int id = sid[j];
-    int place = 0, same = 0;
+    int place = 0;
     float m = 0.f;
-    bool first = true;
+#pragma unroll 4
     for (int q = 0; q < K; ++q) {
       const int o = sid[q];
       place += (o < id || (o == id && q < j)) ? 1 : 0;
-      if (o == id) {
-        m += sp[q];
-        ++same;
-        if (q < j) first = false;
-      }
-    }
-    if (same > 1 && id != INT_MAX) {
-      if (sp[j] > 0.f) h_fix -= static_cast<double>(sp[j]) * log(static_cast<double>(sp[j]));
-      if (first && m > 0.f) h_fix += static_cast<double>(m) * log(static_cast<double>(m));
+      m += o == id ? sp[q] : 0.f;
     }
     ids_out[place] = live ? id : INT_MAX;
     mass_out[place] = live && id != INT_MAX ? m : 0.f;
   }
-  const double h = warp_sum(own_h + h_fix);
-  P = warp_sum(P);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) P += __shfl_xor_sync(0xffffffffu, P, off);
   if (lane == 0) {
-    out.stat[i] = make_double2(bad ? static_cast<double>(__int_as_float(0x7fc00000)) : h, P);
+    out.stat[i] = make_float2(bad ? __int_as_float(0x7fc00000) : static_cast<float>(P),
+                              static_cast<float>(fmax(0.0, 1.0 - P)));
     out.mark[i] = live ? V : -1;
   }
 }
@@ -158,8 +172,14 @@ __global__ void __launch_bounds__(32 * TOPK_WARPS)
 // keeps row r's online maximum and sum over the c-th of the 4, and walks r's
 // list, whose ids ascend with the warp's vocabulary rows.  One partial per CTA
 // and row.
+// Bound by the read of W: 151,936 x 4,096 takes 179, 185 and 217 us for 1, 2
+// and 4 rows (7.0, 6.7 and 5.7 TB/s), where the tiled forward took 279, 260
+// and 230 (few rows of h are few lines of L2, which every SM then asks for at
+// once; 16 rows take it 194).  Two CTAs to an SM with 8 loads of 16 bytes in
+// flight per lane; 4 loads and 2 CTAs 207 us, 4 loads and 4 CTAs 184.
 constexpr int TOPK_GEMV_ROWS = 4;
 constexpr int TOPK_GEMV_WARPS = 8;
+constexpr int TOPK_GEMV_CTAS = 2;
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
   uint4 v;
@@ -169,8 +189,18 @@ __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
   return v;
 }
 
+// a b + c on two fp32 at a time
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return d;
+}
+
 template <int NR>
-__global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS)
+__global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS, TOPK_GEMV_CTAS)
     topk_gemv_kernel(const uint16_t* __restrict__ h, const uint16_t* __restrict__ W, int N, int H, int V, int K,
                      const TopkRows rows, int tf_softcap, float tf_a, float tf_b, float2* __restrict__ part) {
   extern __shared__ float4 gemv_h[];  // [NR][H / 4]
@@ -194,11 +224,11 @@ __global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS)
   const int groups = (V + 3) / 4;
   for (int g = blockIdx.x * TOPK_GEMV_WARPS + warp; g < groups; g += warps) {
     const int v0 = 4 * g;
-    float acc[NR][4];
+    float2 acc[NR][4];  // even and odd elements
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+      for (int c = 0; c < 4; ++c) acc[r][c] = make_float2(0.f, 0.f);
     const uint16_t* w[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) w[c] = W + static_cast<long long>(min(v0 + c, V - 1)) * H + lane * 8;
@@ -218,10 +248,9 @@ __global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS)
         for (int c = 0; c < 4; ++c) {
           const uint32_t u[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[r][c] = fmaf(__uint_as_float(u[e] << 16), x[2 * e], acc[r][c]);
-            acc[r][c] = fmaf(__uint_as_float(u[e] & 0xffff0000u), x[2 * e + 1], acc[r][c]);
-          }
+          for (int e = 0; e < 4; ++e)
+            acc[r][c] = fma2(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)),
+                             make_float2(x[2 * e], x[2 * e + 1]), acc[r][c]);
         }
       }
     }
@@ -230,7 +259,7 @@ __global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS)
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float a = acc[r][c];
+        float a = acc[r][c].x + acc[r][c].y;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
         if (lane == 4 * r + c) z = a;
@@ -293,59 +322,68 @@ __global__ void __launch_bounds__(SMALL_THREADS)
         out.coef[i] = 0.f;
       }
     } else {
-      // the columns that are not listed
+      // the columns that are not listed: log2 maximum m2 and sum of 2^(. - m2)
       float m2 = -INFINITY;
       for (int s = lane; s < S; s += 32) m2 = fmaxf(m2, part[static_cast<idx_t>(s) * stride + static_cast<idx_t>(i)].x);
       m2 = warp_max(m2);
-      double rest = 0.0;
+      float rest = 0.f;
       if (m2 > -INFINITY)
         for (int s = lane; s < S; s += 32) {
           const float2 q = part[static_cast<idx_t>(s) * stride + static_cast<idx_t>(i)];
           rest += q.y * exp2f(q.x - m2);
         }
       rest = warp_sum(rest);
-      const double rest_top = static_cast<double>(m2) * 0.6931471805599453;  // natural log units
-      // the listed ones, each id once
+      // the listed ones, each id once, relative to the larger of the two maxima
       float mk = -INFINITY;
       for (int j = lane; j < K; j += 32)
         if (ids[j] != INT_MAX) mk = fmaxf(mk, val[j]);
       mk = warp_max(mk);
-      const double A = fmax(rest_top, static_cast<double>(mk));
-      double listed = 0.0;
+      // m2 ln 2 as a rounded product and its rest (ln 2 in two parts)
+      const float2 rt = m2 > -INFINITY ? make_float2(m2 * kLn2, fmaf(m2, kLn2, -(m2 * kLn2)) + m2 * kLn2Low)
+                                       : make_float2(-INFINITY, 0.f);
+      const float A = fmaxf(rt.x, mk);
+      float listed = 0.f;
       for (int j = lane; j < K; j += 32)
-        if (ids[j] != INT_MAX && (j == 0 || ids[j - 1] != ids[j]))
-          listed += expf(static_cast<float>(static_cast<double>(val[j]) - A));
+        if (ids[j] != INT_MAX && (j == 0 || ids[j - 1] != ids[j])) listed += expf(val[j] - A);
       listed = warp_sum(listed);
-      const double rest_A = m2 > -INFINITY ? rest * static_cast<double>(expf(static_cast<float>(rest_top - A))) : 0.0;
-      const double lse = A + log(rest_A + listed);
-      const double lse_rest = rest > 0.0 ? rest_top + log(rest) : static_cast<double>(-INFINITY);
-      const double R = rest > 0.0 ? rest_A / (rest_A + listed) : 0.0;
-      const double2 st = out.stat[i];
-      const double T = tail && rest > 0.0 ? fmax(0.0, 1.0 - st.y) : 0.0;
-      const double M = st.y + T;
+      const float rest_A = rest > 0.f ? rest * expf((rt.x - A) + rt.y) : 0.f;
+      const float total = rest_A + listed;
+      const float logtot = logf(total);
+      const float log_rest = ((rt.x - A) + rt.y) + logf(rest);  // relative to A; -inf where there is no rest
+      const float R = rest > 0.f ? rest_A / total : 0.f;
+      const float2 st = out.stat[i];  // P (NaN: an id outside the vocabulary), T
+      const float T = tail && rest > 0.f ? st.y : 0.f;
       const float w = weights ? weights[i] : 1.f;
-      double cross = 0.0;
+      // P for the gradients: a bad id takes no part in them
+      float P = st.x;
+      if (P != P) {
+        P = 0.f;
+        for (int j = lane; j < K; j += 32)
+          if (ids[j] != INT_MAX && (j == 0 || ids[j - 1] != ids[j])) P += mass[j];
+        P = warp_sum(P);
+      }
+      const float M = P + T;
+      float kl = 0.f;
       for (int j = lane; j < K; j += 32) {
         const int id = ids[j];
         if (id == INT_MAX) continue;
         const float u = val[j], p = mass[j];
-        const double lq = static_cast<double>(u) - lse;
-        if (p > 0.f && (j == 0 || ids[j - 1] != id)) cross += p * lq;
+        const float lq = (u - A) - logtot;
+        if (p > 0.f && (j == 0 || ids[j - 1] != id)) kl = fmaf(p, logf(p) - lq, kl);
         const float fd = tf_softcap ? tf_d * (1.f - (u / tf_b) * (u / tf_b)) : tf_a;
-        val[j] = w * static_cast<float>(M * expf(static_cast<float>(lq)) - p) * fd;
+        val[j] = w * fmaf(M, expf(lq), -p) * fd;
       }
-      cross = warp_sum(cross);
+      kl = warp_sum(kl);
       if (lane == 0) {
-        double kl = st.x - cross;
-        if (T > 0.0) kl += T * (log(T) - (lse_rest - lse));
-        const float klf = live ? static_cast<float>(kl) : 0.f;
-        if (out_kl) out_kl[i] = klf;
-        if (out_lse) out_lse[i] = static_cast<float>(lse);
-        out.lse_rest[i] = static_cast<float>(lse_rest);
-        out.coef[i] = live ? w * static_cast<float>(M * R - T) : 0.f;
+        if (T > 0.f) kl += T * (logf(T) - (log_rest - logtot));
+        if (st.x != st.x) kl = st.x;
+        if (out_kl) out_kl[i] = live ? kl : 0.f;
+        if (out_lse) out_lse[i] = A + logtot;
+        out.lse_rest[i] = A + log_rest;
+        out.coef[i] = live ? w * fmaf(M, R, -T) : 0.f;
         if (live) {
           cnt = 1;
-          contrib = -static_cast<double>(w) * kl;  // the final kernel negates the sum
+          contrib = -static_cast<double>(w) * static_cast<double>(kl);  // the final kernel negates the sum
         }
       }
     }

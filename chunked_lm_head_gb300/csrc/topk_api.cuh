@@ -36,13 +36,13 @@ TopkLayout topk_layout(int64_t N, int64_t K) {
   L.coef = take(n * 4);
   L.state = o;
   L.mass = take(nk * 4);
-  L.stat = take(n * 16);
+  L.stat = take(n * 8);
   // one-call: ceil(N / R) segments of R / TOPK_ROWS block sums, R a multiple of
   // 128 and at most N rounded up to one
   const size_t blocks = (2 * n + 256) / TOPK_ROWS + 1;
   L.bsum = take(blocks * 8);
   L.bcnt = take(blocks * 8);
-  L.gemv = take(n <= TOPK_GEMV_ROWS ? static_cast<size_t>(2 * device_sms()) * n * 8 : 0);
+  L.gemv = take(n <= TOPK_GEMV_ROWS ? static_cast<size_t>(TOPK_GEMV_CTAS * device_sms()) * n * 8 : 0);
   L.total = o;
   return L;
 }
@@ -55,7 +55,7 @@ TopkRows topk_rows_at(const TopkLayout& L, uint8_t* state, uint8_t* scratch) {
   r.lse_rest = reinterpret_cast<float*>(state + L.lse_rest);
   r.coef = reinterpret_cast<float*>(state + L.coef);
   r.mass = reinterpret_cast<float*>(scratch + L.mass);
-  r.stat = reinterpret_cast<double2*>(scratch + L.stat);
+  r.stat = reinterpret_cast<float2*>(scratch + L.stat);
   return r;
 }
 
@@ -118,6 +118,19 @@ flce_status topk_round_dw(const float* x, int64_t n, void* dW, cudaStream_t st) 
 }  // namespace
 
 extern "C" {
+
+flce_status flce_scale_grads_bf16(flce_bf16* dH, int64_t n_dH, flce_bf16* dW, int64_t n_dW, const float* scale,
+                                  void* stream) {
+  if (n_dH < 0 || n_dW < 0 || scale == nullptr || (n_dH > 0 && dH == nullptr) || (n_dW > 0 && dW == nullptr))
+    return FLCE_ERR_INVALID_ARG;
+  if (!aligned(dH, 16) || !aligned(dW, 16) || !aligned(scale, 4)) return FLCE_ERR_UNSUPPORTED;
+  if (n_dH + n_dW == 0) return FLCE_OK;
+  const long long blocks = std::min<long long>(8LL * device_sms(), ceil_div(n_dH + n_dW, 8LL * SMALL_THREADS));
+  scale_bf16_pair_kernel<<<static_cast<unsigned>(blocks), SMALL_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
+      reinterpret_cast<__nv_bfloat16*>(dH), n_dH, reinterpret_cast<__nv_bfloat16*>(dW), n_dW, scale);
+  FLCE_CUDA_TRY(cudaGetLastError());
+  return FLCE_OK;
+}
 
 size_t flce_topk_kd_state_bytes(int64_t N, int64_t k) {
   if (N < 0 || N >= INT_MAX || k < 1 || k > TOPK_MAX_K) return 0;

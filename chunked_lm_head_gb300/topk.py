@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import IGNORE_INDEX, _device_scalar, scale_grads
+from .api import IGNORE_INDEX, _device_scalar
 
 _IDS = {torch.int32: _lib.DTYPES["i32"], torch.int64: _lib.DTYPES["i64"]}
 _LOGITS = {torch.float32: _lib.DTYPES["f32"], torch.bfloat16: _lib.DTYPES["bf16"], torch.float16: _lib.DTYPES["f16"]}
@@ -179,9 +179,11 @@ class TopkDistillOneCall(torch.autograd.Function):
             raise RuntimeError("the one-call loss can be differentiated once: its gradients are scaled in place")
         dH, dW = ctx.grads
         ctx.grads = None
-        for d in (dH, dW):  # both bf16
-            if d is not None:
-                scale_grads(d, None, grad_loss)
+        if dH is not None or dW is not None:
+            if grad_loss.dtype != torch.float32:
+                grad_loss = grad_loss.float()
+            _lib.check("flce_scale_grads_bf16", _lib.flce_scale_grads_bf16(
+                dH, 0 if dH is None else dH.numel(), dW, 0 if dW is None else dW.numel(), grad_loss))
         return (dH, dW) + (None,) * 9
 
 

@@ -292,6 +292,10 @@ FLCE_API flce_status flce_backward_ex2(const flce_bf16* h, const flce_bf16* W,
 FLCE_API flce_status flce_scale_grads(flce_bf16* dH, int64_t n_dH, float* dW, int64_t n_dW,
                                       const float* scale, void* stream);
 
+/* flce_scale_grads for gradients that are both bf16, in one launch. */
+FLCE_API flce_status flce_scale_grads_bf16(flce_bf16* dH, int64_t n_dH, flce_bf16* dW, int64_t n_dW,
+                                           const float* scale, void* stream);
+
 /*
  * Distillation: a student head (h_s [N,H_s], W_s [V,H_s]) learns a frozen
  * teacher head's (h_t [N,H_t], W_t [V,H_t]) token distribution.  Source: TRL
