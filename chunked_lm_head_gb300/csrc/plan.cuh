@@ -523,16 +523,22 @@ struct FusedPlan {
   BwdPlan b;  // dH / dW stages over one slab of V columns
 };
 
-FusedPlan plan_fused(long long N, long long H, long long V, long long chunk_rows, int workers, int tm) {
-  FusedPlan fp;
-  N = std::max(1LL, N);
-  const long long nr = round_up(N, BM);
+// Rows of the one-call block, 0 where the budget is too small for it.
+long long fused_rows(long long N, long long chunk_rows) {
+  const long long nr = round_up(std::max(1LL, N), BM);
   // the block is the caller's chunk (rounded up to 128 rows): exponentials in
   // its dlogits budget, the chunk maxima (1/16 of it) on top
   // (at most 32,768 rows: the dlogits pass puts one row per grid row)
-  fp.R = std::min(std::min(round_up(std::max(1LL, chunk_rows), BM), nr), 32768LL);
+  const long long R = std::min(std::min(round_up(std::max(1LL, chunk_rows), BM), nr), 32768LL);
+  return R >= std::min<long long>(2048, nr) ? R : 0;
+}
+
+FusedPlan plan_fused(long long N, long long H, long long V, long long chunk_rows, int workers, int tm) {
+  FusedPlan fp;
+  N = std::max(1LL, N);
+  fp.R = fused_rows(N, chunk_rows);
   fp.ldD = round_up(V, 32);
-  fp.fused = fp.R >= std::min<long long>(2048, nr);
+  fp.fused = fp.R > 0;
   if (!fp.fused) return fp;
   fp.f = plan_forward(fp.R, H, V, workers, tm, kFwdPartialsCap, N);
   fp.b.R = fp.R;

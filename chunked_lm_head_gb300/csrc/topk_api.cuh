@@ -102,9 +102,8 @@ long long topk_bwd_rows(int64_t N, int64_t H, int64_t V, int64_t chunk_rows) {
   return plan_backward(N, H, V, chunk_rows, device_workers(cg), BM * cg).R;
 }
 long long topk_one_call_rows(int64_t N, int64_t H, int64_t V, int64_t chunk_rows) {
-  const int cg = cta_group();
-  const FusedPlan fp = plan_fused(N, H, V, chunk_rows, device_workers(cg), BM * cg);
-  return fp.fused && N > 0 ? fp.R : topk_bwd_rows(N, H, V, chunk_rows);
+  const long long R = N > 0 ? fused_rows(N, chunk_rows) : 0;
+  return R > 0 ? R : topk_bwd_rows(N, H, V, chunk_rows);
 }
 bool topk_dw_ok(const void* dW, int32_t dW_type) { return dW == nullptr || dW_type == FLCE_BF16 || dW_type == FLCE_F32; }
 
@@ -215,7 +214,7 @@ flce_status flce_topk_kd_backward(const flce_bf16* h, const flce_bf16* W, const 
   const long long* count = device_scale ? reinterpret_cast<const long long*>(device_scale->count) : nullptr;
   const float* scale = device_scale ? device_scale->scale : nullptr;
   const bool bf16 = dW != nullptr && dW_type == FLCE_BF16;
-  const TopkGrad tg = topk_grad(dW ? dW_type : FLCE_F32, N, H, V, topk_bwd_rows(N, H, V, chunk_rows));
+  const TopkGrad tg = topk_grad(dW ? dW_type : FLCE_F32, N, H, V, bf16 ? topk_bwd_rows(N, H, V, chunk_rows) : 0);
   if (bf16 && !tg.scratch) c.dW16 = static_cast<flce_bf16*>(dW);
   const size_t inner = align256(flce_workspace_bytes(N, H, V, chunk_rows));
   cudaStream_t st = static_cast<cudaStream_t>(stream);

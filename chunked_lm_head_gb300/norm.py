@@ -41,24 +41,17 @@ def _check(x, weight, residual):
     return ldx, ldr
 
 
-def _forward(x, weight, residual, eps, weight_offset, need_rstd, stream, e4m3):
+def _norm(x, weight, residual, eps, weight_offset, need_rstd, stream):
+    """(y, stream or None, rstd or None)"""
     ldx, ldr = _check(x, weight, residual)
     N, H = x.shape
-    dev = x.device
-    s = None if residual is None else torch.empty((N, H), dtype=residual.dtype, device=dev)
-    rstd = torch.empty(N, dtype=torch.float32, device=dev) if need_rstd else None
-    rt = 0 if residual is None else _TYPES[residual.dtype]
-    if e4m3:
-        q = torch.empty((N, H), dtype=torch.float8_e4m3fn, device=dev)
-        scale = torch.empty(N, dtype=torch.float32, device=dev)
-        _lib.check("flce_rms_norm_e4m3", _lib.flce_rms_norm_e4m3(
-            x, ldx, residual, ldr, rt, weight, _TYPES[weight.dtype], weight_offset, eps, N, H, q, scale, s, rstd,
-            stream))
-        return {"q": q, "scale": scale, "residual": s, "rstd": rstd}
-    y = torch.empty((N, H), dtype=torch.bfloat16, device=dev)
+    y = torch.empty_like(x)  # contiguous, also for rows out of a wider buffer
+    s = None if residual is None else torch.empty_like(residual)
+    rstd = torch.empty(N, dtype=torch.float32, device=x.device) if need_rstd else None
     _lib.check("flce_rms_norm", _lib.flce_rms_norm(
-        x, ldx, residual, ldr, rt, weight, _TYPES[weight.dtype], weight_offset, eps, N, H, y, s, rstd, stream))
-    return {"y": y, "residual": s, "rstd": rstd}
+        x, ldx, residual, ldr, 0 if residual is None else _TYPES[residual.dtype], weight, _TYPES[weight.dtype],
+        weight_offset, eps, N, H, y, s, rstd, stream))
+    return y, s, rstd
 
 
 def rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None,
@@ -67,15 +60,47 @@ def rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, weight_offset:
 
     The stream s = round(x + residual) comes back as ``residual``, in the
     residual's type; y = s rstd (weight + weight_offset)."""
-    return _forward(x, weight, residual, eps, weight_offset, need_rstd, stream, False)
+    y, s, rstd = _norm(x, weight, residual, eps, weight_offset, need_rstd, stream)
+    return {"y": y, "residual": s, "rstd": rstd}
 
 
-def rms_norm_e4m3(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None):
-    """dict(q[N,H] float8_e4m3fn, scale[N] f32, residual[N,H] or None, rstd[N] f32)
-    on device: y of rms_norm quantised per row from its 32-bit value, with
-    q * scale[:, None] = y up to e4m3's rounding.  The operand form of
+def rms_norm_e4m3(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None,
+                  need_rstd: bool = False):
+    """dict(q[N,H] float8_e4m3fn, scale[N] f32, residual[N,H] or None, rstd[N] f32
+    or None) on device: y of rms_norm quantised per row from its 32-bit value,
+    with q * scale[:, None] = y up to e4m3's rounding.  The operand form of
     flce_forward_e4m3; not differentiable."""
-    return _forward(x, weight, residual, eps, weight_offset, True, stream, True)
+    ldx, ldr = _check(x, weight, residual)
+    N, H = x.shape
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    scale = torch.empty(N, dtype=torch.float32, device=x.device)
+    s = None if residual is None else torch.empty_like(residual)
+    rstd = torch.empty_like(scale) if need_rstd else None
+    _lib.check("flce_rms_norm_e4m3", _lib.flce_rms_norm_e4m3(
+        x, ldx, residual, ldr, 0 if residual is None else _TYPES[residual.dtype], weight, _TYPES[weight.dtype],
+        weight_offset, eps, N, H, q, scale, s, rstd, stream))
+    return {"q": q, "scale": scale, "residual": s, "rstd": rstd}
+
+
+def _norm_grads(dy, s, lds, weight, rstd, ds, weight_offset, need_dx, need_dr, need_dweight, workspace, stream):
+    """(dx, dr, dweight) of checked tensors."""
+    N, H = s.shape
+    wide = s.dtype == torch.float32
+    dx = torch.empty_like(dy) if need_dx or (need_dr and not wide) else None
+    dr = torch.empty_like(s, memory_format=torch.contiguous_format) if need_dr and wide else None
+    dw = None
+    if need_dweight:
+        dw = torch.empty_like(weight)
+        if workspace is None and stream is None:  # torch's allocator keeps it for the next call
+            workspace = torch.empty(_lib.flce_rms_norm_backward_workspace_bytes(N, H), dtype=torch.uint8,
+                                    device=s.device)
+    elif dx is None and dr is None:
+        return None, None, None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _lib.check("flce_rms_norm_backward", _lib.flce_rms_norm_backward(
+        dy, s, lds, _TYPES[s.dtype], ds, weight, _TYPES[weight.dtype], weight_offset, rstd, N, H, dx, dr, dw,
+        workspace, ws_bytes, stream))
+    return dx if need_dx else None, (dr if wide else dx) if need_dr else None, dw
 
 
 def rms_norm_backward(dy, s, weight, rstd, ds=None, weight_offset: float = 0.0, need_dx: bool = True,
@@ -86,26 +111,13 @@ def rms_norm_backward(dy, s, weight, rstd, ds=None, weight_offset: float = 0.0, 
     reaches it past the norm, or None.  For a bf16 stream dx and dr are one
     tensor."""
     _, lds = _check(dy, weight, s)
-    N, H = s.shape
-    if rstd.dtype != torch.float32 or rstd.shape != (N,) or not rstd.is_contiguous() or not rstd.is_cuda:
+    if rstd.dtype != torch.float32 or rstd.shape != (s.shape[0],) or not rstd.is_contiguous() or not rstd.is_cuda:
         raise ValueError("rstd must be a contiguous float32 [N] CUDA tensor")
     if not dy.is_contiguous():
         raise ValueError("dy must be contiguous")
     if ds is not None and (not ds.is_cuda or ds.dtype != s.dtype or ds.shape != s.shape or not ds.is_contiguous()):
         raise ValueError("ds must be a contiguous CUDA tensor of s's shape and type")
-    wide = s.dtype == torch.float32
-    dx = torch.empty((N, H), dtype=torch.bfloat16, device=s.device) if need_dx or (need_dr and not wide) else None
-    dr = torch.empty((N, H), dtype=torch.float32, device=s.device) if need_dr and wide else None
-    dw = torch.empty_like(weight) if need_dweight else None
-    if dx is not None or dr is not None or dw is not None:
-        if workspace is None and dw is not None:  # torch's allocator keeps it for the next call
-            workspace = torch.empty(_lib.flce_rms_norm_backward_workspace_bytes(N, H), dtype=torch.uint8,
-                                    device=s.device)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _lib.check("flce_rms_norm_backward", _lib.flce_rms_norm_backward(
-            dy, s, lds, _TYPES[s.dtype], ds, weight, _TYPES[weight.dtype], weight_offset, rstd, N, H, dx, dr, dw,
-            workspace, ws_bytes, stream))
-    return dx if need_dx else None, (dr if wide else dx) if need_dr else None, dw
+    return _norm_grads(dy, s, lds, weight, rstd, ds, weight_offset, need_dx, need_dr, need_dweight, workspace, stream)
 
 
 class RMSNormFunction(torch.autograd.Function):
@@ -114,11 +126,10 @@ class RMSNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps, weight_offset):
         ctx.set_materialize_grads(False)
-        out = rms_norm_forward(x, weight, residual, eps, weight_offset)
-        s = x if residual is None else out["residual"]
-        ctx.save_for_backward(s, weight, out["rstd"])
+        y, s, rstd = _norm(x, weight, residual, eps, weight_offset, True, None)
+        ctx.save_for_backward(x if s is None else s, weight, rstd)
         ctx.weight_offset = weight_offset
-        return out["y"] if residual is None else (out["y"], s)
+        return y if s is None else (y, s)
 
     @staticmethod
     def backward(ctx, dy, ds=None):
@@ -128,8 +139,9 @@ class RMSNormFunction(torch.autograd.Function):
             if ds is None:
                 return None, None, None, None, None
             return ds.to(torch.bfloat16) if need_x else None, None, ds if need_r else None, None, None
-        dx, dr, dw = rms_norm_backward(dy.contiguous(), s, weight, rstd, None if ds is None else ds.contiguous(),
-                                       ctx.weight_offset, need_x, need_r, need_w)
+        dx, dr, dw = _norm_grads(dy.contiguous(), s, s.stride(0) if s.shape[0] > 1 else s.shape[1], weight, rstd,
+                                 None if ds is None else ds.contiguous(), ctx.weight_offset, need_x, need_r, need_w,
+                                 None, None)
         return dx, dw, dr, None, None
 
 
@@ -141,8 +153,8 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, weight_offset: float =
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or
                                     (residual is not None and residual.requires_grad)):
         return RMSNormFunction.apply(x, weight, residual, eps, weight_offset)
-    out = rms_norm_forward(x, weight, residual, eps, weight_offset, need_rstd=False)
-    return out["y"] if residual is None else (out["y"], out["residual"])
+    y, s, _ = _norm(x, weight, residual, eps, weight_offset, False, None)
+    return y if s is None else (y, s)
 
 
 class RMSNorm(torch.nn.Module):

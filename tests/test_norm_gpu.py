@@ -57,7 +57,7 @@ def test_forward_matches_the_definition(N, H, residual):
 def test_e4m3_matches_the_definition(N, H, residual):
     weight, offset = ((F32, 1.0) if (N + H // 8) % 2 else (BF16, 0.0))
     x, r, w, _ = make(N, H, residual, weight, offset)
-    out = flce.rms_norm_e4m3(x, w, r, eps=1e-5, weight_offset=offset)
+    out = flce.rms_norm_e4m3(x, w, r, eps=1e-5, weight_offset=offset, need_rstd=True)
     s = R.stream(x, r)
     if r is not None:
         assert torch.equal(out["residual"], s)
