@@ -19,62 +19,101 @@ int norm_group(int64_t H, int vpt) { return static_cast<int>(round_up(ceil_div(H
 // Groups of a CTA of about `threads`.
 int norm_groups(int T, int threads) { return std::max(1, std::min(kNormGroups, threads / T)); }
 
-template <bool kQ, int VPT>
-cudaError_t launch_norm_v(NormParams p, bool res, bool res_f32, int threads, cudaStream_t st) {
+template <class R, bool kQ, int VPT, int MAXT, int CTAS>
+cudaError_t launch_norm_groups(NormParams p, cudaStream_t st) {
   p.T = norm_group(p.H, VPT);
-  const int groups = norm_groups(p.T, threads);
-  const unsigned grid = static_cast<unsigned>(ceil_div(p.N, groups));
-  if (!res)
-    rms_norm_kernel<NoResidual, kQ, VPT><<<grid, groups * p.T, 0, st>>>(p);
-  else if (res_f32)
-    rms_norm_kernel<float, kQ, VPT><<<grid, groups * p.T, 0, st>>>(p);
-  else
-    rms_norm_kernel<uint16_t, kQ, VPT><<<grid, groups * p.T, 0, st>>>(p);
+  const int groups = norm_groups(p.T, MAXT);
+  rms_norm_kernel<R, kQ, VPT, MAXT, CTAS>
+      <<<static_cast<unsigned>(ceil_div(p.N, groups)), groups * p.T, 0, st>>>(p);
+  return cudaGetLastError();
+}
+template <bool kRes, bool kQ, int VPL, int CTAS>
+cudaError_t launch_norm_warps(const NormParams& p, cudaStream_t st) {
+  rms_norm_warp_kernel<kRes, kQ, VPL, CTAS>
+      <<<static_cast<unsigned>(ceil_div(p.N, NORM_WARP_ROWS)), 32 * NORM_WARP_ROWS, 0, st>>>(p);
   return cudaGetLastError();
 }
 
-// Two vectors to a thread in CTAs of about 512 threads (131,072 x 2,560 without
-// a residual: 257 us, against 387 with one vector and 362 with four; CTAs of
-// 256 threads 480); rows of a warp or less one vector in CTAs of 256 (262,144 x
-// 256: 102 against 104 us); past 8,192 elements four, so that a row fits a CTA.
-template <bool kQ>
-cudaError_t launch_norm(const NormParams& p, bool res, bool res_f32, cudaStream_t st) {
-  if (p.H <= 256) return launch_norm_v<kQ, 1>(p, res, res_f32, 256, st);
-  if (p.H <= 8192) return launch_norm_v<kQ, 2>(p, res, res_f32, 512, st);
-  return launch_norm_v<kQ, 4>(p, res, res_f32, 512, st);
+// A warp to a row where the row fits its registers beside what else it needs:
+// without a residual up to 4,096 elements (131,072 x 2,560: 196 us in bf16 and
+// 162 in e4m3, against 220 and 232 on groups), with a bf16 residual up to 1,024
+// (262,144 x 256: 81 against 100 us; at 1,024 81 either way, at 4,096 87 against
+// 81).  Else groups of two vectors to a thread in CTAs of about 512 threads;
+// past 8,192 elements four, so that a row fits a CTA.
+template <class R, bool kQ>
+cudaError_t launch_norm_as(const NormParams& p, cudaStream_t st) {
+  constexpr bool kRes = !std::is_same<R, NoResidual>::value;
+  if constexpr (!std::is_same<R, float>::value) {
+    if (p.H <= 256) return launch_norm_warps<kRes, kQ, 1, 6>(p, st);
+    if (p.H <= 512) return launch_norm_warps<kRes, kQ, 2, 6>(p, st);
+    if (p.H <= 1024) return launch_norm_warps<kRes, kQ, 4, 4>(p, st);
+  }
+  if constexpr (!kRes) {
+    if (p.H <= 2048) return launch_norm_warps<false, kQ, 8, 3>(p, st);
+    if (p.H <= 2560) return launch_norm_warps<false, kQ, 10, 3>(p, st);
+    if (p.H <= 4096) return launch_norm_warps<false, kQ, 16, 2>(p, st);
+  }
+  // 32 registers and four CTAs to an SM pay without a residual to read, 40 and
+  // three with one (16,384 x 4,096 fp32: 118 against 124 us)
+  if (p.H <= 8192) return launch_norm_groups<R, kQ, 2, 512, kRes ? 2 : 4>(p, st);
+  if (p.H <= 16384) return launch_norm_groups<R, kQ, 4, 512, 2>(p, st);
+  return launch_norm_groups<R, kQ, 4, 1024, 1>(p, st);
 }
 
-// How the backward runs rows of H: vectors per thread, the group and the CTA.
+template <bool kQ>
+cudaError_t launch_norm(const NormParams& p, bool res, bool res_f32, cudaStream_t st) {
+  if (!res) return launch_norm_as<NoResidual, kQ>(p, st);
+  return res_f32 ? launch_norm_as<float, kQ>(p, st) : launch_norm_as<uint16_t, kQ>(p, st);
+}
+
+// How the backward runs rows of H: vectors per thread, the group, the groups
+// of a CTA and the CTAs.  The latency of a row (its loads, a reduction, its
+// stores) sets the pace, so as many rows as fit are worked on at once, the
+// next one's loads in flight.
+//   bf16 stream, H <= 2,048: one vector to a thread, two CTAs of 512 threads
+//   (65,536 x 1,024: 85 us against 90 for the next shape); up to 8,192 two
+//   vectors, one CTA of up to 896 threads (131,072 x 2,560: 305 us against 359
+//   with 512 threads and 359 with one vector; 16,384 x 4,096: 85 against 89 and
+//   89).  Two rows deep in shared memory: three and four take as long.
+//   fp32 stream: straight from global memory, whose second read hits L1
+//   (16,384 x 4,096: 190 us against 238 through shared memory, where a
+//   thread's 32 bytes of a row halve every access).
 struct NormBwdShape {
   int vpt, T, groups, ctas;
 };
-// One CTA of 512 threads to an SM, two vectors to a thread (16,384 x 4,096 bf16
-// with the stream's gradient: 93 us, against 116 with one vector and 99 with
-// four; two CTAs to an SM 96, their dweight partials twice as many).  Rows of
-// a warp or less: one vector, three CTAs to an SM (262,144 x 256: 97 us
-// against 166 with one CTA).
-NormBwdShape norm_bwd_shape(int64_t N, int64_t H) {
+NormBwdShape norm_bwd_shape(int64_t N, int64_t H, bool f32) {
   NormBwdShape b;
-  b.vpt = H <= 256 ? 1 : H <= 8192 ? 2 : 4;
+  const bool one = H <= (f32 ? 4096 : 2048);
+  b.vpt = one ? 1 : H <= 8192 ? 2 : 4;
   b.T = norm_group(H, b.vpt);
-  b.groups = norm_groups(b.T, 512);
-  const int64_t most = static_cast<int64_t>(H <= 256 ? 3 : 1) * device_sms();
+  b.groups = norm_groups(b.T, b.vpt == 2 ? 896 : 512);
+  const int64_t most = (one ? 2LL : 1LL) * device_sms();
   b.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(N, b.groups), most)));
   return b;
 }
 
+template <class S, int VPT, int DEPTH, int MAXT, int CTAS>
+cudaError_t launch_norm_bwd_as(const NormBwdParams& p, const NormBwdShape& b, cudaStream_t st) {
+  const int threads = b.groups * b.T;
+  const size_t stage = static_cast<size_t>(threads) * VPT * 8 * (2 + (p.up ? 2 : 1) * sizeof(S));
+  // the rows in flight, then the groups' dweight: at most 2 x 86,016 bytes, and 57,344
+  const size_t smem = std::max(DEPTH * stage, p.part ? static_cast<size_t>(b.groups - 1) * p.H * 4 : 0);
+  auto kern = rms_norm_bwd_kernel<S, VPT, DEPTH, MAXT, CTAS>;
+  if (smem > 32768) {  // (the kernel has 8 KB of its own beside it)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 204800);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<b.ctas, threads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <class S>
 cudaError_t launch_norm_bwd(const NormBwdParams& p, const NormBwdShape& b, cudaStream_t st) {
-  // the groups' dweight to be joined: at most 7 x 2,048 floats
-  const size_t smem = p.part ? static_cast<size_t>(b.groups - 1) * p.H * 4 : 0;
-  auto go = [&](auto kern) -> cudaError_t {
-    kern<<<b.ctas, b.groups * b.T, smem, st>>>(p);
-    return cudaGetLastError();
-  };
-  if (b.vpt == 1) return go(rms_norm_bwd_kernel<S, 1, 512, true>);
-  if (b.vpt == 2) return go(rms_norm_bwd_kernel<S, 2, 512, true>);
-  if (b.T <= 512) return go(rms_norm_bwd_kernel<S, 4, 512, false>);
-  return go(rms_norm_bwd_kernel<S, 4, 1024, false>);
+  constexpr bool f32 = std::is_same<S, float>::value;
+  if (b.vpt == 1) return launch_norm_bwd_as<S, 1, f32 ? 0 : 2, 512, 2>(p, b, st);
+  if (b.vpt == 2) return launch_norm_bwd_as<S, 2, f32 ? 0 : 2, 896, 1>(p, b, st);
+  if (b.T <= 512) return launch_norm_bwd_as<S, 4, f32 ? 0 : 1, 512, 1>(p, b, st);
+  return launch_norm_bwd_as<S, 4, 0, 1024, 1>(p, b, st);
 }
 
 }  // namespace
@@ -143,7 +182,8 @@ flce_status flce_rms_norm_e4m3(const flce_bf16* x, int64_t ldx, const void* resi
 
 size_t flce_rms_norm_backward_workspace_bytes(int64_t N, int64_t H) {
   if (!norm_sizes_ok(N, H)) return 0;
-  return align256(static_cast<size_t>(norm_bwd_shape(N, H).ctas) * H * 4);
+  // of either stream type
+  return align256(static_cast<size_t>(std::max(norm_bwd_shape(N, H, false).ctas, norm_bwd_shape(N, H, true).ctas)) * H * 4);
 }
 
 flce_status flce_rms_norm_backward(const flce_bf16* dy, const void* s, int64_t lds, int32_t s_type,
@@ -164,7 +204,7 @@ flce_status flce_rms_norm_backward(const flce_bf16* dy, const void* s, int64_t l
     if (dweight) FLCE_CUDA_TRY(cudaMemsetAsync(dweight, 0, H * (weight_type == FLCE_F32 ? 4 : 2), st));
     return FLCE_OK;
   }
-  const NormBwdShape b = norm_bwd_shape(N, H);
+  const NormBwdShape b = norm_bwd_shape(N, H, s_type == FLCE_F32);
   Workspace ws;
   if (dweight) {
     const flce_status g =

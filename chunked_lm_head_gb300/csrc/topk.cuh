@@ -189,16 +189,6 @@ __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
   return v;
 }
 
-// a b + c on two fp32 at a time
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
-        "l"(reinterpret_cast<const unsigned long long&>(c)));
-  return d;
-}
-
 template <int NR>
 __global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS, TOPK_GEMV_CTAS)
     topk_gemv_kernel(const uint16_t* __restrict__ h, const uint16_t* __restrict__ W, int N, int H, int V, int K,
@@ -242,15 +232,15 @@ __global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS, TOPK_GEMV_CTAS)
       }
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        float x[8];
-        load8(hs + r * H + k, x);
+        Raw8<float> x;
+        x.load(hs + r * H + k);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t u[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             acc[r][c] = fma2(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)),
-                             make_float2(x[2 * e], x[2 * e + 1]), acc[r][c]);
+                             x.pair(e), acc[r][c]);
         }
       }
     }
