@@ -208,7 +208,7 @@ static flce_status forward_impl(const flce_bf16* h, const flce_bf16* W, const in
       }
       ProfScope ps(K_FWD, st);
       const int w = std::min(q.num_units, workers);
-      FLCE_CUDA_TRY(topk ? launch_fwd_listed<MODE_FWD>(cg, kLong, tA, tB, q, w, st)
+      FLCE_CUDA_TRY(topk ? launch_fwd_listed<MODE_FWD>(cg, kLong, tA, tB, tB, q, w, st)
                          : launch_gemm<MODE_FWD>(cg, kLong, tA, tB, tB, q, w, st));
     }
     if (topk) {
@@ -721,12 +721,15 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
   base.tf_a = tfp.tf_a;
   base.tf_b = tfp.tf_b;
   base.tf_d = tfp.tf_d;
+  CUtensorMap E_st;  // the listed forward's exponentials
   if (topk) {
     base.grad_scale = grad_scale;
     base.sp_ids = topk->rows.ids;
     base.sp_val = topk->rows.val;
     base.sp_k = topk->K;
     base.tf_a *= 1.f + mma_cut(H);
+    base.ld_mx = static_cast<int>(fused_ld_mx(V));
+    if (!make_map(&E_st, E, fp.ldD, fp.R, fp.ldD, 64, 32)) return FLCE_ERR_CUDA;
     bsum = topk->bsum;
     bcnt = topk->bcnt;
   }
@@ -771,7 +774,7 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
       ProfScope ps(K_FWD, st);
       const CUtensorMap& A = compact ? hc_k : h_k;
       const int nw = std::min(q.num_units, workers);
-      FLCE_CUDA_TRY(topk ? launch_fwd_listed<MODE_FUSED_FWD>(cg, kLong, A, W_k, q, nw, st)
+      FLCE_CUDA_TRY(topk ? launch_fwd_listed<MODE_FUSED_FWD>(cg, kLong, A, W_k, E_st, q, nw, st)
                          : launch_gemm<MODE_FUSED_FWD>(cg, kLong, A, W_k, W_k, q, nw, st));
     }
     if (topk) {  // (2) the block's lse, kl, loss partials and dlogits coefficients

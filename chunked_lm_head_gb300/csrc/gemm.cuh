@@ -36,6 +36,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <climits>
 #include <cstdint>
 #include <type_traits>
@@ -266,6 +267,7 @@ struct GemmParams {
   const int* sp_ids;
   float* sp_val;
   int sp_k;
+  int ld_mx;  // FUSED_FWD with listed columns: row pitch of mx, a multiple of 8 that covers whole tiles
 };
 
 // grad_scale of the dlogits modes with its device-side factors: / max(count, 1)
@@ -762,6 +764,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
 // One 32-column chunk of this thread's row (32 bf16 = 64 bytes) into half
 // `half` of a 32-row x 64-column bf16 box in 128B-swizzled shared memory
 // (row = lane): 16-byte granule g of the row lands at g ^ (row & 7).
@@ -1146,13 +1153,19 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
       const float scale_a = scale * lin_a;
       // listed columns: this row's list from the unit's first column on
       static_assert(!kSp || MODE == MODE_FWD || MODE == MODE_FUSED_FWD, "listed columns: the forwards");
+      // (its next id and the two after it in registers: a load's latency is
+      // spent before the id is due)
       const int* sp_row = nullptr;
-      int sp_at = 0, sp_next = INT_MAX;
+      int sp_at = 0, sp_next = INT_MAX, sp_next1 = INT_MAX, sp_next2 = INT_MAX;
+      float4 sp_mx = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto sp_id = [&](int i) { return i < p.sp_k ? sp_row[i] : INT_MAX; };
       if constexpr (kSp) {
         if (row_ok) {
           sp_row = p.sp_ids + static_cast<long long>(grow) * p.sp_k;
           sp_at = list_lower_bound(sp_row, p.sp_k, t.n0 * BN);
-          sp_next = sp_at < p.sp_k ? sp_row[sp_at] : INT_MAX;
+          sp_next = sp_id(sp_at);
+          sp_next1 = sp_id(sp_at + 1);
+          sp_next2 = sp_id(sp_at + 2);
         }
       }
       for (int n = t.n0; n < t.n1; ++n) {
@@ -1214,7 +1227,9 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                   p.sp_val[static_cast<long long>(grow) * p.sp_k + sp_at] = select32(v, j) * lin_a;
                   listed |= 1u << j;
                   ++sp_at;
-                  sp_next = sp_at < p.sp_k ? sp_row[sp_at] : INT_MAX;
+                  sp_next = sp_next1;
+                  sp_next1 = sp_next2;
+                  sp_next2 = sp_id(sp_at + 2);
                 }
                 __syncwarp();  // the next accumulator load is the whole warp's
 #pragma unroll
@@ -1226,14 +1241,59 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
 #pragma unroll
             for (int j = 1; j < 32; ++j) cm = fmaxf(cm, v[j]);
             const float nm = fmaxf(run_m, cm * l2a);
-            if (nm != -INFINITY) {
+            if constexpr (MODE == MODE_FUSED_FWD && kSp) {
+              // the stored exponentials, 2^(u log2e - chunk max), summed as they
+              // are formed: one exponential per column instead of two.  Stored in
+              // fp16, whose 11 bits suit values of at most one: their rounding is
+              // an eighth of the dlogits' own (what falls below 2^-25 of the
+              // chunk's largest is lost)
+              const float cmL = cm * l2a;
+              float a = 0.f;
+              uint32_t pk[16];
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float e0 = cm == -INFINITY ? 0.f : ex2_approx(fmaf(v[j], l2a, -cmL));
+                const float e1 = cm == -INFINITY ? 0.f : ex2_approx(fmaf(v[j + 1], l2a, -cmL));
+                a += e0 + e1;
+                pk[j / 2] = pack_f16x2(e0, e1);
+              }
+              if (nm != -INFINITY) {
+                run_s = run_s * ex2_approx(run_m - nm) + a * ex2_approx(cmL - nm);
+                run_m = nm;
+              }
+              // two chunks fill a 32-row x 64-column box that TMA stores (whole
+              // 128-byte lines; 16-byte pieces of 32 rows at a time slowed the
+              // operand loads: 1,126 x 1,096 x 32,003 took 121 us a forward).
+              // Rows without loss are written too, and read by nobody.
+              const int half = c & 1;
+              const uint32_t box = out_stage + (warp - 2) * (2 * OUT_BOX_BYTES) + ((c >> 1) & 1) * OUT_BOX_BYTES;
+              if (half == 0) {
+                if (lane == 0) bulk_wait_read<1>();  // the copy that last used this box has read it
+                __syncwarp();
+              }
+              stage_bf16_half(box, lane, half, pk);
+              if (half == 1) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  const int lrow0 = t.m * C::TM + rank * BM + q * 32;
+                  const int x = col0 - 32;  // first column of the box
+                  if (x < p.ldD && lrow0 < p.rows_cap) tma_store_2d(&tmC, box, x, lrow0);
+                  bulk_commit();
+                }
+              }
+              // a row's maxima leave four at a time
+              sp_mx = make_float4(sp_mx.y, sp_mx.z, sp_mx.w, cmL);
+              if ((c & 3) == 3 && row_ok)
+                *reinterpret_cast<float4*>(p.mx + static_cast<idx_t>(lr) * p.ld_mx + (col0 / 32 - 3)) = sp_mx;
+            } else if (nm != -INFINITY) {
               float a = 0.f;
 #pragma unroll
               for (int j = 0; j < 32; ++j) a += ex2_approx(fmaf(v[j], l2a, -nm));
               run_s = run_s * ex2_approx(run_m - nm) + a;
               run_m = nm;
             }
-            if constexpr (MODE == MODE_FUSED_FWD) {
+            if constexpr (MODE == MODE_FUSED_FWD && !kSp) {
               // 2^(u log2e - chunk max) in [0, 1] as bf16, and the chunk max,
               // for the dlogits pass once the row's lse is known (an ignored
               // row's dlogits are zero: the pass does not read them)
@@ -1513,8 +1573,8 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
             // dW rounded to bf16 once (its only row block): two chunks fill a
             // 32-row x 64-column box, which TMA stores; columns past H and
             // rows past V are clipped.  Half the bytes of the fp32 gradient,
-            // and none are read back to be rounded (256 x 2,048 x 248,320: see
-            // the launch in launch.cuh)
+            // and none are read back to be rounded: 256 x 2,048 x 248,320 takes
+            // 232 us where the fp32 dW and a rounding pass took 382 and 510
             static_assert(MODE == MODE_DW, "bf16 output: the dW mode");
             uint32_t pk[16];
 #pragma unroll
@@ -1585,6 +1645,8 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
         if (lane == 0) {
           if constexpr (CG == 1)
             mbar_arrive(acc ? tempty_target1 : tempty_target0);
+          else if constexpr (kOut16 || kSp)
+            mbar_arrive_cluster_tmem(acc ? tempty_target1 : tempty_target0);
           else
             mbar_arrive_cluster(acc ? tempty_target1 : tempty_target0);
         }
@@ -1631,7 +1693,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
   }
 
   if constexpr (MODE == MODE_DW || MODE == MODE_DH || MODE == MODE_DH2 || MODE == MODE_DHDW || MODE == MODE_DLOGITS ||
-                MODE == MODE_PIPE) {
+                MODE == MODE_PIPE || (MODE == MODE_FUSED_FWD && kSp)) {
     if (warp >= 2 && lane == 0) bulk_wait_all();  // output boxes written before the CTA retires
   }
   __syncthreads();

@@ -210,15 +210,15 @@ cudaError_t launch_fwd_e4m3(int cg, bool kLong, const CUtensorMap& a, const CUte
 }
 
 // A forward over rows with listed columns (the distillation from a teacher's
-// top logits): MODE_FWD or MODE_FUSED_FWD.
+// top logits): MODE_FWD, or MODE_FUSED_FWD whose exponentials leave through c.
 template <int MODE>
-cudaError_t launch_fwd_listed(int cg, bool kLong, const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
-                              int workers, cudaStream_t st) {
+cudaError_t launch_fwd_listed(int cg, bool kLong, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
+                              const GemmParams& p, int workers, cudaStream_t st) {
   auto go = [&](auto kern, int smem, int grid_mult) -> cudaError_t {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_persistent(kern, grid_mult * grid_workers(workers), grid_mult, gemm_threads(EPI_WARPS), smem, st,
-                             a, b, b, a, b, b, a, b, b, p);
+                             a, b, c, a, b, c, a, b, c, p);
   };
   if (cg == 2)
     return kLong ? go(flce_gemm_kernel<MODE, true, 2, false, EPI_WARPS, true>, TileCfg<2>::SMEM, 2)
@@ -242,8 +242,10 @@ cudaError_t launch_dw16_t(int cg, const CUtensorMap& a, const CUtensorMap& b, co
 }
 cudaError_t launch_dw16(int cg, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const GemmParams& p,
                         int workers, cudaStream_t st) {
-  // 16 epilogue warps at short K, as the fp32 dW
-  return p.k_blocks <= kDwWideEpilogueMaxKBlocks ? launch_dw16_t<4 * EPI_WARPS>(cg, a, b, c, p, workers, st)
+  // 8 epilogue warps at short K (256 x 2,048 x 248,320: 232 us against 245 with
+  // 16, whose staging takes two operand stages, and 237 with 4; 1,024 x 4,096 x
+  // 151,936: 819 against 847 with 4), 4 beyond (2,048 rows: 1,447 against 1,512)
+  return p.k_blocks <= kDwWideEpilogueMaxKBlocks ? launch_dw16_t<2 * EPI_WARPS>(cg, a, b, c, p, workers, st)
                                                  : launch_dw16_t<EPI_WARPS>(cg, a, b, c, p, workers, st);
 }
 
@@ -652,9 +654,11 @@ flce_status topk_gemv(const TopkCall& c, const GemmParams& p, const flce_bf16* h
 flce_status topk_dlogits(const TopkCall& c, bool kLong, const GemmParams& p, uint16_t* E, const float* mx, int row0,
                          int rows, const int* ri, const int* n_valid, cudaStream_t st) {
   ProfScope ps(K_DLOGITS, st);
-  const dim3 grid(static_cast<unsigned>(ceil_div(p.ldD, TOPK_DL_COLS)), static_cast<unsigned>(rows));
+  const long long runs = ceil_div(p.ldD, TOPK_DL_COLS);
+  const int steps = static_cast<int>(std::max<long long>(1, std::min<long long>(4, runs * rows / (16LL * device_sms()))));
+  const dim3 grid(static_cast<unsigned>(ceil_div(runs, steps)), static_cast<unsigned>(rows));
   auto go = [&](auto kern) {
-    kern<<<grid, SMALL_THREADS, 0, st>>>(E, mx, p.ldD, row0, ri, c.rows, c.K, n_valid, p.grad_scale, p.tf_softcap,
+    kern<<<grid, SMALL_THREADS, 0, st>>>(E, mx, p.ldD, p.ld_mx, steps, row0, ri, c.rows, c.K, n_valid, p.grad_scale, p.tf_softcap,
                                          p.tf_a, p.tf_b, p.tf_d);
   };
   if (kLong)

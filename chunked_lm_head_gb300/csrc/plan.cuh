@@ -554,6 +554,9 @@ FusedPlan plan_fused(long long N, long long H, long long V, long long chunk_rows
   return fp;
 }
 
+// Row pitch of the chunk maxima: whole 256-column tiles of 8.
+long long fused_ld_mx(long long V) { return ceil_div(V, BN) * (BN / 32); }
+
 struct FusedLayout {
   size_t zt = 0, part = 0, bsum = 0, bcnt = 0, bad = 0, E = 0, mx = 0, lse = 0, dh_part = 0, idx = 0,
          blk = 0, count = 0, hc = 0, lp = 0, wg = 0, total = 0;
@@ -574,7 +577,7 @@ FusedLayout fused_layout(long long N, long long H, const FusedPlan& fp) {
   L.bcnt = take(nblk * 8);
   L.bad = take(256);
   L.E = take(static_cast<size_t>(fp.R) * fp.ldD * 2);
-  L.mx = take(static_cast<size_t>(fp.R) * (fp.ldD / 32) * 4);
+  L.mx = take(static_cast<size_t>(fp.R) * fused_ld_mx(fp.b.Vs) * 4);
   L.lse = take(static_cast<size_t>(N) * 4);
   L.dh_part = take(fp.b.dh_f32 ? static_cast<size_t>(fp.b.dh_splits) * fp.R * H * 4 : 0);
   L.idx = take(static_cast<size_t>(N) * 4);

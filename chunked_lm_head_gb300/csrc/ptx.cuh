@@ -193,6 +193,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same for a barrier that only hands tensor memory back (the reads are
+// ordered by tcgen05.wait::ld and tcgen05.fence): released at CTA scope, so
+// that it does not wait until the thread's shared-memory writes and output
+// copies are visible across the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // TMA load into this CTA's shared memory whose completion is counted on an
 // mbarrier of either CTA of the pair (the pair's MMA-issuing CTA).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map,

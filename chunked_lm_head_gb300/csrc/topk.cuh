@@ -382,17 +382,18 @@ __global__ void __launch_bounds__(SMALL_THREADS)
 }
 
 // dlogits of one row block of the one-call step, in place: the forward's
-// exponentials E = 2^(u log2 e - chunk max) (0 in the listed columns and past
-// the vocabulary) become
+// fp16 exponentials E = 2^(u log2 e - chunk max) (0 in the listed columns and
+// past the vocabulary) become the bf16
 //   D = E 2^(chunk max - lse_rest) coef g f'(z),  g = grad_scale / max(n_valid, 1),
-// then the listed columns get theirs.  A CTA takes TOPK_DL_COLS columns of a
-// row (blockIdx.y), a lane 8 neighbouring columns per step, so that a warp's
-// 16-byte accesses are contiguous.  Rows as fused_dlogits_kernel.
+// then the listed columns get theirs.  A CTA takes `steps` runs of
+// TOPK_DL_COLS columns of a row (blockIdx.y), a lane 8 neighbouring columns at
+// a time, so that a warp's 16-byte accesses are contiguous.  Rows as
+// fused_dlogits_kernel.
 constexpr int TOPK_DL_COLS = SMALL_THREADS * 32;
 
 template <bool kLong>
 __global__ void __launch_bounds__(SMALL_THREADS)
-    topk_dlogits_kernel(uint16_t* __restrict__ E, const float* __restrict__ mx, int ldD, int row0,
+    topk_dlogits_kernel(uint16_t* __restrict__ E, const float* __restrict__ mx, int ldD, int ld_mx, int steps, int row0,
                         const int* __restrict__ ri, const TopkRows rows, int K, const int* __restrict__ n_valid,
                         float grad_scale, int tf_softcap, float tf_a, float tf_b, float tf_d) {
   using idx_t = typename std::conditional<kLong, long long, int>::type;
@@ -404,50 +405,58 @@ __global__ void __launch_bounds__(SMALL_THREADS)
   const bool live = rows.mark[i] >= 0;
   const float scale = live ? rows.coef[i] * g : 0.f;
   uint16_t* row = E + static_cast<idx_t>(r) * ldD;
-  const float* rmx = mx + static_cast<idx_t>(r) * (ldD / 32);
-  const int c0 = blockIdx.x * TOPK_DL_COLS;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float nlse2 = -rows.lse_rest[i] * kLog2e;
-  uint4 q[4];
-  float base[4];
+  const float* rmx = mx + static_cast<idx_t>(r) * ld_mx;
+  const int c0 = blockIdx.x * steps * TOPK_DL_COLS;
+  const int c1 = min(ldD, c0 + steps * TOPK_DL_COLS);
+  const int first = c0 + (threadIdx.x >> 5) * 1024 + (threadIdx.x & 31) * 8;
+  if (scale == 0.f) {  // a row without loss or weight, whose exponentials may never have been written
+    for (int c = c0 + threadIdx.x * 8; c < c1; c += SMALL_THREADS * 8)
+      *reinterpret_cast<uint4*>(row + c) = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    const float nlse2 = -rows.lse_rest[i] * kLog2e;
+    for (int cs = first; cs < c1; cs += TOPK_DL_COLS) {
+      uint4 q[4];
+      float cm[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = c0 + warp * 1024 + k * 256 + lane * 8;
-    q[k] = make_uint4(0u, 0u, 0u, 0u);
-    base[k] = 0.f;
-    if (c < ldD && scale != 0.f) {
-      q[k] = *reinterpret_cast<const uint4*>(row + c);
-      base[k] = rmx[c / 32];
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = c0 + warp * 1024 + k * 256 + lane * 8;
-    if (c >= ldD) continue;
-    uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-    if (scale != 0.f) {  // else zeros: a row without loss or weight, whose exponentials may never have been written
-      const float kf = ex2_approx(base[k] + nlse2) * scale;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
-        if (!tf_softcap) {
-          lo *= kf * tf_a;
-          hi *= kf * tf_a;
-        } else {  // u = ln(E) + chunk max, tanh(a z) = u / b
-          const float ul = (__log2f(lo) + base[k]) * kLn2 / tf_b, uh = (__log2f(hi) + base[k]) * kLn2 / tf_b;
-          lo = lo > 0.f ? lo * kf * tf_d * (1.f - ul * ul) : 0.f;
-          hi = hi > 0.f ? hi * kf * tf_d * (1.f - uh * uh) : 0.f;
+      for (int k = 0; k < 4; ++k) {
+        const int c = cs + k * 256;
+        if (c < c1) {
+          q[k] = *reinterpret_cast<const uint4*>(row + c);
+          cm[k] = rmx[c / 32];
         }
-        w[e] = pack_bf16x2(lo, hi);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = cs + k * 256;
+        if (c >= c1) continue;
+        uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+        const float kf = ex2_approx(cm[k] + nlse2) * scale;
+        if (!tf_softcap) {
+          const float2 f = both(kf * tf_a);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 d = mul2(__half22float2(*reinterpret_cast<const __half2*>(&w[e])), f);
+            w[e] = pack_bf16x2(d.x, d.y);
+          }
+        } else {  // u = ln(E) + chunk max, tanh(a z) = u / b
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 ev = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+            const float lo = ev.x, hi = ev.y;
+            const float ul = (__log2f(lo) + cm[k]) * kLn2 / tf_b, uh = (__log2f(hi) + cm[k]) * kLn2 / tf_b;
+            w[e] = pack_bf16x2(lo > 0.f ? lo * kf * tf_d * (1.f - ul * ul) : 0.f,
+                               hi > 0.f ? hi * kf * tf_d * (1.f - uh * uh) : 0.f);
+          }
+        }
+        *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-    *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   if (!live) return;  // (the whole CTA)
   __syncthreads();  // the listed columns after the CTA's own stores
   for (int j = threadIdx.x; j < K; j += SMALL_THREADS) {
     const int id = rows.ids[i * K + j];
-    if (id >= c0 && id - c0 < TOPK_DL_COLS && id != INT_MAX)
+    if (id >= c0 && id < c1 && id != INT_MAX)
       row[id] = static_cast<uint16_t>(pack_bf16x2(rows.val[i * K + j] * g, 0.f) & 0xffffu);
   }
 }
