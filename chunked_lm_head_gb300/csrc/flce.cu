@@ -568,7 +568,8 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
   const int cg = cta_group();
   const int workers = device_workers(cg);
   const int tm = BM * cg;
-  const FusedPlan fp = plan_fused(N, H, V, chunk_rows, workers, tm);
+  // (dH through fp32 partials where its scale is completed in the reduction)
+  const FusedPlan fp = plan_fused(N, H, V, chunk_rows, workers, tm, topk && topk->split_scale);
   if (!fp.fused || N == 0) {
     // forward (lse and n_valid into scratch when the caller wants neither),
     // then the tiled backward with grad_scale / n_valid on the device
@@ -728,13 +729,14 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
     base.sp_val = topk->rows.val;
     base.sp_k = topk->K;
     base.tf_a *= 1.f + mma_cut(H);
+    if (topk->split_scale) base.out_count = ccount;
     base.ld_mx = static_cast<int>(fused_ld_mx(V));
     if (!make_map(&E_st, E, fp.ldD, fp.R, fp.ldD, 64, 32)) return FLCE_ERR_CUDA;
     bsum = topk->bsum;
     bcnt = topk->bcnt;
   }
   const DhDwStage dhdw{cg, workers, tm, kLong, &fp.b, H, V, dh_part, dH, dW, &W_mn, &dW_map, &dhp_map,
-                       dW16 != nullptr};
+                       dW16 != nullptr, base.out_count, grad_scale};
   // loss block sums: a segment per row block
   const long long per = ceil_div(fp.R, topk ? TOPK_ROWS : SMALL_THREADS);
   if (!topk) {  // the last block's segment may be shorter than the others: zero it whole

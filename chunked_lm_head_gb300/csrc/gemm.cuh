@@ -267,6 +267,8 @@ struct GemmParams {
   const int* sp_ids;
   float* sp_val;
   int sp_k;
+  // bf16 dW: what the dlogits' power-of-two scale leaves of grad_scale / count
+  const int* out_count;
   int ld_mx;  // FUSED_FWD with listed columns: row pitch of mx, a multiple of 8 that covers whole tiles
 };
 
@@ -277,6 +279,20 @@ __device__ __forceinline__ float device_grad_scale(const GemmParams& p) {
   if (p.count_scale != nullptr) g *= 1.f / fmaxf(1.f, static_cast<float>(*p.count_scale));
   if (p.scale_dev != nullptr) g *= *p.scale_dev;
   return g;
+}
+
+// g = grad_scale / max(count, 1) as a power of two and a factor in [1, 2) (of
+// g's sign).  The dlogits take the power of two, exactly; the factor multiplies
+// the fp32 results, so that a common g, whose rounding would be every row's,
+// costs the gradients nothing.
+struct SplitScale {
+  float pow2, rest;
+};
+__device__ __forceinline__ SplitScale split_scale(float grad_scale, const int* count) {
+  const float g = grad_scale / fmaxf(1.f, static_cast<float>(*count));
+  const uint32_t u = __float_as_uint(g);
+  if ((u & 0x7f800000u) == 0u) return SplitScale{1.f, g};  // zero (or too small for a power of two)
+  return SplitScale{__uint_as_float(u & 0x7f800000u), __uint_as_float((u & 0x807fffffu) | 0x3f800000u)};
 }
 
 // Problem extents that depend on the device-side row count of a compacted pass.
@@ -1576,9 +1592,10 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
             // and none are read back to be rounded: 256 x 2,048 x 248,320 takes
             // 232 us where the fp32 dW and a rounding pass took 382 and 510
             static_assert(MODE == MODE_DW, "bf16 output: the dW mode");
+            const float rest = p.out_count != nullptr ? split_scale(p.grad_scale, p.out_count).rest : 1.f;
             uint32_t pk[16];
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) pk[j / 2] = pack_bf16x2(v[j], v[j + 1]);
+            for (int j = 0; j < 32; j += 2) pk[j / 2] = pack_bf16x2(v[j] * rest, v[j + 1] * rest);
             const int half = c & 1;
             const uint32_t box =
                 out_stage + (warp - 2) * (kBoxes * OUT_BOX_BYTES) + ((c >> 1) % kBoxes) * OUT_BOX_BYTES;

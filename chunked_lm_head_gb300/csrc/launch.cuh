@@ -437,6 +437,8 @@ struct DhDwStage {
   const CUtensorMap* dW_map;
   const CUtensorMap* dhp_map;  // fp32 dH partials [dh_splits * R][H]
   bool dw16 = false;           // one row block: dW in bf16, dW_map 64 x 32 boxes of it
+  const int* out_count = nullptr;  // the dlogits took grad_scale / count's power of two: the count
+  float grad_scale = 1.f;
 };
 
 flce_status slab_dh_dw(const DhDwStage& a, const GemmParams& p, int rows, int block, int slab, int v0,
@@ -551,10 +553,12 @@ flce_status block_dh_finish(const DhDwStage& a, int row0, int rows, const int* r
       1, std::min<long long>(ceil_div(total, SMALL_THREADS), 8LL * device_sms())));
   if (a.kLong)
     dh_reduce_kernel<true><<<grid, SMALL_THREADS, 0, st>>>(a.dh_part, b.dh_splits, rows, static_cast<int>(b.R),
-                                                           static_cast<int>(a.H), row0, a.dH, ri, dc, first);
+                                                           static_cast<int>(a.H), row0, a.dH, ri, dc, first,
+                                                           a.out_count, a.grad_scale);
   else
     dh_reduce_kernel<false><<<grid, SMALL_THREADS, 0, st>>>(a.dh_part, b.dh_splits, rows, static_cast<int>(b.R),
-                                                            static_cast<int>(a.H), row0, a.dH, ri, dc, first);
+                                                            static_cast<int>(a.H), row0, a.dH, ri, dc, first,
+                                                            a.out_count, a.grad_scale);
   FLCE_CUDA_TRY(cudaGetLastError());
   return FLCE_OK;
 }
@@ -593,6 +597,7 @@ struct TopkCall {
   double* bsum = nullptr;  // block sums of the row kernel
   long long* bcnt = nullptr;
   float2* gemv = nullptr;  // [CTAs][N] partials of the few-row forward
+  bool split_scale = false;   // the one-call dlogits take the power of two of their scale
   flce_bf16* dW16 = nullptr;  // dW in bf16 straight from the GEMM (one row block), instead of dW
 };
 
@@ -658,8 +663,8 @@ flce_status topk_dlogits(const TopkCall& c, bool kLong, const GemmParams& p, uin
   const int steps = static_cast<int>(std::max<long long>(1, std::min<long long>(4, runs * rows / (16LL * device_sms()))));
   const dim3 grid(static_cast<unsigned>(ceil_div(runs, steps)), static_cast<unsigned>(rows));
   auto go = [&](auto kern) {
-    kern<<<grid, SMALL_THREADS, 0, st>>>(E, mx, p.ldD, p.ld_mx, steps, row0, ri, c.rows, c.K, n_valid, p.grad_scale, p.tf_softcap,
-                                         p.tf_a, p.tf_b, p.tf_d);
+    kern<<<grid, SMALL_THREADS, 0, st>>>(E, mx, p.ldD, p.ld_mx, steps, row0, ri, c.rows, c.K, n_valid, p.grad_scale,
+                                         p.out_count != nullptr, p.tf_softcap, p.tf_a, p.tf_b, p.tf_d);
   };
   if (kLong)
     go(topk_dlogits_kernel<true>);

@@ -533,7 +533,8 @@ long long fused_rows(long long N, long long chunk_rows) {
   return R >= std::min<long long>(2048, nr) ? R : 0;
 }
 
-FusedPlan plan_fused(long long N, long long H, long long V, long long chunk_rows, int workers, int tm) {
+FusedPlan plan_fused(long long N, long long H, long long V, long long chunk_rows, int workers, int tm,
+                     bool dh_f32 = false) {
   FusedPlan fp;
   N = std::max(1LL, N);
   fp.R = fused_rows(N, chunk_rows);
@@ -550,7 +551,7 @@ FusedPlan plan_fused(long long N, long long H, long long V, long long chunk_rows
   int sp = dh_split_count(ceil_div(fp.R, tm) * ceil_div(H, fp.b.dh_wide ? 2 * BN : BN), kb, workers);
   fp.b.dh_kb_per_split = static_cast<int>(ceil_div(kb, sp));
   fp.b.dh_splits = static_cast<int>(ceil_div(kb, fp.b.dh_kb_per_split));
-  fp.b.dh_f32 = fp.b.dh_splits > 1;
+  fp.b.dh_f32 = dh_f32 || fp.b.dh_splits > 1;
   return fp;
 }
 

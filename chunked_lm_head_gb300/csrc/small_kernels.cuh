@@ -144,14 +144,15 @@ __global__ void final_kernel(const double* __restrict__ blk_sum, const long long
   }
 }
 
-// dH[row, :] = bf16(sum over k-splits of the fp32 partials), split order
-// fixed; row = row_idx[first + r] for a compacted pass (row count read from
+// dH[row, :] = bf16(sum over k-splits of the fp32 partials, times the rest of
+// the split scale where out_count is given), split order fixed; row = row_idx[first + r] for a compacted pass (row count read from
 // dyn_count), else row0 + r.
 template <bool kLong>
 __global__ void dh_reduce_kernel(const float* __restrict__ part, int splits, int rows, int rows_cap,
                                  int H, int row0, uint16_t* __restrict__ dH,
                                  const int* __restrict__ row_idx, const int* __restrict__ dyn_count,
-                                 int first) {
+                                 int first, const int* __restrict__ out_count = nullptr, float grad_scale = 1.f) {
+  const float rest = out_count != nullptr ? split_scale(grad_scale, out_count).rest : 1.f;
   using idx_t = typename std::conditional<kLong, long long, int>::type;
   if (dyn_count != nullptr) rows = max(0, min(*dyn_count - first, rows_cap));
   const int h4 = H / 4;
@@ -168,6 +169,12 @@ __global__ void dh_reduce_kernel(const float* __restrict__ part, int splits, int
       s.y += q.y;
       s.z += q.z;
       s.w += q.w;
+    }
+    if (out_count != nullptr) {
+      s.x *= rest;
+      s.y *= rest;
+      s.z *= rest;
+      s.w *= rest;
     }
     const int out_row = row_idx != nullptr ? row_idx[first + r] : row0 + r;
     *reinterpret_cast<uint2*>(dH + static_cast<idx_t>(out_row) * H + c) =
@@ -571,14 +578,18 @@ __global__ void scale_bf16_kernel(__nv_bfloat16* __restrict__ x, long long n, co
     x[i] = __float2bfloat16_rn(__bfloat162float(x[i]) * s);
 }
 
-// bf16 of n fp32 values (n a multiple of 8), each rounded once.
-__global__ void round_bf16_kernel(const float* __restrict__ x, long long n, uint16_t* __restrict__ y) {
+// bf16 of n fp32 values (n a multiple of 8), each rounded once, times the rest
+// of the split scale where out_count is given.
+__global__ void round_bf16_kernel(const float* __restrict__ x, long long n, uint16_t* __restrict__ y,
+                                  const int* __restrict__ out_count, float grad_scale) {
+  const float f = out_count != nullptr ? split_scale(grad_scale, out_count).rest : 1.f;
   const long long nv = n / 8;
   const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
   for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < nv; i += stride) {
     const float4 a = reinterpret_cast<const float4*>(x)[2 * i], b = reinterpret_cast<const float4*>(x)[2 * i + 1];
     reinterpret_cast<uint4*>(y)[i] =
-        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+        make_uint4(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f), pack_bf16x2(b.x * f, b.y * f),
+                   pack_bf16x2(b.z * f, b.w * f));
   }
 }
 

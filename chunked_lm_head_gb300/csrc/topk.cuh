@@ -384,7 +384,8 @@ __global__ void __launch_bounds__(SMALL_THREADS)
 // dlogits of one row block of the one-call step, in place: the forward's
 // fp16 exponentials E = 2^(u log2 e - chunk max) (0 in the listed columns and
 // past the vocabulary) become the bf16
-//   D = E 2^(chunk max - lse_rest) coef g f'(z),  g = grad_scale / max(n_valid, 1),
+//   D = E 2^(chunk max - lse_rest) coef g f'(z),  g = grad_scale / max(n_valid, 1)
+// (split: g's power of two),
 // then the listed columns get theirs.  A CTA takes `steps` runs of
 // TOPK_DL_COLS columns of a row (blockIdx.y), a lane 8 neighbouring columns at
 // a time, so that a warp's 16-byte accesses are contiguous.  Rows as
@@ -395,13 +396,13 @@ template <bool kLong>
 __global__ void __launch_bounds__(SMALL_THREADS)
     topk_dlogits_kernel(uint16_t* __restrict__ E, const float* __restrict__ mx, int ldD, int ld_mx, int steps, int row0,
                         const int* __restrict__ ri, const TopkRows rows, int K, const int* __restrict__ n_valid,
-                        float grad_scale, int tf_softcap, float tf_a, float tf_b, float tf_d) {
+                        float grad_scale, int split, int tf_softcap, float tf_a, float tf_b, float tf_d) {
   using idx_t = typename std::conditional<kLong, long long, int>::type;
   const int r = blockIdx.y;
   const int n = *n_valid;
   if (ri != nullptr && r >= (n - row0 + 63) / 64 * 64) return;  // row0: the block's first position
   const long long i = ri ? ri[r] : row0 + r;
-  const float g = grad_scale / fmaxf(1.f, static_cast<float>(n));
+  const float g = split ? split_scale(grad_scale, n_valid).pow2 : grad_scale / fmaxf(1.f, static_cast<float>(n));
   const bool live = rows.mark[i] >= 0;
   const float scale = live ? rows.coef[i] * g : 0.f;
   uint16_t* row = E + static_cast<idx_t>(r) * ldD;

@@ -107,9 +107,10 @@ long long topk_one_call_rows(int64_t N, int64_t H, int64_t V, int64_t chunk_rows
 }
 bool topk_dw_ok(const void* dW, int32_t dW_type) { return dW == nullptr || dW_type == FLCE_BF16 || dW_type == FLCE_F32; }
 
-flce_status topk_round_dw(const float* x, int64_t n, void* dW, cudaStream_t st) {
+flce_status topk_round_dw(const float* x, int64_t n, void* dW, const int* out_count, float grad_scale,
+                          cudaStream_t st) {
   ProfScope ps(K_DH_REDUCE, st);
-  round_bf16_kernel<<<8 * device_sms(), SMALL_THREADS, 0, st>>>(x, n, static_cast<uint16_t*>(dW));
+  round_bf16_kernel<<<8 * device_sms(), SMALL_THREADS, 0, st>>>(x, n, static_cast<uint16_t*>(dW), out_count, grad_scale);
   FLCE_CUDA_TRY(cudaGetLastError());
   return FLCE_OK;
 }
@@ -147,11 +148,23 @@ size_t flce_topk_kd_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, in
          topk_grad(dW_type, N, H, V, topk_bwd_rows(N, H, V, chunk_rows)).bytes;
 }
 
+// Workspace of the one-call step inside: with a bf16 dW, or none, its fused
+// form completes the dlogits' scale in fp32 (split_scale).
+static size_t topk_one_call_inner(int64_t N, int64_t H, int64_t V, int64_t chunk_rows, bool split) {
+  const int cg = cta_group();
+  const int workers = device_workers(cg);
+  const FusedPlan fp = plan_fused(N, H, V, chunk_rows, workers, BM * cg, split);
+  return align256(fp.fused && N > 0 ? fused_layout(N, H, fp).total
+                                    : fallback_workspace(N, H, V, chunk_rows, workers, BM * cg));
+}
+
 size_t flce_topk_kd_forward_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k, int64_t chunk_rows,
                                                      int32_t dW_type) {
   if (!sizes_ok(N, H, V) || k < 1 || k > TOPK_MAX_K) return 0;
-  return align256(flce_forward_backward_workspace_bytes(N, H, V, chunk_rows)) + topk_layout(N, k).total +
-         topk_grad(dW_type, N, H, V, topk_one_call_rows(N, H, V, chunk_rows)).bytes;
+  // (a call without dW needs what one with a bf16 dW does)
+  return std::max(topk_one_call_inner(N, H, V, chunk_rows, true),
+                  dW_type == FLCE_F32 ? topk_one_call_inner(N, H, V, chunk_rows, false) : 0) +
+         topk_layout(N, k).total + topk_grad(dW_type, N, H, V, topk_one_call_rows(N, H, V, chunk_rows)).bytes;
 }
 
 flce_status flce_topk_kd_forward(const flce_bf16* h, const flce_bf16* W, const flce_top_logits* teacher,
@@ -226,7 +239,7 @@ flce_status flce_topk_kd_backward(const flce_bf16* h, const flce_bf16* W, const 
   s = backward_impl(h, W, reinterpret_cast<const int64_t*>(c.rows.mark), c.rows.coef, c.rows.lse_rest, grad_scale, dH,
                     sum, N, H, V, chunk_rows, kMarkIgnored, transform, ws.ptr, inner, stream, count, scale, &c);
   if (s != FLCE_OK || !tg.scratch) return s;
-  return topk_round_dw(sum, V * H, dW, st);
+  return topk_round_dw(sum, V * H, dW, nullptr, 1.f, st);
 }
 
 flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W, const flce_top_logits* teacher,
@@ -245,10 +258,11 @@ flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W
       !aligned(out_kl, 4) || !aligned(out_lse, 4) || !aligned(out_loss, 4) || !aligned(out_n_valid, 8))
     return FLCE_ERR_UNSUPPORTED;
   const TopkLayout L = topk_layout(N, teacher->k);
-  const size_t inner = align256(flce_forward_backward_workspace_bytes(N, H, V, chunk_rows));
+  const bool bf16 = dW != nullptr && dW_type == FLCE_BF16;
+  const bool split = (bf16 || dW == nullptr) && N > 0 && fused_rows(N, chunk_rows) > 0;
+  const size_t inner = topk_one_call_inner(N, H, V, chunk_rows, split);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Workspace ws;
-  const bool bf16 = dW != nullptr && dW_type == FLCE_BF16;
   const TopkGrad tg = topk_grad(dW ? dW_type : FLCE_F32, N, H, V, topk_one_call_rows(N, H, V, chunk_rows));
   s = get_workspace(ws, workspace, workspace_bytes, inner + L.total + tg.bytes, st);
   if (s != FLCE_OK) return s;
@@ -256,6 +270,7 @@ flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W
   float* sum = tg.scratch ? reinterpret_cast<float*>(wb + inner + L.total) : bf16 ? nullptr : static_cast<float*>(dW);
   TopkCall c;
   if (bf16 && !tg.scratch) c.dW16 = static_cast<flce_bf16*>(dW);
+  c.split_scale = split;
   c.rows = topk_rows_at(L, wb + inner, wb + inner);
   c.K = teacher->k;
   c.tail = teacher->tail;
@@ -271,7 +286,14 @@ flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W
                             kMarkIgnored, transform, grad_scale, nullptr, nullptr, out_loss, out_n_valid, dH, sum, wb,
                             inner, stream, nullptr, &c);
   if (s != FLCE_OK || !tg.scratch) return s;
-  return topk_round_dw(sum, V * H, dW, st);
+  // the count that the step left in its workspace
+  const int* count = nullptr;
+  if (split) {
+    const int cg = cta_group();
+    const FusedPlan fp = plan_fused(N, H, V, chunk_rows, device_workers(cg), BM * cg, true);
+    count = reinterpret_cast<const int*>(wb + fused_layout(N, H, fp).count);
+  }
+  return topk_round_dw(sum, V * H, dW, count, grad_scale, st);
 }
 
 }  // extern "C"
