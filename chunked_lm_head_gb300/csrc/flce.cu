@@ -208,7 +208,7 @@ static flce_status forward_impl(const flce_bf16* h, const flce_bf16* W, const in
       }
       ProfScope ps(K_FWD, st);
       const int w = std::min(q.num_units, workers);
-      FLCE_CUDA_TRY(topk ? launch_fwd_listed<MODE_FWD>(cg, kLong, tA, tB, tB, q, w, st)
+      FLCE_CUDA_TRY(topk ? launch_listed<MODE_FWD>(cg, kLong, tA, tB, tB, q, w, st)
                          : launch_gemm<MODE_FWD>(cg, kLong, tA, tB, tB, q, w, st));
     }
     if (topk) {
@@ -288,9 +288,12 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   const int cg = cta_group();
   const int workers = device_workers(cg);
   const int tm = BM * cg;
-  // (a list's columns are written over each slab's dlogits, between its launches)
-  const BwdPlan b = topk ? plan_backward(N, H, V, chunk_rows, workers, tm)
-                         : plan_backward_call(N, H, V, chunk_rows, workers, tm, dH != nullptr && dW != nullptr);
+  // (with listed columns one block of rows keeps the unpipelined plan, whose dW
+  // GEMM can write bf16: the sums' order, and so dH's bits, are the same
+  // whatever dW's type)
+  BwdPlan b = plan_backward(N, H, V, chunk_rows, workers, tm);
+  if (!topk || N > b.R)
+    b = plan_backward_call(N, H, V, chunk_rows, workers, tm, dH != nullptr && dW != nullptr);
   const BwdLayout L = bwd_layout(N, H, b);
   Workspace ws;
   flce_status s = get_workspace(ws, workspace, workspace_bytes, L.total, st);
@@ -349,6 +352,11 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   base.tf_a = tfp.tf_a;
   base.tf_b = tfp.tf_b;
   base.tf_d = tfp.tf_d;
+  if (topk) {
+    base.sp_ids = topk->rows.ids;
+    base.sp_val = topk->rows.val;
+    base.sp_k = topk->K;
+  }
 
   // Row compaction: the chunks run over the non-ignored rows (count and
   // indices stay on the device; the kernels read each chunk's row count), so
@@ -418,7 +426,8 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
     }
     if (pipe) {
       const flce_status s2 = pipe_block(dhdw, p, rows, block, A_dl, W_k, D_st, Dpipe_k, Dpipe_mn, B_dw,
-                                        dep + (block % 2) * dep_words, dep + ((block + 1) % 2) * dep_words, st);
+                                        dep + (block % 2) * dep_words, dep + ((block + 1) % 2) * dep_words,
+                                        topk != nullptr, st);
       if (s2 != FLCE_OK) return s2;
     }
     for (int slab = 0; slab < (pipe ? 0 : b.n_slabs); ++slab) {
@@ -439,14 +448,10 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
         // per 4096-row block at 16 against 3.5 GB at 8)
         q.group_m = std::min(16, q.m_tiles);
         ProfScope ps(K_DLOGITS, st);
-        FLCE_CUDA_TRY(launch_gemm<MODE_DLOGITS>(cg, kLong, A_dl, W_k, q.d_tma ? D_st : W_k, q,
-                                                std::min(q.num_units, workers), st));
-      }
-      if (topk) {
-        const flce_status sc = topk_scatter(*topk, kLong, p, Dbuf, v0, width, static_cast<int>(row0), rows,
-                                            compact ? cidx : nullptr, compact ? ccount : nullptr,
-                                            static_cast<int>(row0), count_scale, st);
-        if (sc != FLCE_OK) return sc;
+        const CUtensorMap& D_out = q.d_tma ? D_st : W_k;
+        const int nw = std::min(q.num_units, workers);
+        FLCE_CUDA_TRY(topk ? launch_listed<MODE_DLOGITS>(cg, kLong, A_dl, W_k, D_out, q, nw, st)
+                           : launch_gemm<MODE_DLOGITS>(cg, kLong, A_dl, W_k, D_out, q, nw, st));
       }
       // (2) dH[rows] (+)= D W[slab], (3) dW[slab] (+)= D^T h[rows]
       const flce_status s2 = slab_dh_dw(dhdw, p, rows, block, slab, v0, width, D_k, D_mn, B_dw, st);
@@ -776,7 +781,7 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
       ProfScope ps(K_FWD, st);
       const CUtensorMap& A = compact ? hc_k : h_k;
       const int nw = std::min(q.num_units, workers);
-      FLCE_CUDA_TRY(topk ? launch_fwd_listed<MODE_FUSED_FWD>(cg, kLong, A, W_k, E_st, q, nw, st)
+      FLCE_CUDA_TRY(topk ? launch_listed<MODE_FUSED_FWD>(cg, kLong, A, W_k, E_st, q, nw, st)
                          : launch_gemm<MODE_FUSED_FWD>(cg, kLong, A, W_k, W_k, q, nw, st));
     }
     if (topk) {  // (2) the block's lse, kl, loss partials and dlogits coefficients

@@ -263,7 +263,8 @@ struct GemmParams {
   unsigned* pp_dep_zero;
   // listed columns (the kernel's kSp): each row's sp_k ids in ascending order
   // ([N][sp_k], INT_MAX past the last); the forward writes their transformed
-  // logits to sp_val [N][sp_k] and leaves them out of its log-sum-exp
+  // logits to sp_val [N][sp_k] and leaves them out of its log-sum-exp, the
+  // dlogits units read their gradients (before the scale) from it
   const int* sp_ids;
   float* sp_val;
   int sp_k;
@@ -809,7 +810,7 @@ __device__ __forceinline__ int list_lower_bound(const int* ids, int k, int v) {
   return lo;
 }
 
-// kSp: the forwards with listed columns; kOut16: the DW mode with a bf16 dW.
+// kSp: the forwards and dlogits with listed columns; kOut16: the DW mode with a bf16 dW.
 template <int MODE, bool kLong, int CG, bool kF8 = false, int EW = EPI_WARPS, bool kSp = false, bool kOut16 = false>
 __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
     flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -1168,7 +1169,8 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
       }
       const float scale_a = scale * lin_a;
       // listed columns: this row's list from the unit's first column on
-      static_assert(!kSp || MODE == MODE_FWD || MODE == MODE_FUSED_FWD, "listed columns: the forwards");
+      static_assert(!kSp || MODE == MODE_FWD || MODE == MODE_FUSED_FWD || MODE == MODE_DLOGITS || MODE == MODE_PIPE,
+                    "listed columns: the forwards and the dlogits units");
       // (its next id and the two after it in registers: a load's latency is
       // spent before the id is due)
       const int* sp_row = nullptr;
@@ -1176,9 +1178,9 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
       float4 sp_mx = make_float4(0.f, 0.f, 0.f, 0.f);
       auto sp_id = [&](int i) { return i < p.sp_k ? sp_row[i] : INT_MAX; };
       if constexpr (kSp) {
-        if (row_ok) {
+        if (row_ok && (unit_dl || MODE == MODE_FWD || MODE == MODE_FUSED_FWD)) {
           sp_row = p.sp_ids + static_cast<long long>(grow) * p.sp_k;
-          sp_at = list_lower_bound(sp_row, p.sp_k, t.n0 * BN);
+          sp_at = list_lower_bound(sp_row, p.sp_k, uv0 + t.n0 * BN);
           sp_next = sp_id(sp_at);
           sp_next1 = sp_id(sp_at + 1);
           sp_next2 = sp_id(sp_at + 2);
@@ -1383,6 +1385,24 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                   d1 = (gcol0 + j + 1 < p.V) ? p1 * scale * p.tf_d * (1.f - t1 * t1) : 0.f;
                 }
                 pk[j / 2] = pack_bf16x2(d0, d1);
+              }
+            }
+            if constexpr (kSp) {
+              // the listed columns' own gradients, formed by the row kernel
+              if (__any_sync(0xffffffffu, sp_next < gcol0 + 32)) {
+                const float gs = device_grad_scale(p);
+                while (sp_next < gcol0 + 32) {
+                  const int j = sp_next - gcol0;
+                  const uint32_t d = pack_bf16x2(p.sp_val[static_cast<long long>(grow) * p.sp_k + sp_at] * gs, 0.f);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k)
+                    if (k == (j >> 1)) pk[k] = (j & 1) ? ((pk[k] & 0x0000ffffu) | (d << 16)) : ((pk[k] & 0xffff0000u) | d);
+                  ++sp_at;
+                  sp_next = sp_next1;
+                  sp_next1 = sp_next2;
+                  sp_next2 = sp_id(sp_at + 2);
+                }
+                __syncwarp();  // the box is the whole warp's
               }
             }
             if (p.d_tma) {

@@ -209,22 +209,28 @@ cudaError_t launch_fwd_e4m3(int cg, bool kLong, const CUtensorMap& a, const CUte
                : go(flce_gemm_kernel<MODE_FWD, false, 1, true>, TileCfg<1>::SMEM, 1);
 }
 
-// A forward over rows with listed columns (the distillation from a teacher's
-// top logits): MODE_FWD, or MODE_FUSED_FWD whose exponentials leave through c.
+// A launch over rows with listed columns (the distillation from a teacher's top
+// logits): MODE_FWD, MODE_FUSED_FWD whose exponentials leave through c,
+// MODE_DLOGITS, or MODE_PIPE.
 template <int MODE>
-cudaError_t launch_fwd_listed(int cg, bool kLong, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                              const GemmParams& p, int workers, cudaStream_t st) {
+cudaError_t launch_listed(int cg, bool kLong, const Maps& m, const GemmParams& p, int workers, cudaStream_t st) {
   auto go = [&](auto kern, int smem, int grid_mult) -> cudaError_t {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_persistent(kern, grid_mult * grid_workers(workers), grid_mult, gemm_threads(EPI_WARPS), smem, st,
-                             a, b, c, a, b, c, a, b, c, p);
+    return launch_persistent(kern, grid_mult * grid_workers(workers), grid_mult, kernel_threads<MODE>(EPI_WARPS), smem,
+                             st, *m.a, *m.b, *m.c, *m.a2, *m.b2, *m.c2, *m.a3, *m.b3, *m.c3, p);
   };
+  constexpr int s2 = KernelCfg<MODE, 2, EPI_WARPS>::SMEM, s1 = KernelCfg<MODE, 1, EPI_WARPS>::SMEM;
   if (cg == 2)
-    return kLong ? go(flce_gemm_kernel<MODE, true, 2, false, EPI_WARPS, true>, TileCfg<2>::SMEM, 2)
-                 : go(flce_gemm_kernel<MODE, false, 2, false, EPI_WARPS, true>, TileCfg<2>::SMEM, 2);
-  return kLong ? go(flce_gemm_kernel<MODE, true, 1, false, EPI_WARPS, true>, TileCfg<1>::SMEM, 1)
-               : go(flce_gemm_kernel<MODE, false, 1, false, EPI_WARPS, true>, TileCfg<1>::SMEM, 1);
+    return kLong ? go(flce_gemm_kernel<MODE, true, 2, false, EPI_WARPS, true>, s2, 2)
+                 : go(flce_gemm_kernel<MODE, false, 2, false, EPI_WARPS, true>, s2, 2);
+  return kLong ? go(flce_gemm_kernel<MODE, true, 1, false, EPI_WARPS, true>, s1, 1)
+               : go(flce_gemm_kernel<MODE, false, 1, false, EPI_WARPS, true>, s1, 1);
+}
+template <int MODE>
+cudaError_t launch_listed(int cg, bool kLong, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
+                          const GemmParams& p, int workers, cudaStream_t st) {
+  return launch_listed<MODE>(cg, kLong, Maps{&a, &b, &c, &a, &b, &c, &a, &b, &c}, p, workers, st);
 }
 
 // The dW GEMM with a bf16 result.
@@ -530,12 +536,17 @@ flce_status slab_dh_dw(const DhDwStage& a, const GemmParams& p, int rows, int bl
 flce_status pipe_block(const DhDwStage& a, const GemmParams& p, int rows, int block, const CUtensorMap& A_dl,
                        const CUtensorMap& W_k, const CUtensorMap& D_st, const CUtensorMap& D_k,
                        const CUtensorMap& D_mn, const CUtensorMap& B_dw, unsigned* dep, unsigned* dep_zero,
-                       cudaStream_t st) {
+                       bool listed, cudaStream_t st) {
   GemmParams q = pipe_params(*a.plan, p, a.H, a.tm, rows, block);
   q.dH_part = a.dh_part;
   q.pp_dep = dep;
   q.pp_dep_zero = dep_zero;
   ProfScope ps(K_PIPE, st);
+  if (listed) {
+    FLCE_CUDA_TRY(launch_listed<MODE_PIPE>(
+        a.cg, a.kLong, Maps{&D_k, a.W_mn, a.dhp_map, &D_mn, &B_dw, a.dW_map, &A_dl, &W_k, &D_st}, q, a.workers, st));
+    return FLCE_OK;
+  }
   FLCE_CUDA_TRY(launch_gemm<MODE_PIPE>(a.cg, a.kLong, D_k, *a.W_mn, *a.dhp_map, q, a.workers, st, &D_mn, &B_dw,
                                        a.dW_map, &A_dl, &W_k, &D_st));
   return FLCE_OK;
@@ -682,25 +693,6 @@ flce_status topk_index(const TopkCall& c, int N, int* blk, int* idx, int* count,
                            true, st);
   ProfScope ps(K_COMPACT, st);
   topk_index_kernel<<<1, 1024, 0, st>>>(c.rows.mark, N, idx, count);
-  FLCE_CUDA_TRY(cudaGetLastError());
-  return FLCE_OK;
-}
-
-// The listed columns of the dlogits block D (local columns of slab v0).
-flce_status topk_scatter(const TopkCall& c, bool kLong, const GemmParams& p, uint16_t* D, int v0, int width, int row0,
-                         int rows, const int* ri, const int* dyn_count, int first, const long long* count,
-                         cudaStream_t st) {
-  ProfScope ps(K_TOPK, st);
-  const unsigned grid = static_cast<unsigned>(std::max<long long>(
-      1, std::min<long long>(ceil_div(static_cast<long long>(rows) * c.K, SMALL_THREADS), 8LL * device_sms())));
-  auto go = [&](auto kern) {
-    kern<<<grid, SMALL_THREADS, 0, st>>>(D, p.ldD, v0, width, row0, rows, ri, dyn_count, first, c.K, c.rows.ids,
-                                         c.rows.val, p.grad_scale, count, p.scale_dev);
-  };
-  if (kLong)
-    go(topk_scatter_kernel<true>);
-  else
-    go(topk_scatter_kernel<false>);
   FLCE_CUDA_TRY(cudaGetLastError());
   return FLCE_OK;
 }

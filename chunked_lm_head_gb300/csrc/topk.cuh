@@ -500,29 +500,4 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// The listed columns of a dlogits block: D[r][id - v0] = val * scale, bf16,
-// for the ids inside [v0, v0 + width).  Local row r is row row0 + r, or
-// ri[first + r]; rows past the device-side count are left alone.
-template <bool kLong>
-__global__ void topk_scatter_kernel(uint16_t* __restrict__ D, int ldD, int v0, int width, int row0, int rows,
-                                    const int* __restrict__ ri, const int* __restrict__ dyn_count, int first, int K,
-                                    const int* __restrict__ ids, const float* __restrict__ val, float grad_scale,
-                                    const long long* __restrict__ count, const float* __restrict__ scale_dev) {
-  using idx_t = typename std::conditional<kLong, long long, int>::type;
-  if (dyn_count != nullptr) rows = max(0, min(*dyn_count - first, rows));
-  float g = grad_scale;
-  if (count != nullptr) g *= 1.f / fmaxf(1.f, static_cast<float>(*count));
-  if (scale_dev != nullptr) g *= *scale_dev;
-  const long long total = static_cast<long long>(rows) * K;
-  for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < total;
-       e += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int r = static_cast<int>(e / K);
-    const int j = static_cast<int>(e - static_cast<long long>(r) * K);
-    const long long i = ri ? ri[first + r] : row0 + r;
-    const int id = ids[i * K + j];
-    if (id < v0 || id - v0 >= width) continue;
-    D[static_cast<idx_t>(r) * ldD + (id - v0)] = static_cast<uint16_t>(pack_bf16x2(val[i * K + j] * g, 0.f) & 0xffffu);
-  }
-}
-
 }  // namespace flce

@@ -97,6 +97,8 @@ TopkGrad topk_grad(int32_t dW_type, int64_t N, int64_t H, int64_t V, long long b
   if (g.scratch) g.bytes = align256(static_cast<size_t>(V) * H * 4);
   return g;
 }
+// Rows of the tiled backward's block in its unpipelined plan, the one that a call
+// of one block keeps.
 long long topk_bwd_rows(int64_t N, int64_t H, int64_t V, int64_t chunk_rows) {
   const int cg = cta_group();
   return plan_backward(N, H, V, chunk_rows, device_workers(cg), BM * cg).R;
