@@ -145,6 +145,7 @@ class TopkDistill(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, h, W, ids, logits, lse_t, targets, weights, tail, chunk_rows, ignore_index, transform):
+        ctx.set_materialize_grads(False)  # no zeros for the outputs without a gradient
         out = topk_kd_forward(h, W, ids, logits, lse_t, targets, weights, tail, chunk_rows, ignore_index, transform,
                               skip_ignored=True, for_backward=True)
         ctx.save_for_backward(h, W, out["state"], out["n_valid"])
@@ -154,6 +155,8 @@ class TopkDistill(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_loss, grad_kl, grad_n):
+        if grad_loss is None:
+            return (None,) * 11
         h, W, state, n_valid = ctx.saved_tensors
         dH, dW = topk_kd_backward(h, W, state, ctx.k, 1.0, ctx.chunk_rows, ctx.transform, ctx.needs_input_grad[0],
                                   ctx.needs_input_grad[1], scale=grad_loss, count=n_valid, dW_dtype=W.dtype)
@@ -166,6 +169,7 @@ class TopkDistillOneCall(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, h, W, ids, logits, lse_t, targets, weights, tail, chunk_rows, ignore_index, transform):
+        ctx.set_materialize_grads(False)  # no zeros for the outputs without a gradient
         out = topk_kd_forward_backward(h, W, ids, logits, lse_t, targets, weights, tail, chunk_rows, ignore_index,
                                        1.0, ctx.needs_input_grad[0], ctx.needs_input_grad[1], transform=transform,
                                        need_lse=False, dW_dtype=W.dtype)
@@ -175,6 +179,8 @@ class TopkDistillOneCall(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_loss, grad_kl, grad_n):
+        if grad_loss is None:
+            return (None,) * 11
         if ctx.grads is None:
             raise RuntimeError("the one-call loss can be differentiated once: its gradients are scaled in place")
         dH, dW = ctx.grads

@@ -322,3 +322,28 @@ def test_workspace_of_the_caller_is_enough():
         flce.topk_kd_forward(c["h"], c["W"], c["ids"], c["logits"], workspace=ws[:-256])
     with pytest.raises(ValueError, match="state"):
         flce.topk_kd_backward(c["h"], c["W"], a["state"], K - 1, 1.0)
+
+
+@pytest.mark.parametrize("N,H,V", [(37, 64, 77825), (200, 264, 80003), (256, 520, 90112), (300, 264, 78001),
+                                   (512, 136, 100003)])
+@pytest.mark.parametrize("mask", [False, True])
+def test_few_rows_of_a_wide_vocabulary(N, H, V, mask):
+    """bf16 dW whose units are whole rows of tiles: one to eight K blocks of
+    rows, ragged last tiles, rows left out on the device."""
+    c = make(N, H, V, 19, seed=11, std=0.05, mask=mask, pad=mask, weights=mask)
+    ref = R.reference(**c)
+    args = (c["h"], c["W"], c["ids"], c["logits"], c["lse_t"], c["targets"], c["weights"])
+    got = flce.topk_kd_forward_backward(*args, chunk_rows=4096, dW_dtype=torch.bfloat16)
+    assert _lib.flce_device_status() == 0
+    R.check(got, ref, roundings=2)
+    again = flce.topk_kd_forward_backward(*args, chunk_rows=4096, dW_dtype=torch.bfloat16)
+    assert torch.equal(got["dW"], again["dW"])
+
+
+def test_no_counted_row_of_a_wide_vocabulary():
+    c = make(130, 64, 78001, 5, seed=12)
+    got = flce.topk_kd_forward_backward(c["h"], c["W"], c["ids"], c["logits"], None,
+                                        torch.full((130,), -100, device="cuda"), chunk_rows=4096,
+                                        dW_dtype=torch.bfloat16)
+    assert _lib.flce_device_status() == 0
+    assert not got["dW"].any() and not got["dH"].any() and int(got["n_valid"]) == 0
