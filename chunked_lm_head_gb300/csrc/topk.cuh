@@ -80,31 +80,53 @@ __device__ __forceinline__ float2 two_sum(float x, float y) {
 // The row's list in ascending order of id with the teacher's masses and their
 // logarithms (one warp per row).  An entry's place is the number of entries
 // before it (by id, then by position), counted in one walk over the list that
-// also adds up the mass of equal ids: K^2 / 32 steps of a lane, no barrier.
+// also adds up the mass of equal ids: K^2 / 32 comparisons of a lane, four of
+// its entries against four of the list per shared-memory read, no barrier.
 // t - lse carries what its rounding leaves out; with the tail the masses and
 // their sum are taken in 64 bits, since T = 1 - P is small where they are not.
 __global__ void __launch_bounds__(32 * TOPK_WARPS)
     topk_list_kernel(const TopkTeacher t, const int64_t* __restrict__ targets, long long ignore, int N, int V,
                      const TopkRows out) {
-  extern __shared__ int topk_smem[];
+  extern __shared__ __align__(16) int topk_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int K = t.k;
+  const int K = t.k, Kp = (K + 3) & ~3;  // (the last few of Kp: no entries)
   const long long i = static_cast<long long>(blockIdx.x) * TOPK_WARPS + warp;
   if (i >= N) return;
-  int* sid = topk_smem + warp * 2 * K;
-  float* sp = reinterpret_cast<float*>(sid + K);
+  int* sid = topk_smem + warp * 2 * Kp;
+  float* sp = reinterpret_cast<float*>(sid + Kp);
+  if (lane < Kp - K) {
+    sid[K + lane] = INT_MAX;
+    sp[K + lane] = 0.f;
+  }
   bool any = false, bad = false;
   float top = -INFINITY;
-  for (int j = lane; j < K; j += 32) {
-    const long long id = t.ids_type == 4 ? static_cast<const int64_t*>(t.ids)[i * t.ld_ids + j]
-                                         : static_cast<const int32_t*>(t.ids)[i * t.ld_ids + j];
-    const bool in = id >= 0 && id < V;
-    bad |= id >= V;
-    any |= in;
-    const float u = in ? topk_logit(t, i, j) : -INFINITY;
-    sid[j] = in ? static_cast<int>(id) : INT_MAX;
-    sp[j] = u;
-    top = fmaxf(top, u);
+  for (int j0 = lane; j0 < K; j0 += 128) {
+    // four entries' ids and logits at once: one latency of memory, not eight
+    long long id[4];
+    float u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + 32 * e;
+      id[e] = -1;
+      u[e] = -INFINITY;
+      if (j < K) {
+        id[e] = t.ids_type == 4 ? static_cast<const int64_t*>(t.ids)[i * t.ld_ids + j]
+                                : static_cast<const int32_t*>(t.ids)[i * t.ld_ids + j];
+        u[e] = topk_logit(t, i, j);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + 32 * e;
+      if (j >= K) break;
+      const bool in = id[e] >= 0 && id[e] < V;
+      bad |= id[e] >= V;
+      any |= in;
+      const float x = in ? u[e] : -INFINITY;
+      sid[j] = in ? static_cast<int>(id[e]) : INT_MAX;
+      sp[j] = x;
+      top = fmaxf(top, x);
+    }
   }
   any = __any_sync(0xffffffffu, any);
   bad = __any_sync(0xffffffffu, bad);
@@ -142,18 +164,30 @@ __global__ void __launch_bounds__(32 * TOPK_WARPS)
   __syncwarp();
   int* ids_out = out.ids + i * K;
   float* mass_out = out.mass + i * K;
-  for (int j = lane; j < K; j += 32) {
-    const int id = sid[j];
-    int place = 0;
-    float m = 0.f;
-#pragma unroll 4
-    for (int q = 0; q < K; ++q) {
-      const int o = sid[q];
-      place += (o < id || (o == id && q < j)) ? 1 : 0;
-      m += o == id ? sp[q] : 0.f;
+  for (int j0 = lane; j0 < K; j0 += 128) {
+    int id[4], place[4] = {0, 0, 0, 0};
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) id[e] = j0 + 32 * e < K ? sid[j0 + 32 * e] : INT_MAX;
+    for (int q = 0; q < K; q += 4) {
+      const int4 o4 = *reinterpret_cast<const int4*>(sid + q);
+      const float4 p4 = *reinterpret_cast<const float4*>(sp + q);
+      const int o[4] = {o4.x, o4.y, o4.z, o4.w};
+      const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          place[e] += (o[f] < id[e] || (o[f] == id[e] && q + f < j0 + 32 * e)) ? 1 : 0;
+          m[e] += o[f] == id[e] ? p[f] : 0.f;
+        }
     }
-    ids_out[place] = live ? id : INT_MAX;
-    mass_out[place] = live && id != INT_MAX ? m : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j0 + 32 * e < K) {
+        ids_out[place[e]] = live ? id[e] : INT_MAX;
+        mass_out[place[e]] = live && id[e] != INT_MAX ? m[e] : 0.f;
+      }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) P += __shfl_xor_sync(0xffffffffu, P, off);
@@ -304,6 +338,29 @@ __global__ void __launch_bounds__(SMALL_THREADS)
     const int* ids = out.ids + i * K;
     const float* mass = out.mass + i * K;
     float* val = out.val + i * K;
+    // four partials and four entries of each lane in registers, all read at
+    // once: a row's time is the latency of its loads, one after another
+    float2 pr[4];
+    int idr[4];
+    bool newr[4];
+    float ur[4], pm[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int s = lane + 32 * e, j = lane + 32 * e;
+      pr[e] = s < S ? part[static_cast<idx_t>(s) * stride + static_cast<idx_t>(i)] : make_float2(-INFINITY, 0.f);
+      idr[e] = j < K ? ids[j] : INT_MAX;
+      newr[e] = j < K && (j == 0 || ids[j - 1] != idr[e]);
+      ur[e] = j < K ? val[j] : 0.f;
+      pm[e] = j < K ? mass[j] : 0.f;
+    }
+    // f(position, id's first entry, u, mass) for this lane's entries
+    auto entries = [&](auto&& f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (idr[e] != INT_MAX) f(lane + 32 * e, newr[e], ur[e], pm[e]);
+      for (int j = lane + 128; j < K; j += 32)
+        if (ids[j] != INT_MAX) f(j, ids[j - 1] != ids[j], val[j], mass[j]);
+    };
     if (!live && skipped) {
       if (lane == 0) {
         if (out_kl) out_kl[i] = 0.f;
@@ -314,27 +371,33 @@ __global__ void __launch_bounds__(SMALL_THREADS)
     } else {
       // the columns that are not listed: log2 maximum m2 and sum of 2^(. - m2)
       float m2 = -INFINITY;
-      for (int s = lane; s < S; s += 32) m2 = fmaxf(m2, part[static_cast<idx_t>(s) * stride + static_cast<idx_t>(i)].x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m2 = fmaxf(m2, pr[e].x);
+      for (int s = lane + 128; s < S; s += 32)
+        m2 = fmaxf(m2, part[static_cast<idx_t>(s) * stride + static_cast<idx_t>(i)].x);
       m2 = warp_max(m2);
       float rest = 0.f;
-      if (m2 > -INFINITY)
-        for (int s = lane; s < S; s += 32) {
+      if (m2 > -INFINITY) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rest += pr[e].y * exp2f(pr[e].x - m2);
+        for (int s = lane + 128; s < S; s += 32) {
           const float2 q = part[static_cast<idx_t>(s) * stride + static_cast<idx_t>(i)];
           rest += q.y * exp2f(q.x - m2);
         }
+      }
       rest = warp_sum(rest);
       // the listed ones, each id once, relative to the larger of the two maxima
       float mk = -INFINITY;
-      for (int j = lane; j < K; j += 32)
-        if (ids[j] != INT_MAX) mk = fmaxf(mk, val[j]);
+      entries([&](int, bool, float u, float) { mk = fmaxf(mk, u); });
       mk = warp_max(mk);
       // m2 ln 2 as a rounded product and its rest (ln 2 in two parts)
       const float2 rt = m2 > -INFINITY ? make_float2(m2 * kLn2, fmaf(m2, kLn2, -(m2 * kLn2)) + m2 * kLn2Low)
                                        : make_float2(-INFINITY, 0.f);
       const float A = fmaxf(rt.x, mk);
       float listed = 0.f;
-      for (int j = lane; j < K; j += 32)
-        if (ids[j] != INT_MAX && (j == 0 || ids[j - 1] != ids[j])) listed += expf(val[j] - A);
+      entries([&](int, bool first, float u, float) {
+        if (first) listed += expf(u - A);
+      });
       listed = warp_sum(listed);
       const float rest_A = rest > 0.f ? rest * expf((rt.x - A) + rt.y) : 0.f;
       const float total = rest_A + listed;
@@ -348,21 +411,19 @@ __global__ void __launch_bounds__(SMALL_THREADS)
       float P = st.x;
       if (P != P) {
         P = 0.f;
-        for (int j = lane; j < K; j += 32)
-          if (ids[j] != INT_MAX && (j == 0 || ids[j - 1] != ids[j])) P += mass[j];
+        entries([&](int, bool first, float, float p) {
+          if (first) P += p;
+        });
         P = warp_sum(P);
       }
       const float M = P + T;
       float kl = 0.f;
-      for (int j = lane; j < K; j += 32) {
-        const int id = ids[j];
-        if (id == INT_MAX) continue;
-        const float u = val[j], p = mass[j];
+      entries([&](int j, bool first, float u, float p) {
         const float lq = (u - A) - logtot;
-        if (p > 0.f && (j == 0 || ids[j - 1] != id)) kl = fmaf(p, logf(p) - lq, kl);
+        if (p > 0.f && first) kl = fmaf(p, logf(p) - lq, kl);
         const float fd = tf_softcap ? tf_d * (1.f - (u / tf_b) * (u / tf_b)) : tf_a;
         val[j] = w * fmaf(M, expf(lq), -p) * fd;
-      }
+      });
       kl = warp_sum(kl);
       if (lane == 0) {
         if (T > 0.f) kl += T * (logf(T) - (log_rest - logtot));
