@@ -104,6 +104,22 @@ cudaError_t launch_persistent(Kern k, int grid, int cluster, int threads, int sm
   return cudaGetLastError();
 }
 
+// A kernel that begins with dependent_start(), or with its wait.
+template <class Kern, class... Args>
+cudaError_t launch_dependent(Kern k, dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_on() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
 // The operand / output maps of one launch: (a, b, c) for every mode, (a2, b2,
 // c2) for the second operand set of the two-head and DHDW modes, (a3, b3, c3)
 // for the DLOGITS units of PIPE.  Unused ones repeat (a, b, c).
@@ -629,15 +645,11 @@ flce_status topk_rows(const TopkCall& c, bool kLong, const FwdPlan& f, const Gem
   ProfScope ps(K_TOPK, st);
   const unsigned grid = static_cast<unsigned>(ceil_div(rows, TOPK_ROWS));
   auto go = [&](auto kern) {
-    kern<<<grid, SMALL_THREADS, 0, st>>>(part, f.S, N, row0, rows, ri, c.K, c.tail, c.weights, c.rows, p.tf_softcap,
-                                         p.tf_a, p.tf_b, p.tf_d, skipped ? 1 : 0, c.out_kl, c.out_lse,
-                                         c.bsum + block0, c.bcnt + block0);
+    return launch_dependent(kern, dim3(grid), SMALL_THREADS, 0, st, part, f.S, N, row0, rows, ri, c.K, c.tail,
+                            c.weights, c.rows, p.tf_softcap, p.tf_a, p.tf_b, p.tf_d, skipped ? 1 : 0, c.out_kl,
+                            c.out_lse, c.bsum + block0, c.bcnt + block0);
   };
-  if (kLong)
-    go(topk_row_kernel<true>);
-  else
-    go(topk_row_kernel<false>);
-  FLCE_CUDA_TRY(cudaGetLastError());
+  FLCE_CUDA_TRY(kLong ? go(topk_row_kernel<true>) : go(topk_row_kernel<false>));
   return FLCE_OK;
 }
 
@@ -658,9 +670,8 @@ flce_status topk_gemv(const TopkCall& c, const GemmParams& p, const flce_bf16* h
     const size_t smem = static_cast<size_t>(nr) * p.H * 4;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGemvMaxSmem));
     if (e != cudaSuccess) return e;
-    kern<<<topk_gemv_ctas(p.V), 32 * TOPK_GEMV_WARPS, smem, st>>>(h, W, p.N, p.H, p.V, c.K, c.rows, p.tf_softcap,
-                                                                 p.tf_a, p.tf_b, part);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(topk_gemv_ctas(p.V)), 32 * TOPK_GEMV_WARPS, smem, st, h, W, p.N, p.H, p.V, c.K,
+                            c.rows, p.tf_softcap, p.tf_a, p.tf_b, part);
   };
   FLCE_CUDA_TRY(p.N == 1 ? go(topk_gemv_kernel<1>, 1) : p.N == 2 ? go(topk_gemv_kernel<2>, 2) : go(topk_gemv_kernel<4>, 4));
   return FLCE_OK;
@@ -674,14 +685,10 @@ flce_status topk_dlogits(const TopkCall& c, bool kLong, const GemmParams& p, uin
   const int steps = static_cast<int>(std::max<long long>(1, std::min<long long>(4, runs * rows / (16LL * device_sms()))));
   const dim3 grid(static_cast<unsigned>(ceil_div(runs, steps)), static_cast<unsigned>(rows));
   auto go = [&](auto kern) {
-    kern<<<grid, SMALL_THREADS, 0, st>>>(E, mx, p.ldD, p.ld_mx, steps, row0, ri, c.rows, c.K, n_valid, p.grad_scale,
-                                         p.out_count != nullptr, p.tf_softcap, p.tf_a, p.tf_b, p.tf_d);
+    return launch_dependent(kern, grid, SMALL_THREADS, 0, st, E, mx, p.ldD, p.ld_mx, steps, row0, ri, c.rows, c.K,
+                            n_valid, p.grad_scale, p.out_count != nullptr ? 1 : 0, p.tf_softcap, p.tf_a, p.tf_b, p.tf_d);
   };
-  if (kLong)
-    go(topk_dlogits_kernel<true>);
-  else
-    go(topk_dlogits_kernel<false>);
-  FLCE_CUDA_TRY(cudaGetLastError());
+  FLCE_CUDA_TRY(kLong ? go(topk_dlogits_kernel<true>) : go(topk_dlogits_kernel<false>));
   return FLCE_OK;
 }
 
@@ -692,8 +699,7 @@ flce_status topk_index(const TopkCall& c, int N, int* blk, int* idx, int* count,
     return list_valid_rows(reinterpret_cast<const int64_t*>(c.rows.mark), N, kMarkIgnored, blk, idx, count,
                            true, st);
   ProfScope ps(K_COMPACT, st);
-  topk_index_kernel<<<1, 1024, 0, st>>>(c.rows.mark, N, idx, count);
-  FLCE_CUDA_TRY(cudaGetLastError());
+  FLCE_CUDA_TRY(launch_dependent(topk_index_kernel, dim3(1), 1024, 0, st, c.rows.mark, N, idx, count));
   return FLCE_OK;
 }
 

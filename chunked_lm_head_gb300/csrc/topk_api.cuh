@@ -77,10 +77,9 @@ flce_status topk_lists(const flce_top_logits* t, const int64_t* targets, int64_t
   const TopkTeacher d{t->ids,     t->logits,   t->lse,         t->ld_ids, t->ld_logits,
                       t->ids_type, t->logits_type, t->k, t->tail};
   ProfScope ps(K_TOPK, st);
-  topk_list_kernel<<<static_cast<unsigned>(ceil_div(N, TOPK_WARPS)), 32 * TOPK_WARPS,
-                     static_cast<size_t>(TOPK_WARPS) * 2 * ((t->k + 3) & ~3) * 4, st>>>(
-      d, targets, ignore_index, static_cast<int>(N), static_cast<int>(V), rows);
-  FLCE_CUDA_TRY(cudaGetLastError());
+  FLCE_CUDA_TRY(launch_dependent(topk_list_kernel, dim3(static_cast<unsigned>(ceil_div(N, TOPK_WARPS))),
+                                 32 * TOPK_WARPS, static_cast<size_t>(TOPK_WARPS) * 2 * ((t->k + 3) & ~3) * 4, st, d,
+                                 targets, ignore_index, static_cast<int>(N), static_cast<int>(V), rows));
   return FLCE_OK;
 }
 
