@@ -574,7 +574,8 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
   const int workers = device_workers(cg);
   const int tm = BM * cg;
   // (dH through fp32 partials where its scale is completed in the reduction)
-  const FusedPlan fp = plan_fused(N, H, V, chunk_rows, workers, tm, topk && topk->split_scale);
+  const FusedPlan fp = plan_fused(N, H, V, chunk_rows, workers, tm,
+                                  !topk ? OneCall::kCe : topk->split_scale ? OneCall::kListedSplit : OneCall::kListed);
   if (!fp.fused || N == 0) {
     // forward (lse and n_valid into scratch when the caller wants neither),
     // then the tiled backward with grad_scale / n_valid on the device
@@ -817,8 +818,8 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
       }
     }
     if (topk) {  // (3) exponentials -> dlogits, in place
-      s = topk_dlogits(*topk, kLong, p, E, mx, static_cast<int>(row0), rows, compact ? cidx + row0 : nullptr, ccount,
-                       st);
+      s = topk_dlogits(*topk, kLong, p, E, mx, static_cast<int>(row0), rows, static_cast<int>(fp.lo),
+                       compact ? cidx + row0 : nullptr, ccount, st);
       if (s != FLCE_OK) return s;
     } else {
       ProfScope ps(K_DLOGITS, st);
@@ -838,12 +839,24 @@ static flce_status forward_backward_impl(const flce_bf16* h, const flce_bf16* W,
     // (4) dH[rows] = D W, dW (+)= D^T h[rows]; compacted: the block's
     // non-ignored rows, min(n_valid - row0, rows) read on the device
     if (compact) p.dyn_count = ccount;
+    // (dlogits in two parts: both parts' rows, against the rows of h twice; the
+    // parts of a dH row are sums of its reduction like the k-splits')
+    const int d_rows = fp.lo > 0 ? static_cast<int>(2 * fp.lo) : rows;
+    p.rows = d_rows;
+    p.dw_h_blocks = static_cast<int>(fp.lo / BK);
+    BwdPlan reduce = fp.b;
+    if (fp.lo > 0) {
+      reduce.dh_splits *= 2;
+      reduce.R = fp.lo;
+    }
+    DhDwStage finish = dhdw;
+    finish.plan = &reduce;
     CUtensorMap D_k, D_mn;
-    if (!make_map(&D_k, E, fp.ldD, rows, fp.ldD, BK, BM) || !make_map(&D_mn, E, fp.ldD, rows, fp.ldD, 64, BK))
+    if (!make_map(&D_k, E, fp.ldD, d_rows, fp.ldD, BK, BM) || !make_map(&D_mn, E, fp.ldD, d_rows, fp.ldD, 64, BK))
       return FLCE_ERR_CUDA;
-    s = slab_dh_dw(dhdw, p, rows, block, 0, 0, static_cast<int>(V), D_k, D_mn, compact ? hc_mn : h_mn, st);
+    s = slab_dh_dw(dhdw, p, d_rows, block, 0, 0, static_cast<int>(V), D_k, D_mn, compact ? hc_mn : h_mn, st);
     if (s != FLCE_OK) return s;
-    s = block_dh_finish(dhdw, p.row0, rows, compact ? cidx : nullptr, compact ? ccount : nullptr,
+    s = block_dh_finish(finish, p.row0, rows, compact ? cidx : nullptr, compact ? ccount : nullptr,
                         static_cast<int>(row0), st);
     if (s != FLCE_OK) return s;
   }

@@ -79,6 +79,7 @@ constexpr long long DRAIN_LIMIT_CYCLES = 400000000LL;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2f = 0.6931471805599453f;
+constexpr float kExpScale = 32768.f;  // of the listed forward's fp16 exponentials
 
 enum Mode : int {
   MODE_FWD = 0,
@@ -270,6 +271,8 @@ struct GemmParams {
   int sp_k;
   // bf16 dW: what the dlogits' power-of-two scale leaves of grad_scale / count
   const int* out_count;
+  // DW: the rows of h repeat after this many K blocks (0: they do not)
+  int dw_h_blocks;
   int ld_mx;  // FUSED_FWD with listed columns: row pitch of mx, a multiple of 8 that covers whole tiles
 };
 
@@ -708,11 +711,12 @@ __device__ __forceinline__ void load_stage(const CUtensorMap* tA, const CUtensor
     static_assert(MODE == MODE_DW, "every mode needs its operand loads");
     // A = D^T (vocabulary contiguous: MN-major), B = h (hidden contiguous:
     // MN-major); K runs over the chunk's rows
+    const int hb = p.dw_h_blocks > 0 && kb >= p.dw_h_blocks ? kb - p.dw_h_blocks : kb;
 #pragma unroll
     for (int j = 0; j < 2; ++j) tma_ld<MODE, CG>(sA + j * MN_BOX_BYTES, tA, bar, a0 + 64 * j, doff + kb * BK);
 #pragma unroll
     for (int j = 0; j < C::B_ROWS / 64; ++j)
-      tma_ld<MODE, CG>(sB + j * MN_BOX_BYTES, tB, bar, b0 + 64 * j, p.row0 + kb * BK);
+      tma_ld<MODE, CG>(sB + j * MN_BOX_BYTES, tB, bar, b0 + 64 * j, p.row0 + hb * BK);
   }
 }
 
@@ -1262,9 +1266,10 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
             if constexpr (MODE == MODE_FUSED_FWD && kSp) {
               // the stored exponentials, 2^(u log2e - chunk max), summed as they
               // are formed: one exponential per column instead of two.  Stored in
-              // fp16, whose 11 bits suit values of at most one: their rounding is
-              // an eighth of the dlogits' own (what falls below 2^-25 of the
-              // chunk's largest is lost)
+              // fp16 times kExpScale: 11 bits down to 2^-29 of the chunk's
+              // largest, an eighth of the dlogits' own rounding (what falls below
+              // 2^-40 is lost).  The product comes after the exponential, whose
+              // argument keeps its bits only near zero
               const float cmL = cm * l2a;
               float a = 0.f;
               uint32_t pk[16];
@@ -1273,7 +1278,8 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                 const float e0 = cm == -INFINITY ? 0.f : ex2_approx(fmaf(v[j], l2a, -cmL));
                 const float e1 = cm == -INFINITY ? 0.f : ex2_approx(fmaf(v[j + 1], l2a, -cmL));
                 a += e0 + e1;
-                pk[j / 2] = pack_f16x2(e0, e1);
+                const float2 es = mul2(make_float2(e0, e1), both(kExpScale));
+                pk[j / 2] = pack_f16x2(es.x, es.y);
               }
               if (nm != -INFINITY) {
                 run_s = run_s * ex2_approx(run_m - nm) + a * ex2_approx(cmL - nm);

@@ -679,16 +679,19 @@ flce_status topk_gemv(const TopkCall& c, const GemmParams& p, const flce_bf16* h
 
 // The dlogits of one row block of the one-call step, listed columns included.
 flce_status topk_dlogits(const TopkCall& c, bool kLong, const GemmParams& p, uint16_t* E, const float* mx, int row0,
-                         int rows, const int* ri, const int* n_valid, cudaStream_t st) {
+                         int rows, int lo, const int* ri, const int* n_valid, cudaStream_t st) {
   ProfScope ps(K_DLOGITS, st);
   const long long runs = ceil_div(p.ldD, TOPK_DL_COLS);
   const int steps = static_cast<int>(std::max<long long>(1, std::min<long long>(4, runs * rows / (16LL * device_sms()))));
-  const dim3 grid(static_cast<unsigned>(ceil_div(runs, steps)), static_cast<unsigned>(rows));
+  const dim3 grid(static_cast<unsigned>(ceil_div(runs, steps)), static_cast<unsigned>(std::max(rows, lo)));
   auto go = [&](auto kern) {
-    return launch_dependent(kern, grid, SMALL_THREADS, 0, st, E, mx, p.ldD, p.ld_mx, steps, row0, ri, c.rows, c.K,
+    return launch_dependent(kern, grid, SMALL_THREADS, 0, st, E, mx, p.ldD, p.ld_mx, steps, row0, rows, lo, ri, c.rows, c.K,
                             n_valid, p.grad_scale, p.out_count != nullptr ? 1 : 0, p.tf_softcap, p.tf_a, p.tf_b, p.tf_d);
   };
-  FLCE_CUDA_TRY(kLong ? go(topk_dlogits_kernel<true>) : go(topk_dlogits_kernel<false>));
+  if (lo > 0)
+    FLCE_CUDA_TRY(kLong ? go(topk_dlogits_kernel<true, true>) : go(topk_dlogits_kernel<false, true>));
+  else
+    FLCE_CUDA_TRY(kLong ? go(topk_dlogits_kernel<true, false>) : go(topk_dlogits_kernel<false, false>));
   return FLCE_OK;
 }
 

@@ -521,7 +521,26 @@ struct FusedPlan {
   long long R = 0, ldD = 0;
   FwdPlan f;
   BwdPlan b;  // dH / dW stages over one slab of V columns
+  // few rows of the listed step: the dlogits in two bf16 parts, the second in
+  // rows [lo, 2 lo) of the buffer (0: one part)
+  long long lo = 0;
 };
+// Whose one-call step a plan is for: the cross-entropy's; or the listed
+// distillation's, with its dlogits' scale whole, or split (split_scale), which
+// dH's reduction from fp32 partials completes.
+enum class OneCall { kCe, kListed, kListedSplit };
+// Rows of a part of the dlogits, 0 where they take one.  Up to half a 256-row
+// tile the second part's rows are rows of the tile that would be empty, in dH,
+// and K blocks under the write of dW.  With so few rows one entry often holds
+// most of a gradient, whose bf16 rounding would be the whole gradient's: drawn
+// cases of 1 to 128 rows came out up to 2.3 times as far from the gradients in
+// 64 bits as bf16 outputs have to be (more rows: 1.3 to 1.6 times); in two
+// parts none is further off than its outputs' rounding.  64 rows x 2,048 x
+// 50,000 take 173 us for 166, 128 x 4,096 x 151,936 766 for 711.
+long long fused_lo_rows(long long N, long long chunk_rows) {
+  const long long lo = round_up(std::max(1LL, N), BK);
+  return lo <= BM && 2 * lo <= round_up(std::max(1LL, chunk_rows), BM) ? lo : 0;
+}
 
 // Rows of the one-call block, 0 where the budget is too small for it.
 long long fused_rows(long long N, long long chunk_rows) {
@@ -534,7 +553,7 @@ long long fused_rows(long long N, long long chunk_rows) {
 }
 
 FusedPlan plan_fused(long long N, long long H, long long V, long long chunk_rows, int workers, int tm,
-                     bool dh_f32 = false) {
+                     OneCall call = OneCall::kCe) {
   FusedPlan fp;
   N = std::max(1LL, N);
   fp.R = fused_rows(N, chunk_rows);
@@ -542,6 +561,8 @@ FusedPlan plan_fused(long long N, long long H, long long V, long long chunk_rows
   fp.fused = fp.R > 0;
   if (!fp.fused) return fp;
   fp.f = plan_forward(fp.R, H, V, workers, tm, kFwdPartialsCap, N);
+  if (call != OneCall::kCe) fp.lo = fused_lo_rows(N, chunk_rows);
+  if (fp.lo > 0) fp.R = std::max(fp.R, 2 * fp.lo);
   fp.b.R = fp.R;
   fp.b.Vs = V;
   fp.b.n_slabs = 1;
@@ -551,7 +572,7 @@ FusedPlan plan_fused(long long N, long long H, long long V, long long chunk_rows
   int sp = dh_split_count(ceil_div(fp.R, tm) * ceil_div(H, fp.b.dh_wide ? 2 * BN : BN), kb, workers);
   fp.b.dh_kb_per_split = static_cast<int>(ceil_div(kb, sp));
   fp.b.dh_splits = static_cast<int>(ceil_div(kb, fp.b.dh_kb_per_split));
-  fp.b.dh_f32 = dh_f32 || fp.b.dh_splits > 1;
+  fp.b.dh_f32 = call == OneCall::kListedSplit || fp.lo > 0 || fp.b.dh_splits > 1;
   return fp;
 }
 

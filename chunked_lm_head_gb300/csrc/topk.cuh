@@ -458,38 +458,50 @@ __global__ void __launch_bounds__(SMALL_THREADS)
 }
 
 // dlogits of one row block of the one-call step, in place: the forward's
-// fp16 exponentials E = 2^(u log2 e - chunk max) (0 in the listed columns and
+// fp16 exponentials E = 2^(u log2 e - chunk max) kExpScale (0 in the listed columns and
 // past the vocabulary) become the bf16
-//   D = E 2^(chunk max - lse_rest) coef g f'(z),  g = grad_scale / max(n_valid, 1)
+//   D = E / kExpScale 2^(chunk max - lse_rest) coef g f'(z),  g = grad_scale / max(n_valid, 1)
 // (split: g's power of two),
 // then the listed columns get theirs.  A CTA takes `steps` runs of
 // TOPK_DL_COLS columns of a row (blockIdx.y), a lane 8 neighbouring columns at
 // a time, so that a warp's 16-byte accesses are contiguous.  Rows as
-// fused_dlogits_kernel.
+// fused_dlogits_kernel.  kLo: D in two parts, what the first one's rounding
+// leaves out lo rows further on; the rows from `count` to lo are zeroed.
 constexpr int TOPK_DL_COLS = SMALL_THREADS * 32;
 
-template <bool kLong>
+// What the bf16 pair w = (x, y) leaves out of x and y, as a bf16 pair
+// (nothing of values that are not finite).
+__device__ __forceinline__ uint32_t bf16x2_rest(float x, float y, uint32_t w) {
+  const float rx = x - __uint_as_float(w << 16), ry = y - __uint_as_float(w & 0xffff0000u);
+  return pack_bf16x2(rx - rx == 0.f ? rx : 0.f, ry - ry == 0.f ? ry : 0.f);
+}
+
+template <bool kLong, bool kLo>
 __global__ void __launch_bounds__(SMALL_THREADS)
     topk_dlogits_kernel(uint16_t* __restrict__ E, const float* __restrict__ mx, int ldD, int ld_mx, int steps, int row0,
-                        const int* __restrict__ ri, const TopkRows rows, int K, const int* __restrict__ n_valid,
+                        int count, int lo, const int* __restrict__ ri, const TopkRows rows, int K, const int* __restrict__ n_valid,
                         float grad_scale, int split, int tf_softcap, float tf_a, float tf_b, float tf_d) {
   dependent_start();
   using idx_t = typename std::conditional<kLong, long long, int>::type;
   const int r = blockIdx.y;
   const int n = *n_valid;
   if (ri != nullptr && r >= (n - row0 + 63) / 64 * 64) return;  // row0: the block's first position
-  const long long i = ri ? ri[r] : row0 + r;
+  const bool inside = !kLo || r < count;
+  const long long i = !inside ? 0 : ri ? ri[r] : row0 + r;
   const float g = split ? split_scale(grad_scale, n_valid).pow2 : grad_scale / fmaxf(1.f, static_cast<float>(n));
-  const bool live = rows.mark[i] >= 0;
+  const bool live = inside && rows.mark[i] >= 0;
   const float scale = live ? rows.coef[i] * g : 0.f;
   uint16_t* row = E + static_cast<idx_t>(r) * ldD;
+  uint16_t* row2 = row + static_cast<idx_t>(lo) * ldD;
   const float* rmx = mx + static_cast<idx_t>(r) * ld_mx;
   const int c0 = blockIdx.x * steps * TOPK_DL_COLS;
   const int c1 = min(ldD, c0 + steps * TOPK_DL_COLS);
   const int first = c0 + (threadIdx.x >> 5) * 1024 + (threadIdx.x & 31) * 8;
   if (scale == 0.f) {  // a row without loss or weight, whose exponentials may never have been written
-    for (int c = c0 + threadIdx.x * 8; c < c1; c += SMALL_THREADS * 8)
+    for (int c = c0 + threadIdx.x * 8; c < c1; c += SMALL_THREADS * 8) {
       *reinterpret_cast<uint4*>(row + c) = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (kLo) *reinterpret_cast<uint4*>(row2 + c) = make_uint4(0u, 0u, 0u, 0u);
+    }
   } else {
     const float nlse2 = -rows.lse_rest[i] * kLog2e;
     for (int cs = first; cs < c1; cs += TOPK_DL_COLS) {
@@ -508,25 +520,31 @@ __global__ void __launch_bounds__(SMALL_THREADS)
         const int c = cs + k * 256;
         if (c >= c1) continue;
         uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-        const float kf = ex2_approx(cm[k] + nlse2) * scale;
+        uint32_t w2[4];
+        const float kf = ex2_approx(cm[k] + nlse2) * scale * (1.f / kExpScale);
         if (!tf_softcap) {
           const float2 f = both(kf * tf_a);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 d = mul2(__half22float2(*reinterpret_cast<const __half2*>(&w[e])), f);
             w[e] = pack_bf16x2(d.x, d.y);
+            if constexpr (kLo) w2[e] = bf16x2_rest(d.x, d.y, w[e]);
           }
         } else {  // u = ln(E) + chunk max, tanh(a z) = u / b
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 ev = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-            const float lo = ev.x, hi = ev.y;
-            const float ul = (__log2f(lo) + cm[k]) * kLn2 / tf_b, uh = (__log2f(hi) + cm[k]) * kLn2 / tf_b;
-            w[e] = pack_bf16x2(lo > 0.f ? lo * kf * tf_d * (1.f - ul * ul) : 0.f,
-                               hi > 0.f ? hi * kf * tf_d * (1.f - uh * uh) : 0.f);
+            const float el = ev.x, eh = ev.y;
+            const float ul = (__log2f(el * (1.f / kExpScale)) + cm[k]) * kLn2 / tf_b;
+            const float uh = (__log2f(eh * (1.f / kExpScale)) + cm[k]) * kLn2 / tf_b;
+            const float dl = el > 0.f ? el * kf * tf_d * (1.f - ul * ul) : 0.f;
+            const float dh = eh > 0.f ? eh * kf * tf_d * (1.f - uh * uh) : 0.f;
+            w[e] = pack_bf16x2(dl, dh);
+            if constexpr (kLo) w2[e] = bf16x2_rest(dl, dh, w[e]);
           }
         }
         *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (kLo) *reinterpret_cast<uint4*>(row2 + c) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
       }
     }
   }
@@ -534,8 +552,12 @@ __global__ void __launch_bounds__(SMALL_THREADS)
   __syncthreads();  // the listed columns after the CTA's own stores
   for (int j = threadIdx.x; j < K; j += SMALL_THREADS) {
     const int id = rows.ids[i * K + j];
-    if (id >= c0 && id < c1 && id != INT_MAX)
-      row[id] = static_cast<uint16_t>(pack_bf16x2(rows.val[i * K + j] * g, 0.f) & 0xffffu);
+    if (id >= c0 && id < c1 && id != INT_MAX) {
+      const float d = rows.val[i * K + j] * g;
+      const uint32_t w = pack_bf16x2(d, 0.f);
+      row[id] = static_cast<uint16_t>(w & 0xffffu);
+      if constexpr (kLo) row2[id] = static_cast<uint16_t>(bf16x2_rest(d, 0.f, w) & 0xffffu);
+    }
   }
 }
 

@@ -154,7 +154,8 @@ size_t flce_topk_kd_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, in
 static size_t topk_one_call_inner(int64_t N, int64_t H, int64_t V, int64_t chunk_rows, bool split) {
   const int cg = cta_group();
   const int workers = device_workers(cg);
-  const FusedPlan fp = plan_fused(N, H, V, chunk_rows, workers, BM * cg, split);
+  const FusedPlan fp = plan_fused(N, H, V, chunk_rows, workers, BM * cg,
+                                  split ? OneCall::kListedSplit : OneCall::kListed);
   return align256(fp.fused && N > 0 ? fused_layout(N, H, fp).total
                                     : fallback_workspace(N, H, V, chunk_rows, workers, BM * cg));
 }
@@ -291,7 +292,7 @@ flce_status flce_topk_kd_forward_backward(const flce_bf16* h, const flce_bf16* W
   const int* count = nullptr;
   if (split) {
     const int cg = cta_group();
-    const FusedPlan fp = plan_fused(N, H, V, chunk_rows, device_workers(cg), BM * cg, true);
+    const FusedPlan fp = plan_fused(N, H, V, chunk_rows, device_workers(cg), BM * cg, OneCall::kListedSplit);
     count = reinterpret_cast<const int*>(wb + fused_layout(N, H, fp).count);
   }
   return topk_round_dw(sum, V * H, dW, count, grad_scale, st);

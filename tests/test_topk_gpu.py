@@ -347,3 +347,21 @@ def test_no_counted_row_of_a_wide_vocabulary():
                                         dW_dtype=torch.bfloat16)
     assert _lib.flce_device_status() == 0
     assert not got["dW"].any() and not got["dH"].any() and int(got["n_valid"]) == 0
+
+
+@pytest.mark.parametrize("options", [{}, {"cta_group": 1}])
+@pytest.mark.parametrize("N,H,V,K,mask", [(1, 64, 1691, 1, False), (3, 760, 5003, 8, True), (64, 136, 3000, 16, False),
+                                          (65, 264, 2049, 5, True), (128, 64, 4097, 40, False)])
+def test_few_rows_take_their_dlogits_in_two_parts(N, H, V, K, mask, options):
+    """dlogits of 16 bits and more: what is left is the rounding of the fp16
+    exponentials, half a step of 2^-10 (a quarter of bf16's half step covers it
+    and the fp32 sums), where one bf16 rounding is 2^-8."""
+    c = make(N, H, V, K, seed=13, whole=True, mask=mask, weights=mask)
+    ref = R.reference(**c, tail=True)
+    args = (c["h"], c["W"], c["ids"], c["logits"], c["lse_t"], c["targets"], c["weights"], True)
+    with _lib.options(**options):
+        got = flce.topk_kd_forward_backward(*args, chunk_rows=4096)
+        half = flce.topk_kd_forward_backward(*args, chunk_rows=4096, dW_dtype=torch.bfloat16)
+    assert _lib.flce_device_status() == 0
+    R.check(got, ref, roundings=0.25)
+    R.check(half, ref, roundings=0.25)
