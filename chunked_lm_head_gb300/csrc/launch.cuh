@@ -104,6 +104,11 @@ cudaError_t launch_persistent(Kern k, int grid, int cluster, int threads, int sm
   return cudaGetLastError();
 }
 
+// Most rows of the norm and of the distillation from top logits: their kernels
+// count rows in 32 bits, and past the last one up to a tile, a CTA's rows or
+// two strides of the norm backward's grid (15 groups on two CTAs to an SM).
+constexpr int64_t kMaxRows = INT_MAX - 65536;
+
 // A kernel that begins with dependent_start(), or with its wait.
 template <class Kern, class... Args>
 cudaError_t launch_dependent(Kern k, dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {

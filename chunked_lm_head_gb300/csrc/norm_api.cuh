@@ -11,7 +11,7 @@ using namespace flce;
 // Longest row: 4 vectors of 8 elements on each of 1,024 threads.
 constexpr int64_t kNormMaxH = 32768;
 
-bool norm_sizes_ok(int64_t N, int64_t H) { return N >= 0 && H > 0 && N < INT_MAX && H < INT_MAX; }
+bool norm_sizes_ok(int64_t N, int64_t H) { return N >= 0 && H > 0 && N <= kMaxRows && H < INT_MAX; }
 bool norm_dtype_ok(int32_t t) { return t == FLCE_BF16 || t == FLCE_F32; }
 
 // Threads of a row's group for VPT vectors of 8 elements to a thread.

@@ -6,6 +6,8 @@
 
 namespace {
 
+bool topk_sizes_ok(int64_t N, int64_t H, int64_t V) { return sizes_ok(N, H, V) && N <= kMaxRows; }
+
 bool topk_teacher_ok(const flce_top_logits* t) {
   if (t == nullptr || t->k < 1) return false;
   if (t->ids_type != FLCE_I32 && t->ids_type != FLCE_I64) return false;
@@ -62,7 +64,7 @@ TopkRows topk_rows_at(const TopkLayout& L, uint8_t* state, uint8_t* scratch) {
 // The checks of a call that takes a teacher.
 flce_status topk_check(const flce_top_logits* t, const int64_t* targets, const float* weights, int64_t N, int64_t H,
                        int64_t V) {
-  if (!sizes_ok(N, H, V) || !topk_teacher_ok(t)) return FLCE_ERR_INVALID_ARG;
+  if (!topk_sizes_ok(N, H, V) || !topk_teacher_ok(t)) return FLCE_ERR_INVALID_ARG;
   if (N > 0 && (!t->ids || !t->logits || t->ld_ids < t->k || t->ld_logits < t->k)) return FLCE_ERR_INVALID_ARG;
   if (t->k > TOPK_MAX_K) return FLCE_ERR_UNSUPPORTED;
   if (!aligned(t->ids, t->ids_type == FLCE_I64 ? 8 : 4) || !aligned(t->logits, t->logits_type == FLCE_F32 ? 4 : 2) ||
@@ -134,17 +136,17 @@ flce_status flce_scale_grads_bf16(flce_bf16* dH, int64_t n_dH, flce_bf16* dW, in
 }
 
 size_t flce_topk_kd_state_bytes(int64_t N, int64_t k) {
-  if (N < 0 || N >= INT_MAX || k < 1 || k > TOPK_MAX_K) return 0;
+  if (N < 0 || N > kMaxRows || k < 1 || k > TOPK_MAX_K) return 0;
   return topk_layout(N, k).state;
 }
 
 size_t flce_topk_kd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k, int64_t chunk_rows) {
-  if (!sizes_ok(N, H, V) || k < 1 || k > TOPK_MAX_K) return 0;
+  if (!topk_sizes_ok(N, H, V) || k < 1 || k > TOPK_MAX_K) return 0;
   return align256(flce_workspace_bytes(N, H, V, chunk_rows)) + topk_layout(N, k).total;
 }
 
 size_t flce_topk_kd_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t chunk_rows, int32_t dW_type) {
-  if (!sizes_ok(N, H, V)) return 0;
+  if (!topk_sizes_ok(N, H, V)) return 0;
   return align256(flce_workspace_bytes(N, H, V, chunk_rows)) +
          topk_grad(dW_type, N, H, V, topk_bwd_rows(N, H, V, chunk_rows)).bytes;
 }
@@ -162,7 +164,7 @@ static size_t topk_one_call_inner(int64_t N, int64_t H, int64_t V, int64_t chunk
 
 size_t flce_topk_kd_forward_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k, int64_t chunk_rows,
                                                      int32_t dW_type) {
-  if (!sizes_ok(N, H, V) || k < 1 || k > TOPK_MAX_K) return 0;
+  if (!topk_sizes_ok(N, H, V) || k < 1 || k > TOPK_MAX_K) return 0;
   // (a call without dW needs what one with a bf16 dW does)
   return std::max(topk_one_call_inner(N, H, V, chunk_rows, true),
                   dW_type == FLCE_F32 ? topk_one_call_inner(N, H, V, chunk_rows, false) : 0) +
@@ -214,7 +216,7 @@ flce_status flce_topk_kd_backward(const flce_bf16* h, const flce_bf16* W, const 
                                   int64_t N, int64_t H, int64_t V, int64_t k, int64_t chunk_rows,
                                   const flce_logit_transform* transform, void* workspace, size_t workspace_bytes,
                                   void* stream) {
-  if (!sizes_ok(N, H, V) || k < 1 || (N > 0 && !state) || !topk_dw_ok(dW, dW_type)) return FLCE_ERR_INVALID_ARG;
+  if (!topk_sizes_ok(N, H, V) || k < 1 || (N > 0 && !state) || !topk_dw_ok(dW, dW_type)) return FLCE_ERR_INVALID_ARG;
   GemmParams tfp{};
   if (!transform_params(transform, tfp) || (!dH && !dW) || (N > 0 && (!h || !W))) return FLCE_ERR_INVALID_ARG;
   if (k > TOPK_MAX_K || H % 8 != 0 || !aligned(state, 256) || !aligned(dW, 16) || !aligned(dH, 16) || !aligned(h, 16) ||

@@ -465,6 +465,7 @@ FLCE_API flce_status flce_jsd_backward_ex2(const flce_bf16* h_s, const flce_bf16
  *   lse     [N] fp32, the log-sum-exp of the teacher's whole row (0 for
  *           log-probs), or NULL: the list's mass is scaled to one.
  *   k       1..1,024 entries per row (ld_ids, ld_logits >= k).
+ *   N       at most 2^31 - 65,537 (rows are counted in 32 bits).
  *   tail    1: the mass outside the list is one more outcome, for teacher and
  *           student alike (needs lse); 0: it takes no part.
  */
@@ -659,7 +660,8 @@ FLCE_API flce_status flce_forward_e4m3(const uint8_t* h8, const float* h_scale, 
  *   out_y    [N,H] bf16, contiguous.  out_rstd [N] fp32 or NULL
  *            (flce_rms_norm_backward needs it).
  * H <= 32,768 and a multiple of 8 (e4m3: of 16), arrays 16-byte aligned, row
- * strides of whole 16 bytes, else FLCE_ERR_UNSUPPORTED.
+ * strides of whole 16 bytes, else FLCE_ERR_UNSUPPORTED.  N <= 2^31 - 65,537
+ * (rows are counted in 32 bits), else FLCE_ERR_INVALID_ARG.
  *
  * flce_rms_norm_e4m3 gives the operands of flce_forward_e4m3 instead of y:
  * out_scale[i] = max_j |y_ij| / 448 (1 for an all-zero row and for one that
