@@ -117,6 +117,8 @@ def rms_norm_backward(dy, s, weight, rstd, ds=None, weight_offset: float = 0.0, 
         raise ValueError("dy must be contiguous")
     if ds is not None and (not ds.is_cuda or ds.dtype != s.dtype or ds.shape != s.shape or not ds.is_contiguous()):
         raise ValueError("ds must be a contiguous CUDA tensor of s's shape and type")
+    if workspace is not None and not workspace.is_cuda:
+        raise ValueError("workspace must be a CUDA tensor")
     return _norm_grads(dy, s, lds, weight, rstd, ds, weight_offset, need_dx, need_dr, need_dweight, workspace, stream)
 
 

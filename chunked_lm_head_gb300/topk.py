@@ -29,6 +29,8 @@ def _workspace(workspace, nbytes, stream, device):
         if stream is not None:
             return None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif not workspace.is_cuda:
+        raise ValueError("workspace must be a CUDA tensor")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -56,6 +58,13 @@ def _check(h, W, ids, logits, lse_t, targets, weights, tail):
     ld = [x.stride(0) if N > 1 else K for x in (ids, logits)]
     return _lib.TopLogits(ids.data_ptr(), logits.data_ptr(), _lib._ptr(lse_t), ld[0], ld[1], _IDS[ids.dtype],
                           _LOGITS[logits.dtype], K, 1 if tail else 0)
+
+
+def _check_state(state, N, k):
+    if state is None or state.numel() * state.element_size() != _lib.flce_topk_kd_state_bytes(N, k):
+        raise ValueError("state must come from topk_kd_forward(for_backward=True) of the same N and k")
+    if not state.is_cuda or not state.is_contiguous():
+        raise ValueError("state must be a contiguous CUDA tensor")
 
 
 def topk_kd_forward(h, W, ids, logits, lse_t=None, targets=None, weights=None, tail: bool = False,
@@ -98,8 +107,7 @@ def topk_kd_backward(h, W, state, k: int, grad_scale: float, chunk_rows: int = 2
     (N, H), V, dev = h.shape, W.shape[0], h.device
     if W.shape[1] != H or any(not x.is_cuda or x.dtype != torch.bfloat16 or not x.is_contiguous() for x in (h, W)):
         raise ValueError("h[N,H] and W[V,H] must be contiguous bfloat16 CUDA tensors")
-    if state is None or state.numel() * state.element_size() != _lib.flce_topk_kd_state_bytes(N, k):
-        raise ValueError("state must come from topk_kd_forward(for_backward=True) of the same N and k")
+    _check_state(state, N, k)
     dH = torch.empty_like(h) if need_dH else None
     dW = torch.empty((V, H), dtype=dW_dtype, device=dev) if need_dW else None
     scale = _device_scalar(scale, torch.float32, dev)
