@@ -997,7 +997,12 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
         if (u < 0) break;
         const Unit t = decode_unit<MODE, C::TM>(p, dsh, u);
         for (int n = t.n0; n < t.n1 && ok; ++n) {
-          if (!wait_bar(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.err)) {
+          // (the epilogues that hand tensor memory back by a relaxed arrive of
+          // either CTA are waited for at cluster scope)
+          const bool drained = CG == 2 && (kOut16 || kSp)
+                                   ? wait_bar_cluster(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.err)
+                                   : wait_bar(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.err);
+          if (!drained) {
             ok = false;
             break;
           }

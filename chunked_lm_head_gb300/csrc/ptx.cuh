@@ -218,12 +218,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
-// The same for a barrier that only hands tensor memory back (the reads are
-// ordered by tcgen05.wait::ld and tcgen05.fence): released at CTA scope, so
-// that it does not wait until the thread's shared-memory writes and output
-// copies are visible across the cluster.
+// The same for a barrier that only hands tensor memory back, PTX's pattern for
+// ordering tcgen05 operations of different threads: the reader's loads have
+// returned (tcgen05.wait::ld) and are ordered before this arrive by
+// tcgen05.fence::before_thread_sync, the issuer's next MMA after its wait by
+// tcgen05.fence::after_thread_sync.  Arrive and wait are at cluster scope,
+// which covers both CTAs; the arrive orders no other memory (relaxed), so it
+// does not wait until the thread's shared-memory writes and output copies are
+// visible across the cluster.
 __device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // TMA load into this CTA's shared memory whose completion is counted on an
