@@ -1286,7 +1286,9 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                 const float2 es = mul2(make_float2(e0, e1), both(kExpScale));
                 pk[j / 2] = pack_f16x2(es.x, es.y);
               }
-              if (nm != -INFINITY) {
+              // (a NaN sum, also of a chunk that is NaN throughout and has no
+              // maximum, stays one)
+              if (nm != -INFINITY || a != a) {
                 run_s = run_s * ex2_approx(run_m - nm) + a * ex2_approx(cmL - nm);
                 run_m = nm;
               }
@@ -1321,6 +1323,8 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
               for (int j = 0; j < 32; ++j) a += ex2_approx(fmaf(v[j], l2a, -nm));
               run_s = run_s * ex2_approx(run_m - nm) + a;
               run_m = nm;
+            } else if (kSp && cm != cm) {
+              run_s = cm;  // NaN throughout, without a maximum so far
             }
             if constexpr (MODE == MODE_FUSED_FWD && !kSp) {
               // 2^(u log2e - chunk max) in [0, 1] as bf16, and the chunk max,

@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS, TOPK_GEMV_CTAS)
         for (; at < K && ids[at] == v; ++at) val[at] = u;
       } else {
         const float u2 = u * kLog2e, nm = fmaxf(m, u2);
-        if (nm > -INFINITY) {
+        if (u2 != -INFINITY) {  // (a NaN, which the maximum passes over, stays in the sum)
           s = s * exp2f(m - nm) + exp2f(u2 - nm);
           m = nm;
         }
@@ -324,9 +324,9 @@ __global__ void __launch_bounds__(32 * TOPK_GEMV_WARPS, TOPK_GEMV_CTAS)
     float M = -INFINITY, S = 0.f;
     for (int i = 0; i < TOPK_GEMV_WARPS; ++i)
       for (int c = 0; c < 4; ++c) M = fmaxf(M, merged[i][lane + c].x);
-    if (M > -INFINITY)
-      for (int i = 0; i < TOPK_GEMV_WARPS; ++i)
-        for (int c = 0; c < 4; ++c) S += merged[i][lane + c].y * exp2f(merged[i][lane + c].x - M);
+    const float base = M > -INFINITY ? M : 0.f;  // (sums without a maximum are 0 or NaN)
+    for (int i = 0; i < TOPK_GEMV_WARPS; ++i)
+      for (int c = 0; c < 4; ++c) S += merged[i][lane + c].y * exp2f(merged[i][lane + c].x - base);
     part[static_cast<long long>(blockIdx.x) * N + my_r] = make_float2(M, S);
   }
 }
@@ -391,14 +391,14 @@ __global__ void __launch_bounds__(SMALL_THREADS)
       for (int s = lane + 128; s < S; s += 32)
         m2 = fmaxf(m2, part[static_cast<idx_t>(s) * stride + static_cast<idx_t>(i)].x);
       m2 = warp_max(m2);
+      // (a partial without a maximum is 0 or, of logits that are no numbers, NaN)
+      const float base2 = m2 > -INFINITY ? m2 : 0.f;
       float rest = 0.f;
-      if (m2 > -INFINITY) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rest += pr[e].y * exp2f(pr[e].x - m2);
-        for (int s = lane + 128; s < S; s += 32) {
-          const float2 q = part[static_cast<idx_t>(s) * stride + static_cast<idx_t>(i)];
-          rest += q.y * exp2f(q.x - m2);
-        }
+      for (int e = 0; e < 4; ++e) rest += pr[e].y * exp2f(pr[e].x - base2);
+      for (int s = lane + 128; s < S; s += 32) {
+        const float2 q = part[static_cast<idx_t>(s) * stride + static_cast<idx_t>(i)];
+        rest += q.y * exp2f(q.x - base2);
       }
       rest = warp_sum(rest);
       // the listed ones, each id once, relative to the larger of the two maxima
@@ -414,13 +414,14 @@ __global__ void __launch_bounds__(SMALL_THREADS)
         if (first) listed += expf(u - A);
       });
       listed = warp_sum(listed);
-      const float rest_A = rest > 0.f ? rest * expf((rt.x - A) + rt.y) : 0.f;
+      // (no rest: exactly 0; a NaN goes on into lse and kl)
+      const float rest_A = rest != 0.f ? rest * expf((rt.x - A) + rt.y) : 0.f;
       const float total = rest_A + listed;
       const float logtot = logf(total);
       const float log_rest = ((rt.x - A) + rt.y) + logf(rest);  // relative to A; -inf where there is no rest
-      const float R = rest > 0.f ? rest_A / total : 0.f;
+      const float R = rest != 0.f ? rest_A / total : 0.f;
       const float2 st = out.stat[i];  // P (NaN: an id outside the vocabulary), T
-      const float T = tail && rest > 0.f ? st.y : 0.f;
+      const float T = tail && rest != 0.f ? st.y : 0.f;
       const float w = weights ? weights[i] : 1.f;
       // P for the gradients: a bad id takes no part in them
       float P = st.x;
