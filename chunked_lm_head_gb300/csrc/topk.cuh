@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(32 * TOPK_WARPS)
     sid[K + lane] = INT_MAX;
     sp[K + lane] = 0.f;
   }
-  bool any = false, bad = false;
+  bool any = false, bad = false, nan = false;
   float top = -INFINITY;
   for (int j0 = lane; j0 < K; j0 += 128) {
     // four entries' ids and logits at once: one latency of memory, not eight
@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(32 * TOPK_WARPS)
       bad |= id[e] >= V;
       any |= in;
       const float x = in ? u[e] : -INFINITY;
+      nan |= x != x;  // (the maximum passes over it)
       sid[j] = in ? static_cast<int>(id[e]) : INT_MAX;
       sp[j] = x;
       top = fmaxf(top, x);
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(32 * TOPK_WARPS)
   }
   any = __any_sync(0xffffffffu, any);
   bad = __any_sync(0xffffffffu, bad);
+  nan = __any_sync(0xffffffffu, nan);
   top = warp_max(top);
   bool live = any || bad;
   // log p = (u - ref) - logsum: ref the teacher's log-sum-exp, or the list's
@@ -152,10 +154,14 @@ __global__ void __launch_bounds__(32 * TOPK_WARPS)
   if (t.lse != nullptr) {
     ref = t.lse[i];
   } else {
-    live = live && (top > -INFINITY || bad);  // a list without mass sums to nothing
+    // a list without mass sums to nothing; beside an id outside the vocabulary
+    // its entries have mass 0
+    const bool none = top == -INFINITY;
+    live = live && (!none || bad || nan);
+    ref = none ? 0.f : top;
     float s = 0.f;
-    for (int j = lane; j < K; j += 32) s += expf(sp[j] - top);
-    logsum = logf(warp_sum(s));
+    for (int j = lane; j < K; j += 32) s += expf(sp[j] - ref);
+    logsum = none && !nan ? 0.f : logf(warp_sum(s));
   }
   live = live && (targets == nullptr || targets[i] != ignore);
   double P = 0.0;

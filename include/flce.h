@@ -455,7 +455,9 @@ FLCE_API flce_status flce_jsd_backward_ex2(const flce_bf16* h_s, const flce_bf16
  *   loss = sum_i m w kl / sum_i m,
  * with 0 log 0 = 0, and no tail term where the list holds the whole
  * vocabulary.  m is 0 where targets[i] == ignore_index (targets NULL: nowhere)
- * and where the list is empty.
+ * and where the list is empty or, without lse, holds no mass (logits of minus
+ * infinity alone).  A NaN among the row's listed logits or the student's makes
+ * its kl, and the loss, NaN.
  *   ids     [N, ld_ids] int32 or int64 (ids_type); a negative id is no entry
  *           (lists of unequal length), the order is free.  An id >= V makes
  *           the row's kl, and the loss, NaN; it takes part in no gradient and
