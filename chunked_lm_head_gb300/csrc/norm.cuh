@@ -126,6 +126,23 @@ struct NormParams {
   float* rstd;         // [N], or null
 };
 
+// The e4m3 scale of a row from rstd and top = max_j |s_j gain_j|, and the
+// factors with q_j = e4m3((s_j gain_j up) f): y / scale without a division per
+// element.  448 / top passes fp32's range below 2^-119; such a row is taken
+// times 2^64 first, which rounds nothing.
+struct RowScale {
+  float scale, f, up;
+};
+__device__ __forceinline__ RowScale row_scale(float rstd, float top) {
+  const float s = rstd * top / 448.f;
+  // an all-zero row (or one whose scale rounds to zero), and one that holds a
+  // NaN or an infinity, has scale 1
+  RowScale e{s > 0.f ? s : 1.f, 0.f, 1.f};
+  if (s > 0.f && top < 0x1p-119f) e.up = 0x1p64f;
+  e.f = rstd / (e.scale * e.up);
+  return e;
+}
+
 // One row on a group of T threads, VPT vectors of 8 elements to a thread in
 // registers (H <= 8 T VPT): the row is read once.  Bound by memory: with a bf16
 // residual 32,768 x 4,096 takes 156 us in bf16 and 139 in e4m3 (6.9 and 6.8
@@ -188,11 +205,15 @@ __global__ void __launch_bounds__(MAXT, CTAS) rms_norm_kernel(const __grid_const
   const float rstd = 1.f / sqrtf(sum / static_cast<float>(p.H) + p.eps);
   float f = rstd;
   if constexpr (kQ) {
-    const float amax = rstd * top;
-    // an all-zero row, and one that holds a NaN or an infinity, has scale 1
-    const float sc = amax > 0.f ? amax / 448.f : 1.f;
-    if (t == 0) p.scale[row] = sc;
-    f = rstd / sc;
+    const RowScale e = row_scale(rstd, top);
+    if (t == 0) p.scale[row] = e.scale;
+    f = e.f;
+    if (e.up != 1.f) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[i][k] = mul2(v[i][k], both(e.up));
+    }
   }
   if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
 #pragma unroll
@@ -287,10 +308,21 @@ __global__ void __launch_bounds__(32 * NORM_WARP_ROWS, CTAS) rms_norm_warp_kerne
   const float rstd = 1.f / sqrtf(sum / static_cast<float>(p.H) + p.eps);
   float f = rstd;
   if constexpr (kQ) {
-    const float amax = rstd * top;
-    const float sc = amax > 0.f ? amax / 448.f : 1.f;
-    if (lane == 0) p.scale[row] = sc;
-    f = rstd / sc;
+    const RowScale e = row_scale(rstd, top);
+    if (lane == 0) p.scale[row] = e.scale;
+    f = e.f;
+    if (e.up != 1.f) {  // the stream itself, which a finite rstd keeps under 2^64
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = mul2(s[i].pair(k), both(e.up));
+          w[k] = pack_bf16x2(v.x, v.y);
+        }
+        s[i].q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
   }
   if (lane == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
 #pragma unroll

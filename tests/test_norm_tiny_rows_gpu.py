@@ -1,13 +1,12 @@
-"""The norm at the ends of its types: rows of tiny values, gradients that start
-off a 16-byte boundary, and second derivatives, which it does not have."""
+"""The e4m3 norm's rows of tiny values, whose factor 448 / max|s gain| is past
+fp32 although y / scale is not."""
 import pytest
 import torch
 
 import chunked_lm_head_gb300 as flce
-from chunked_lm_head_gb300 import _lib
 
 import norm_ref as R
-from test_norm_gpu import BF16, E4M3, F32, FP32, assert_within, make
+from test_norm_gpu import BF16, E4M3, F32, FP32, assert_within
 
 pytestmark = pytest.mark.gpu
 
@@ -15,8 +14,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("residual", [None, BF16, F32], ids=["none", "bf16", "f32"])
 @pytest.mark.parametrize("H", [64, 512, 2560, 4096, 8192, 16400])
 def test_e4m3_rows_of_tiny_values(H, residual):
-    """Rows whose largest value is down to 2^-126, bf16's smallest normal: 448 / max|s gain| is
-    past fp32, y / scale is not."""
+    """Rows whose largest value is down to 2^-126, bf16's smallest normal one."""
     N = 6
     g = torch.Generator(device="cuda").manual_seed(71 + H)
     x = torch.randn(N, H, generator=g, device="cuda").clamp(-2, 2)
@@ -44,25 +42,3 @@ def test_e4m3_row_below_the_smallest_scale():
     for r in (None, torch.zeros(2, 512, device="cuda")):
         out = flce.rms_norm_e4m3(x, w, r, eps=1.0)
         assert bool((out["scale"] == 1).all()) and not out["q"].float().any()
-
-
-@pytest.mark.parametrize("residual", [None, BF16, F32], ids=["none", "bf16", "f32"])
-def test_gradients_off_a_16_byte_boundary(residual):
-    """What autograd hands back for a part of a flat buffer is contiguous, and
-    starts anywhere."""
-    N, H = 6, 72
-    x, r, w, rnd = make(N, H, residual, BF16, 0.0)
-    for v in (x, r, w):
-        if v is not None:
-            v.requires_grad_(True)
-    ins = [v for v in (x, r, w) if v is not None]
-    outs = flce.rms_norm(x, w, r)
-    outs = [outs] if r is None else list(outs)
-    pads = [torch.zeros(3, dtype=o.dtype, device="cuda", requires_grad=True) for o in outs]
-    flat = [torch.cat([p, o.reshape(-1)]) for p, o in zip(pads, outs)]
-    ups = [rnd(3 + N * H).to(o.dtype) for o in outs]
-    got = torch.autograd.grad(flat, ins, ups)
-    outs = flce.rms_norm(x, w, r)
-    outs = [outs] if r is None else list(outs)
-    want = torch.autograd.grad(outs, ins, [u[3:].reshape(N, H).clone() for u in ups])
-    assert all(torch.equal(a, b) for a, b in zip(got, want))
