@@ -356,6 +356,9 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
     base.sp_ids = topk->rows.ids;
     base.sp_val = topk->rows.val;
     base.sp_k = topk->K;
+    // the recomputed logits come out of the same cut sums as the forward's,
+    // whose log-sum-exp they are taken against
+    base.tf_a *= 1.f + mma_cut(H);
   }
 
   // Row compaction: the chunks run over the non-ignored rows (count and

@@ -639,8 +639,14 @@ struct TopkCall {
 // logits, by 0.26 x 2^-24 |z| per step (0.22 at 16 steps, 0.264 at 512; a
 // partial sum is half the logit on average and a cut loses half a unit, which
 // bounds it by 0.5).  Left alone it biases a log-sum-exp of 4,096 products by
-// -4e-6, thirty times a rounded sum's error; the forward with listed columns
-// puts it back in the factor that every logit is multiplied by anyway.
+// -4e-6 of itself, thirty times a rounded sum's error; the forward with listed
+// columns and its recomputing backward put it back in the factor that every
+// logit is multiplied by anyway.  It is a mean over random products (8,192 of
+// them: a log-sum-exp of 33 is off by -2e-6 instead of -2.6e-4); of logits
+// whose partial sums all grow 0.26 leaves two fifths of the cut (-1.6e-4
+// instead of -4.0e-4), and one near zero, whose partial sums have either sign,
+// has nothing to correct.  The cross-entropy's log-sum-exp has no such
+// correction and is lower by that much.
 float mma_cut(int64_t H) { return static_cast<float>(0.26 * static_cast<double>(ceil_div(H, UMMA_K)) / 16777216.0); }
 
 // The row kernel over `rows` rows (row0 + j, or ri[j]); its block sums at
