@@ -65,6 +65,29 @@ def _device_scalar(x, dtype, dev):
     return torch.as_tensor(x).to(device=dev, dtype=dtype).reshape(1).contiguous()
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """Gradients that kernels formed without a graph, tied to the tensors they
+    depend on: differentiating them again is refused, not taken for zero."""
+
+    @staticmethod
+    def forward(ctx, n, *grads_and_inputs):
+        return tuple(g.view_as(g) for g in grads_and_inputs[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("this gradient has no second derivative: it comes from a kernel, without a graph")
+
+
+def _first_order(grads, inputs):
+    """grads (each may be None) as a backward returns them: under create_graph
+    tied to the inputs."""
+    if not torch.is_grad_enabled():
+        return grads
+    some = [g for g in grads if g is not None]
+    tied = iter(_NoSecondDerivative.apply(len(some), *some, *(x for x in inputs if x is not None)))
+    return tuple(None if g is None else next(tied) for g in grads)
+
+
 def backward(h, W, targets, weights, lse, grad_scale: float, chunk_rows: int = 256,
              ignore_index: int = IGNORE_INDEX, need_dH: bool = True, need_dW: bool = True,
              workspace: torch.Tensor | None = None, stream=None, transform=None,

@@ -11,6 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
+from .api import _first_order
 
 _TYPES = {torch.bfloat16: _lib.DTYPES["bf16"], torch.float32: _lib.DTYPES["f32"]}
 
@@ -144,6 +145,7 @@ class RMSNormFunction(torch.autograd.Function):
         dx, dr, dw = _norm_grads(dy.contiguous(), s, s.stride(0) if s.shape[0] > 1 else s.shape[1], weight, rstd,
                                  None if ds is None else ds.contiguous(), ctx.weight_offset, need_x, need_r, need_w,
                                  None, None)
+        dx, dw, dr = _first_order((dx, dw, dr), (s, weight, dy, ds))
         return dx, dw, dr, None, None
 
 

@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import IGNORE_INDEX, _device_scalar
+from .api import IGNORE_INDEX, _device_scalar, _first_order
 
 _IDS = {torch.int32: _lib.DTYPES["i32"], torch.int64: _lib.DTYPES["i64"]}
 _LOGITS = {torch.float32: _lib.DTYPES["f32"], torch.bfloat16: _lib.DTYPES["bf16"], torch.float16: _lib.DTYPES["f16"]}
@@ -168,7 +168,7 @@ class TopkDistill(torch.autograd.Function):
         h, W, state, n_valid = ctx.saved_tensors
         dH, dW = topk_kd_backward(h, W, state, ctx.k, 1.0, ctx.chunk_rows, ctx.transform, ctx.needs_input_grad[0],
                                   ctx.needs_input_grad[1], scale=grad_loss, count=n_valid, dW_dtype=W.dtype)
-        return (dH, dW) + (None,) * 9
+        return _first_order((dH, dW), (h, W, grad_loss)) + (None,) * 9
 
 
 class TopkDistillOneCall(torch.autograd.Function):
@@ -189,6 +189,8 @@ class TopkDistillOneCall(torch.autograd.Function):
     def backward(ctx, grad_loss, grad_kl, grad_n):
         if grad_loss is None:
             return (None,) * 11
+        if torch.is_grad_enabled():  # (h and W are not kept to tie the gradients to)
+            raise RuntimeError("the one-call loss has no second derivative: use recompute=True under create_graph")
         if ctx.grads is None:
             raise RuntimeError("the one-call loss can be differentiated once: its gradients are scaled in place")
         dH, dW = ctx.grads
