@@ -123,6 +123,13 @@ def rms_norm_backward(dy, s, weight, rstd, ds=None, weight_offset: float = 0.0, 
     return _norm_grads(dy, s, lds, weight, rstd, ds, weight_offset, need_dx, need_dr, need_dweight, workspace, stream)
 
 
+def _rows_of(g):
+    """A gradient as the kernels read it: contiguous, from a 16-byte boundary on
+    (a part of a flat buffer may start anywhere)."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class RMSNormFunction(torch.autograd.Function):
     """rms_norm with its backward; the stream is returned beside y."""
 
@@ -142,8 +149,8 @@ class RMSNormFunction(torch.autograd.Function):
             if ds is None:
                 return None, None, None, None, None
             return ds.to(torch.bfloat16) if need_x else None, None, ds if need_r else None, None, None
-        dx, dr, dw = _norm_grads(dy.contiguous(), s, s.stride(0) if s.shape[0] > 1 else s.shape[1], weight, rstd,
-                                 None if ds is None else ds.contiguous(), ctx.weight_offset, need_x, need_r, need_w,
+        dx, dr, dw = _norm_grads(_rows_of(dy), s, s.stride(0) if s.shape[0] > 1 else s.shape[1], weight, rstd,
+                                 None if ds is None else _rows_of(ds), ctx.weight_offset, need_x, need_r, need_w,
                                  None, None)
         dx, dw, dr = _first_order((dx, dw, dr), (s, weight, dy, ds))
         return dx, dw, dr, None, None
