@@ -288,6 +288,10 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   const int cg = cta_group();
   const int workers = device_workers(cg);
   const int tm = BM * cg;
+  // (listed columns, too, leave the dlogits as one bf16 value per entry at any
+  // number of rows, as the cross-entropy's: the empty half of a row tile that the
+  // one-call step fills with what the rounding leaves out, plan.cuh, would double
+  // the slabs' dlogits here)
   // (with listed columns one block of rows keeps the unpipelined plan, whose dW
   // GEMM can write bf16: the sums' order, and so dH's bits, are the same
   // whatever dW's type)

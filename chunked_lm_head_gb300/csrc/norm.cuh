@@ -145,7 +145,7 @@ __device__ __forceinline__ RowScale row_scale(float rstd, float top) {
 
 // One row on a group of T threads, VPT vectors of 8 elements to a thread in
 // registers (H <= 8 T VPT): the row is read once.  Bound by memory: with a bf16
-// residual 32,768 x 4,096 takes 156 us in bf16 and 139 in e4m3 (6.9 and 6.8
+// residual 32,768 x 4,096 takes 157 us in bf16 and 141 in e4m3 (6.8 and 6.7
 // TB/s).
 constexpr int kNormGroups = 15;  // groups of a CTA at most (named barriers 1 to 15)
 
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) rms_norm_kernel(const __grid_const
 // Rows on a warp each, VPL vectors of 8 elements to a lane (H <= 256 VPL), the
 // bf16 stream kept as it is stored: no barrier, and the row's sums cost one
 // butterfly instead of one per warp of a group.  131,072 x 2,560 without a
-// residual: 196 us in bf16, 162 in e4m3 (6.8 and 6.2 TB/s).
+// residual: 197 us in bf16, 166 in e4m3 (6.8 and 6.1 TB/s).
 constexpr int NORM_WARP_ROWS = 8;  // rows of a CTA
 template <bool kRes, bool kQ, int VPL, int CTAS>
 __global__ void __launch_bounds__(32 * NORM_WARP_ROWS, CTAS) rms_norm_warp_kernel(const __grid_constant__ NormParams p) {

@@ -35,11 +35,21 @@ cudaError_t launch_norm_warps(const NormParams& p, cudaStream_t st) {
 }
 
 // A warp to a row where the row fits its registers beside what else it needs:
-// without a residual up to 4,096 elements (131,072 x 2,560: 196 us in bf16 and
-// 162 in e4m3, against 220 and 232 on groups), with a bf16 residual up to 1,024
+// without a residual up to 4,096 elements, with a bf16 residual up to 1,024
 // (262,144 x 256: 81 against 100 us; at 1,024 81 either way, at 4,096 87 against
-// 81).  Else groups of two vectors to a thread in CTAs of about 512 threads;
-// past 8,192 elements four, so that a row fits a CTA.
+// 81).  Without one, bf16 / e4m3 us for 335 M elements in rows of
+//            1,536      2,048      2,304      2,560      2,816      3,584      4,096
+//   8        197 / 188  197 / 172
+//   10       197 / 193  197 / 174  199 / 170  197 / 166
+//   16       246 / 274  215 / 233  209 / 223  203 / 213  199 / 207  199 / 193  201 / 186
+//   groups   221 / 238  219 / 236  231 / 254  223 / 240  250 / 266  229 / 246  221 / 240
+// vectors to a lane (ten are as many as three CTAs to an SM leave registers for).
+// Else groups of two vectors to a thread in CTAs of about 512 threads; past
+// 8,192 elements four, so that a row fits a CTA.  Those rows, 134 M elements,
+// bf16 / e4m3 us: with a bf16 residual 160 / 141 at 12,288, 160 / 139 at 16,384,
+// 170 / 164 at 20,480, 164 / 152 at 32,768 (floors 160 / 140); without one 90 /
+// 104, 98 / 92, 129 / 125 and 111 / 106 (80 / 60): one row to a CTA, whose loads
+// wait for its reduction.
 template <class R, bool kQ>
 cudaError_t launch_norm_as(const NormParams& p, cudaStream_t st) {
   constexpr bool kRes = !std::is_same<R, NoResidual>::value;
@@ -78,6 +88,10 @@ cudaError_t launch_norm(const NormParams& p, bool res, bool res_f32, cudaStream_
 //   fp32 stream: straight from global memory, whose second read hits L1
 //   (16,384 x 4,096: 190 us against 238 through shared memory, where a
 //   thread's 32 bytes of a row halve every access).
+//   Past 8,192 elements one row to a CTA, 1.3 to 2.5 times the floor (134 M
+//   elements with the stream's own gradient, bf16 / fp32 stream: 237 / 526 us at
+//   12,288, 213 / 440 at 16,384, 395 / 524 at 20,480, 295 / 571 at 32,768; floors
+//   160 / 321).
 struct NormBwdShape {
   int vpt, T, groups, ctas;
 };

@@ -593,7 +593,9 @@ __global__ void round_bf16_kernel(const float* __restrict__ x, long long n, uint
   }
 }
 
-// The same for two bf16 arrays in one launch.
+// The same for two bf16 arrays in one launch.  A scale that is no power of two
+// rounds them a second time (bf16's half step 2^-8 each): the incoming gradient
+// of a loss whose gradients were formed, and rounded, with the loss.
 __global__ void scale_bf16_pair_kernel(__nv_bfloat16* __restrict__ x, long long nx, __nv_bfloat16* __restrict__ y,
                                        long long ny, const float* __restrict__ scale) {
   const float s = *scale;

@@ -212,7 +212,9 @@ def topk_distill_loss(h, W, ids, logits, lse_t=None, targets=None, weights=None,
 
     recompute=False computes the gradients in the forward call without the
     logits recompute (faster when chunk_rows >= 2,048; dH and dW are held from
-    the forward to the backward)."""
+    the forward to the backward).  The backward then multiplies them by the
+    incoming gradient, a second rounding where that is no power of two, and a
+    pass over them where it is not 1; it has no create_graph."""
     args = (h, W, ids, logits, lse_t, targets, weights, tail, chunk_rows, ignore_index, transform)
     if not torch.is_grad_enabled() or not (h.requires_grad or W.requires_grad):
         out = topk_kd_forward(*args, skip_ignored=True)
