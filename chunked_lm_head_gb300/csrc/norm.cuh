@@ -63,6 +63,16 @@ __device__ __forceinline__ void store8(float* p, const float2 (&v)[4]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float2 (&v)[4]) {
+  uint32_t b[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(v[2 * k], __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(v[2 * k + 1], __NV_SATFINITE, __NV_E4M3);
+    b[k] = lo | (hi << 16);
+  }
+  *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
+}
 
 // 8 gains from column c on: weight (fp32 or bf16) + offset.
 __device__ __forceinline__ void gain8(const void* w, int f32, float offset, int c, float2 (&v)[4]) {
@@ -129,7 +139,7 @@ struct NormParams {
 // The e4m3 scale of a row from rstd and top = max_j |s_j gain_j|, and the
 // factors with q_j = e4m3((s_j gain_j up) f): y / scale without a division per
 // element.  448 / top passes fp32's range below 2^-119; such a row is taken
-// times 2^64 first, which rounds nothing.
+// times 2^64 first, which rounds nothing (tiny_row).
 struct RowScale {
   float scale, f, up;
 };
@@ -143,9 +153,26 @@ __device__ __forceinline__ RowScale row_scale(float rstd, float top) {
   return e;
 }
 
+// The e4m3 row whose factor `up` is not 1, from the stream s as it is in memory
+// (each thread reads what it stored): a path of its own, so that no other row's
+// registers pay for it.
+template <class S>
+__device__ __forceinline__ void tiny_row(const S* s, const NormParams& p, long long o, int t, int T, const RowScale& e) {
+#pragma unroll 1
+  for (int i = t; i < p.H / 8; i += T) {
+    Raw8<S> v;
+    v.load(s + i * 8);
+    float2 g[4], y[4];
+    gain8(p.weight, p.w_f32, p.offset, i * 8, g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = mul2(mul2(mul2(v.pair(k), g[k]), both(e.up)), both(e.f));
+    store8_e4m3(p.q + o + i * 8, y);
+  }
+}
+
 // One row on a group of T threads, VPT vectors of 8 elements to a thread in
 // registers (H <= 8 T VPT): the row is read once.  Bound by memory: with a bf16
-// residual 32,768 x 4,096 takes 157 us in bf16 and 141 in e4m3 (6.8 and 6.7
+// residual 32,768 x 4,096 takes 157 us in bf16 and 142 in e4m3 (6.8 and 6.6
 // TB/s).
 constexpr int kNormGroups = 15;  // groups of a CTA at most (named barriers 1 to 15)
 
@@ -209,10 +236,12 @@ __global__ void __launch_bounds__(MAXT, CTAS) rms_norm_kernel(const __grid_const
     if (t == 0) p.scale[row] = e.scale;
     f = e.f;
     if (e.up != 1.f) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[i][k] = mul2(v[i][k], both(e.up));
+      if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+      if constexpr (kRes)
+        tiny_row(static_cast<const R*>(p.s) + o, p, o, t, T, e);
+      else
+        tiny_row(x, p, o, t, T, e);
+      return;  // the whole group
     }
   }
   if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
@@ -223,14 +252,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) rms_norm_kernel(const __grid_const
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[i][k] = mul2(v[i][k], both(f));
       if constexpr (kQ) {
-        uint32_t b[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(v[i][2 * k], __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(v[i][2 * k + 1], __NV_SATFINITE, __NV_E4M3);
-          b[k] = lo | (hi << 16);
-        }
-        *reinterpret_cast<uint2*>(p.q + o + c) = make_uint2(b[0], b[1]);
+        store8_e4m3(p.q + o + c, v[i]);
       } else {
         float2 g[4];
         gain8(p.weight, p.w_f32, p.offset, c, g);
@@ -245,7 +267,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) rms_norm_kernel(const __grid_const
 // Rows on a warp each, VPL vectors of 8 elements to a lane (H <= 256 VPL), the
 // bf16 stream kept as it is stored: no barrier, and the row's sums cost one
 // butterfly instead of one per warp of a group.  131,072 x 2,560 without a
-// residual: 197 us in bf16, 166 in e4m3 (6.8 and 6.1 TB/s).
+// residual: 197 us in bf16, 167 in e4m3 (6.8 and 6.0 TB/s).
 constexpr int NORM_WARP_ROWS = 8;  // rows of a CTA
 template <bool kRes, bool kQ, int VPL, int CTAS>
 __global__ void __launch_bounds__(32 * NORM_WARP_ROWS, CTAS) rms_norm_warp_kernel(const __grid_constant__ NormParams p) {
@@ -311,17 +333,11 @@ __global__ void __launch_bounds__(32 * NORM_WARP_ROWS, CTAS) rms_norm_warp_kerne
     const RowScale e = row_scale(rstd, top);
     if (lane == 0) p.scale[row] = e.scale;
     f = e.f;
-    if (e.up != 1.f) {  // the stream itself, which a finite rstd keeps under 2^64
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 v = mul2(s[i].pair(k), both(e.up));
-          w[k] = pack_bf16x2(v.x, v.y);
-        }
-        s[i].q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+    if (e.up != 1.f) {
+      if (lane == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+      const long long row_o = static_cast<long long>(row) * p.H;
+      tiny_row(kRes ? static_cast<const uint16_t*>(p.s) + row_o : p.x + row * p.ldx, p, row_o, lane, 32, e);
+      return;
     }
   }
   if (lane == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
@@ -331,16 +347,9 @@ __global__ void __launch_bounds__(32 * NORM_WARP_ROWS, CTAS) rms_norm_warp_kerne
       float2 g[4], v[4];
       gain8(p.weight, p.w_f32, p.offset, lane * 8 + i * 256, g);
       if constexpr (kQ) {
-        uint32_t b[2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = mul2(mul2(s[i].pair(k), g[k]), both(f));
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(v[2 * k], __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(v[2 * k + 1], __NV_SATFINITE, __NV_E4M3);
-          b[k] = lo | (hi << 16);
-        }
-        *reinterpret_cast<uint2*>(p.q + o + i * 256) = make_uint2(b[0], b[1]);
+        store8_e4m3(p.q + o + i * 256, v);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = mul2(mul2(s[i].pair(k), both(f)), g[k]);
