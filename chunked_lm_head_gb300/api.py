@@ -84,6 +84,8 @@ def _first_order(grads, inputs):
     if not torch.is_grad_enabled():
         return grads
     some = [g for g in grads if g is not None]
+    if not some:
+        return grads
     tied = iter(_NoSecondDerivative.apply(len(some), *some, *(x for x in inputs if x is not None)))
     return tuple(None if g is None else next(tied) for g in grads)
 

@@ -182,6 +182,7 @@ class TopkDistillOneCall(torch.autograd.Function):
                                        1.0, ctx.needs_input_grad[0], ctx.needs_input_grad[1], transform=transform,
                                        need_lse=False, dW_dtype=W.dtype)
         ctx.grads = (out["dH"], out["dW"])
+        ctx.save_for_backward(h, W)  # read under create_graph alone
         ctx.mark_non_differentiable(out["kl"], out["n_valid"])
         return out["loss"], out["kl"], out["n_valid"]
 
@@ -189,8 +190,6 @@ class TopkDistillOneCall(torch.autograd.Function):
     def backward(ctx, grad_loss, grad_kl, grad_n):
         if grad_loss is None:
             return (None,) * 11
-        if torch.is_grad_enabled():  # (h and W are not kept to tie the gradients to)
-            raise RuntimeError("the one-call loss has no second derivative: use recompute=True under create_graph")
         if ctx.grads is None:
             raise RuntimeError("the one-call loss can be differentiated once: its gradients are scaled in place")
         dH, dW = ctx.grads
@@ -200,6 +199,8 @@ class TopkDistillOneCall(torch.autograd.Function):
                 grad_loss = grad_loss.float()
             _lib.check("flce_scale_grads_bf16", _lib.flce_scale_grads_bf16(
                 dH, 0 if dH is None else dH.numel(), dW, 0 if dW is None else dW.numel(), grad_loss))
+        if torch.is_grad_enabled():
+            dH, dW = _first_order((dH, dW), (*ctx.saved_tensors, grad_loss))
         return (dH, dW) + (None,) * 9
 
 
@@ -214,7 +215,7 @@ def topk_distill_loss(h, W, ids, logits, lse_t=None, targets=None, weights=None,
     logits recompute (faster when chunk_rows >= 2,048; dH and dW are held from
     the forward to the backward).  The backward then multiplies them by the
     incoming gradient, a second rounding where that is no power of two, and a
-    pass over them where it is not 1; it has no create_graph."""
+    pass over them where it is not 1."""
     args = (h, W, ids, logits, lse_t, targets, weights, tail, chunk_rows, ignore_index, transform)
     if not torch.is_grad_enabled() or not (h.requires_grad or W.requires_grad):
         out = topk_kd_forward(*args, skip_ignored=True)

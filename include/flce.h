@@ -666,8 +666,8 @@ FLCE_API flce_status flce_forward_e4m3(const uint8_t* h8, const float* h_scale, 
  * (rows are counted in 32 bits), else FLCE_ERR_INVALID_ARG.
  *
  * flce_rms_norm_e4m3 gives the operands of flce_forward_e4m3 instead of y:
- * out_scale[i] = max_j |y_ij| / 448 (1 for an all-zero row and for one that
- * holds a NaN or an infinity) and out_q = e4m3(y / scale), round to nearest
+ * out_scale[i] = max_j |y_ij| / 448 (1 for an all-zero row, for one so small
+ * that this rounds to zero, and for one that holds a NaN or an infinity) and out_q = e4m3(y / scale), round to nearest
  * even, saturating, from the 32-bit y (not through bf16).
  */
 FLCE_API flce_status flce_rms_norm(const flce_bf16* x, int64_t ldx, const void* residual, int64_t ldr,
