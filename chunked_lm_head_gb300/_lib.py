@@ -118,6 +118,20 @@ SIGNATURES = {
                                               ctypes.c_int32, ctypes.c_float, _c_vp, _c_i64, _c_i64, _c_vp,
                                               _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
     "flce_rms_norm_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64]),
+    "flce_layer_norm": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, ctypes.c_int32, _c_vp, _c_vp, ctypes.c_int32,
+                                       ctypes.c_float, ctypes.c_float, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp,
+                                       _c_vp]),
+    "flce_layer_norm_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_i64, ctypes.c_int32, _c_vp, _c_vp, ctypes.c_int32,
+                                                ctypes.c_float, _c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp,
+                                                _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
+    "flce_layer_norm_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64]),
+    "flce_score": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp,
+                                  _c_vp, _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
+    "flce_score_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "flce_score_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+                                           ctypes.c_int32, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp,
+                                           ctypes.c_size_t, _c_vp]),
+    "flce_score_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int32]),
     "flce_scale_grads": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp]),
     "flce_scale_grads_bf16": (ctypes.c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp]),
     "flce_set_option": (ctypes.c_int, [ctypes.c_int, _c_i64]),
@@ -547,6 +561,53 @@ def flce_rms_norm_backward(dy, s, lds, s_type, ds, weight, weight_type, weight_o
 
 def flce_rms_norm_backward_workspace_bytes(N, H) -> int:
     return int(load().flce_rms_norm_backward_workspace_bytes(N, H))
+
+
+def flce_layer_norm(x, ldx, residual, ldr, residual_type, weight, bias, weight_type, weight_offset, eps, N, H, out_y,
+                    out_residual, out_mean, out_rstd, stream=None) -> int:
+    """Raw C call of the layer norm."""
+    return load().flce_layer_norm(_ptr(x), ldx, _ptr(residual), ldr, residual_type, _ptr(weight), _ptr(bias), weight_type,
+                                  float(weight_offset), float(eps), N, H, _ptr(out_y), _ptr(out_residual), _ptr(out_mean),
+                                  _ptr(out_rstd), _stream_handle(stream))
+
+
+def flce_layer_norm_backward(dy, s, lds, s_type, ds, weight, weight_type, weight_offset, mean, rstd, N, H, dx, dr,
+                             dweight, dbias, workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Raw C call of the layer norm's gradients."""
+    return load().flce_layer_norm_backward(_ptr(dy), _ptr(s), lds, s_type, _ptr(ds), _ptr(weight), weight_type,
+                                           float(weight_offset), _ptr(mean), _ptr(rstd), N, H, _ptr(dx), _ptr(dr),
+                                           _ptr(dweight), _ptr(dbias), _ptr(workspace), workspace_bytes,
+                                           _stream_handle(stream))
+
+
+def flce_layer_norm_backward_workspace_bytes(N, H) -> int:
+    return int(load().flce_layer_norm_backward_workspace_bytes(N, H))
+
+
+def flce_score(h, W, targets, N, H, V, k, ignore_index, transform, out_logp, out_lse, out_entropy, out_ids,
+               out_logprobs, workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Raw C call of the head's scores."""
+    tp, keep = _tf_ptr(transform)
+    return load().flce_score(_ptr(h), _ptr(W), _ptr(targets), N, H, V, k, ignore_index, tp, _ptr(out_logp),
+                             _ptr(out_lse), _ptr(out_entropy), _ptr(out_ids), _ptr(out_logprobs), _ptr(workspace),
+                             workspace_bytes, _stream_handle(stream))
+
+
+def flce_score_backward(h, W, targets, lse, entropy, g_logp, g_entropy, dH, dW, dW_type, N, H, V, chunk_rows,
+                        ignore_index, transform, workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Raw C call of the scores' gradients."""
+    tp, keep = _tf_ptr(transform)
+    return load().flce_score_backward(_ptr(h), _ptr(W), _ptr(targets), _ptr(lse), _ptr(entropy), _ptr(g_logp),
+                                      _ptr(g_entropy), _ptr(dH), _ptr(dW), dW_type, N, H, V, chunk_rows, ignore_index,
+                                      tp, _ptr(workspace), workspace_bytes, _stream_handle(stream))
+
+
+def flce_score_workspace_bytes(N, H, V, k) -> int:
+    return int(load().flce_score_workspace_bytes(N, H, V, k))
+
+
+def flce_score_backward_workspace_bytes(N, H, V, chunk_rows, dW_type) -> int:
+    return int(load().flce_score_backward_workspace_bytes(N, H, V, chunk_rows, dW_type))
 
 
 def flce_quantize_e4m3_rows(x, rows, cols, q, scale, stream=None) -> int:

@@ -1,8 +1,9 @@
 // libflce: the C-ABI entry points.  The tensor-core GEMM engine lives in
 // gemm.cuh, the CUDA-core kernels in small_kernels.cuh, the launch plans and
 // workspace layouts in plan.cuh, tensor maps, launches and shared stages in
-// launch.cuh, the norm in norm.cuh and norm_api.cuh, the distillation from top
-// logits in topk.cuh and topk_api.cuh.  include/flce.h states the contract of
+// launch.cuh, the norms in norm.cuh, norm_api.cuh, layer_norm.cuh and
+// layer_norm_api.cuh, the distillation from top logits in topk.cuh and
+// topk_api.cuh, the scores in score.cuh and score_api.cuh.  include/flce.h states the contract of
 // every entry point.
 #include <cuda.h>
 #include <cuda_fp8.h>
@@ -26,6 +27,8 @@
 #include "plan.cuh"
 #include "launch.cuh"
 #include "norm_api.cuh"
+#include "layer_norm_api.cuh"
+#include "score.cuh"
 
 namespace {
 using namespace flce;
@@ -267,11 +270,11 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
                                  const flce_logit_transform* transform, void* workspace,
                                  size_t workspace_bytes, void* stream,
                                  const long long* count_scale, const float* scale_dev = nullptr,
-                                 const TopkCall* topk = nullptr) {
+                                 const TopkCall* topk = nullptr, const ScoreGrads* score = nullptr) {
   if (!sizes_ok(N, H, V)) return FLCE_ERR_INVALID_ARG;
   GemmParams tfp{};
   if (!transform_params(transform, tfp)) return FLCE_ERR_INVALID_ARG;
-  flce_bf16* dW16 = topk ? topk->dW16 : nullptr;
+  flce_bf16* dW16 = topk ? topk->dW16 : score ? score->dW16 : nullptr;
   if (!dH && !dW && !dW16) return FLCE_ERR_INVALID_ARG;
   if (N > 0 && (!h || !W || !targets || !lse)) return FLCE_ERR_INVALID_ARG;
   if (H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
@@ -292,11 +295,11 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   // number of rows, as the cross-entropy's: the empty half of a row tile that the
   // one-call step fills with what the rounding leaves out, plan.cuh, would double
   // the slabs' dlogits here)
-  // (with listed columns one block of rows keeps the unpipelined plan, whose dW
+  // (with listed columns or scores one block of rows keeps the unpipelined plan, whose dW
   // GEMM can write bf16: the sums' order, and so dH's bits, are the same
   // whatever dW's type)
   BwdPlan b = plan_backward(N, H, V, chunk_rows, workers, tm);
-  if (!topk || N > b.R)
+  if (!(topk || score) || N > b.R)
     b = plan_backward_call(N, H, V, chunk_rows, workers, tm, dH != nullptr && dW != nullptr);
   const BwdLayout L = bwd_layout(N, H, b);
   Workspace ws;
@@ -360,10 +363,15 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
     base.sp_ids = topk->rows.ids;
     base.sp_val = topk->rows.val;
     base.sp_k = topk->K;
-    // the recomputed logits come out of the same cut sums as the forward's,
-    // whose log-sum-exp they are taken against
-    base.tf_a *= 1.f + mma_cut(H);
   }
+  if (score) {
+    base.entropy = score->entropy;
+    base.g_logp = score->g_logp;
+    base.g_entropy = score->g_entropy;
+  }
+  // the recomputed logits come out of the same cut sums as the forward's,
+  // whose log-sum-exp they are taken against
+  if (topk || score) base.tf_a *= 1.f + mma_cut(H);
 
   // Row compaction: the chunks run over the non-ignored rows (count and
   // indices stay on the device; the kernels read each chunk's row count), so
@@ -434,7 +442,7 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
     if (pipe) {
       const flce_status s2 = pipe_block(dhdw, p, rows, block, A_dl, W_k, D_st, Dpipe_k, Dpipe_mn, B_dw,
                                         dep + (block % 2) * dep_words, dep + ((block + 1) % 2) * dep_words,
-                                        topk != nullptr, st);
+                                        topk != nullptr, score != nullptr, st);
       if (s2 != FLCE_OK) return s2;
     }
     for (int slab = 0; slab < (pipe ? 0 : b.n_slabs); ++slab) {
@@ -457,8 +465,9 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
         ProfScope ps(K_DLOGITS, st);
         const CUtensorMap& D_out = q.d_tma ? D_st : W_k;
         const int nw = std::min(q.num_units, workers);
-        FLCE_CUDA_TRY(topk ? launch_listed<MODE_DLOGITS>(cg, kLong, A_dl, W_k, D_out, q, nw, st)
-                           : launch_gemm<MODE_DLOGITS>(cg, kLong, A_dl, W_k, D_out, q, nw, st));
+        FLCE_CUDA_TRY(score  ? (launch_scored<MODE_DLOGITS, SCORE_ENTROPY>(cg, kLong, A_dl, W_k, D_out, q, nw, st))
+                      : topk ? launch_listed<MODE_DLOGITS>(cg, kLong, A_dl, W_k, D_out, q, nw, st)
+                             : launch_gemm<MODE_DLOGITS>(cg, kLong, A_dl, W_k, D_out, q, nw, st));
       }
       // (2) dH[rows] (+)= D W[slab], (3) dW[slab] (+)= D^T h[rows]
       const flce_status s2 = slab_dh_dw(dhdw, p, rows, block, slab, v0, width, D_k, D_mn, B_dw, st);
@@ -1777,3 +1786,4 @@ extern "C" flce_status flce_forward_static_scratch(const flce_bf16* h, const flc
 }
 
 #include "topk_api.cuh"
+#include "score_api.cuh"

@@ -274,6 +274,25 @@ struct GemmParams {
   // DW: the rows of h repeat after this many K blocks (0: they do not)
   int dw_h_blocks;
   int ld_mx;  // FUSED_FWD with listed columns: row pitch of mx, a multiple of 8 that covers whole tiles
+  // scores (the kernel's kScore).  The forward: per row of the pass and split
+  // [rows][cols] a partial (ScorePart), and per row and 32-column chunk
+  // [rows][rec_ld] its record (score_key).  The dlogits units: each row's entropy
+  // and the gradients of its log-probability and entropy ([N], a gradient may be
+  // null: zero)
+  float4* score_part;
+  float2* rec;
+  float* z;    // in the records' place: the logits [rows][rec_ld], fp32
+  int rec_ld;  // covers whole tiles
+  const float* entropy;
+  const float* g_logp;
+  const float* g_entropy;
+};
+
+// Which epilogues a kernel has beside its mode's.
+enum Score : int {
+  SCORE_NONE = 0,
+  SCORE_ENTROPY = 1,  // entropy beside the log-sum-exp (forward) and its gradient (dlogits units)
+  SCORE_TOP = 2       // forward: entropy, and what the likeliest words are found from (chunk records, or logits)
 };
 
 // grad_scale of the dlogits modes with its device-side factors: / max(count, 1)
@@ -814,8 +833,18 @@ __device__ __forceinline__ int list_lower_bound(const int* ids, int k, int v) {
   return lo;
 }
 
-// kSp: the forwards and dlogits with listed columns; kOut16: the DW mode with a bf16 dW.
-template <int MODE, bool kLong, int CG, bool kF8 = false, int EW = EPI_WARPS, bool kSp = false, bool kOut16 = false>
+// The record of a 32-column chunk of raw logits: its largest and its second
+// largest, each with 31 - its column in the low 5 bits of its fp32 value (off by
+// at most 2^-18 of itself).  The select kernel has to look at a chunk's other
+// columns only where the second is near the words it keeps.
+__device__ __forceinline__ float score_key(float z, int j) {
+  return __uint_as_float((__float_as_uint(z) & ~31u) | static_cast<uint32_t>(31 - j));
+}
+
+// kSp: the forwards and dlogits with listed columns; kOut16: the DW mode with a
+// bf16 dW; kScore: see Score.
+template <int MODE, bool kLong, int CG, bool kF8 = false, int EW = EPI_WARPS, bool kSp = false, bool kOut16 = false,
+          int kScore = SCORE_NONE>
 __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
     flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmA2,
@@ -999,7 +1028,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
         for (int n = t.n0; n < t.n1 && ok; ++n) {
           // (the epilogues that hand tensor memory back by a relaxed arrive of
           // either CTA are waited for at cluster scope)
-          const bool drained = CG == 2 && (kOut16 || kSp)
+          const bool drained = CG == 2 && (kOut16 || kSp || kScore != SCORE_NONE)
                                    ? wait_bar_cluster(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.err)
                                    : wait_bar(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.err);
           if (!drained) {
@@ -1124,6 +1153,13 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
       float run_mt = -INFINITY, run_st = 0.f, run_c = 0.f;  // KD_FWD teacher state
       float jsd_t = 0.f, jsd_s = 0.f, klsm = 0.f;            // JSD: mixture terms (log2 units)
       float scale = 0.f, nl2 = 0.f, nlt = 0.f;              // DLOGITS / KD_DLOGITS
+      static_assert(kScore == SCORE_NONE || (!kF8 && !kSp && !kOut16), "scores: bf16 operands, no listed columns");
+      static_assert(kScore == SCORE_NONE || MODE == MODE_FWD ||
+                        (kScore == SCORE_ENTROPY && (MODE == MODE_DLOGITS || MODE == MODE_PIPE)),
+                    "scores: the forward and, for the entropy, the dlogits units");
+      float run_ent = 0.f, run_abs = 0.f;                   // FWD scores: sum 2^(x - m) (m - x), a largest |z|
+      float sc_a = 0.f, sc_b = 0.f, sc_t = 0.f;             // DLOGITS scores: D = p (sc_a log2 p + sc_b) + onehot sc_t
+      float2 rec_even = make_float2(0.f, 0.f);
       // linear transform folded into the exp2 prescale, the gathered target
       // logit and the dlogits scale (soft-capped logits are formed explicitly)
       const float lin_a = p.tf_softcap ? 1.f : p.tf_a;
@@ -1146,7 +1182,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
       const bool row_store = lr < min((dsh.rows + BK - 1) / BK * BK, p.rows_cap);
       float a_sc = 1.f;  // e4m3 forward: this row's dequantisation scale
       if constexpr (MODE == MODE_FWD || MODE == MODE_FUSED_FWD) {
-        if (row_ok) tgt = p.targets[grow];
+        if (row_ok && (kScore == SCORE_NONE || p.targets != nullptr)) tgt = p.targets[grow];
         if constexpr (kF8) {
           if (row_ok) a_sc = p.a_scale[grow];
         }
@@ -1155,8 +1191,18 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
         if (row_ok) {
           tgt = p.targets[grow];
           const bool valid = tgt != p.ignore_index;
-          const float w = p.weights ? p.weights[grow] : 1.f;
-          scale = valid ? w * device_grad_scale(p) : 0.f;
+          if constexpr (kScore == SCORE_ENTROPY) {
+            // D_v = ga ([v = t] - p_v) - ge p_v (log p_v + entropy)
+            const float ga = p.g_logp != nullptr ? p.g_logp[grow] : 0.f;
+            const float ge = p.g_entropy != nullptr ? p.g_entropy[grow] : 0.f;
+            scale = valid && (ga != 0.f || ge != 0.f) ? 1.f : 0.f;
+            sc_a = -ge * kLn2f;
+            sc_b = -fmaf(ge, p.entropy[grow], ga);
+            sc_t = ga;
+          } else {
+            const float w = p.weights ? p.weights[grow] : 1.f;
+            scale = valid ? w * device_grad_scale(p) : 0.f;
+          }
           nl2 = -p.lse[grow] * kLog2e;
         }
       }
@@ -1215,7 +1261,75 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
           }
           const int col0 = n * K::TILE_N + c * 32;
-          if constexpr (MODE == MODE_FWD || MODE == MODE_FUSED_FWD) {
+          if constexpr (MODE == MODE_FWD && kScore != SCORE_NONE) {
+            // entropy = log S + C / S with S = sum 2^(x - m) and C = ln 2 sum
+            // 2^(x - m) (m - x), which holds for any m: every term is positive
+            // where m is the row's maximum, and nothing cancels (lse - sum p x
+            // would, a log-sum-exp of 20 against an entropy near 0).
+            const int nc = min(32, p.V - col0);  // columns of the chunk (32, but in the last tile)
+            run_abs = fmaxf(fmaxf(run_abs, fmaxf(fabsf(v[0]), fabsf(v[8]))), fmaxf(fabsf(v[16]), fabsf(v[24])));
+            if (kScore == SCORE_TOP && p.z != nullptr) {
+              if (row_ok) {
+                float4* dst = reinterpret_cast<float4*>(p.z + static_cast<idx_t>(lr) * p.rec_ld + col0);
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                  dst[g] = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+              }
+            } else if constexpr (kScore == SCORE_TOP) {
+              float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float key = nc == 32 || j < nc ? score_key(v[j], j) : -INFINITY;
+                m2 = fmaxf(m2, fminf(m1, key));
+                m1 = fmaxf(m1, key);
+              }
+              // two chunks' records leave together
+              if ((c & 1) == 0)
+                rec_even = make_float2(m1, m2);
+              else if (row_ok)
+                *reinterpret_cast<float4*>(p.rec + static_cast<idx_t>(lr) * p.rec_ld + (col0 / 32 - 1)) =
+                    make_float4(rec_even.x, rec_even.y, m1, m2);
+            }
+            if (p.tf_softcap) {
+              // (an infinite logit, which tanh would hide, becomes NaN: 0 z)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], 0.f, p.tf_b * tanhf(p.tf_a * v[j]));
+            }
+            if (nc < 32) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j >= nc) v[j] = -INFINITY;
+            }
+            float cm = v[0];
+#pragma unroll
+            for (int j = 1; j < 32; ++j) cm = fmaxf(cm, v[j]);
+            const float nm = fmaxf(run_m, cm * l2a);
+            if (nm != -INFINITY) {
+              float2 a = both(0.f), e = both(0.f);
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 x = fma2(make_float2(v[j], v[j + 1]), both(l2a), both(-nm));
+                const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                a = add2(a, w);
+                // (a logit of -infinity has no share: 0, not 0 times infinity)
+                e = fma2(w, make_float2(fmaxf(x.x, -1000.f), fmaxf(x.y, -1000.f)), e);
+              }
+              const float up = run_m != -INFINITY ? nm - run_m : 0.f;
+              const float r = ex2_approx(run_m - nm);
+              run_ent = fmaf(fmaf(up, run_s, run_ent), r, -(e.x + e.y));
+              run_s = fmaf(run_s, r, a.x + a.y);
+              run_m = nm;
+            } else if (cm != cm) {
+              run_s = cm;  // NaN throughout, without a maximum so far
+            }
+            if constexpr (kScore == SCORE_ENTROPY) {
+              const long long tj = tgt - col0;
+              if (tj >= 0 && tj < nc) {
+                const float z = select32(v, static_cast<int>(tj)) * lin_a;
+                if (row_ok) p.zt[grow] = z;
+              }
+            }
+          } else if constexpr (MODE == MODE_FWD || MODE == MODE_FUSED_FWD) {
             if constexpr (kF8) {  // dequantise: row scale x per-vocabulary-row scale
               if (col0 + 32 <= p.V) {
                 const float4* bs = reinterpret_cast<const float4*>(p.b_scale + col0);
@@ -1360,7 +1474,44 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
             const int gcol0 = uv0 + col0;  // vocabulary column of D's local column col0
             const long long tjl = tgt - gcol0;
             const int tj = (tjl >= 0 && tjl < 32) ? static_cast<int>(tjl) : -1;
-            if (!p.tf_softcap && tj < 0 && gcol0 + 32 <= p.V) {
+            if constexpr (kScore == SCORE_ENTROPY) {
+              if (!p.tf_softcap && tj < 0 && gcol0 + 32 <= p.V) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                  float2 d = both(0.f);
+                  if (scale != 0.f) {
+                    const float2 x = fma2(make_float2(v[j], v[j + 1]), both(l2a), both(nl2));
+                    const float2 q = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                    // (p log p is 0 where p is)
+                    const float2 f = fma2(make_float2(fmaxf(x.x, -1000.f), fmaxf(x.y, -1000.f)), both(sc_a), both(sc_b));
+                    d = mul2(mul2(q, f), both(lin_a));
+                  }
+                  pk[j / 2] = pack_bf16x2(d.x, d.y);
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                  float d[2] = {0.f, 0.f};
+                  if (scale != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                      float x, slope = lin_a;
+                      if (p.tf_softcap) {
+                        const float th = tanhf(p.tf_a * v[j + e]);
+                        x = fmaf(p.tf_b * th, kLog2e, nl2);
+                        slope = p.tf_d * (1.f - th * th);
+                      } else {
+                        x = fmaf(v[j + e], l2a, nl2);
+                      }
+                      float g = ex2_approx(x) * fmaf(fmaxf(x, -1000.f), sc_a, sc_b);
+                      if (j + e == tj) g += sc_t;
+                      d[e] = (gcol0 + j + e < p.V) ? g * slope : 0.f;
+                    }
+                  }
+                  pk[j / 2] = pack_bf16x2(d[0], d[1]);
+                }
+              }
+            } else if (!p.tf_softcap && tj < 0 && gcol0 + 32 <= p.V) {
               // the common chunk: no target column, inside the vocabulary
 #pragma unroll
               for (int j = 0; j < 32; j += 2) {
@@ -1697,7 +1848,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
         if (lane == 0) {
           if constexpr (CG == 1)
             mbar_arrive(acc ? tempty_target1 : tempty_target0);
-          else if constexpr (kOut16 || kSp)
+          else if constexpr (kOut16 || kSp || kScore != SCORE_NONE)
             mbar_arrive_cluster_tmem(acc ? tempty_target1 : tempty_target0);
           else
             mbar_arrive_cluster(acc ? tempty_target1 : tempty_target0);
@@ -1723,7 +1874,10 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
         }
         __syncwarp();
       }
-      if constexpr (MODE == MODE_FWD || MODE == MODE_FUSED_FWD) {
+      if constexpr (MODE == MODE_FWD && kScore != SCORE_NONE) {
+        if (ok && row_ok)
+          p.score_part[static_cast<idx_t>(lr) * p.cols + t.split] = make_float4(run_m, run_s, run_ent, run_abs);
+      } else if constexpr (MODE == MODE_FWD || MODE == MODE_FUSED_FWD) {
         if (ok && row_ok)
           p.partials[static_cast<idx_t>(t.split) * p.N + grow] = make_float2(run_m, run_s);
       }

@@ -254,6 +254,28 @@ cudaError_t launch_listed(int cg, bool kLong, const CUtensorMap& a, const CUtens
   return launch_listed<MODE>(cg, kLong, Maps{&a, &b, &c, &a, &b, &c, &a, &b, &c}, p, workers, st);
 }
 
+// A launch with the scores' epilogue: MODE_FWD, MODE_DLOGITS or MODE_PIPE.
+template <int MODE, int kScore>
+cudaError_t launch_scored(int cg, bool kLong, const Maps& m, const GemmParams& p, int workers, cudaStream_t st) {
+  auto go = [&](auto kern, int smem, int grid_mult) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_persistent(kern, grid_mult * grid_workers(workers), grid_mult, kernel_threads<MODE>(EPI_WARPS), smem,
+                             st, *m.a, *m.b, *m.c, *m.a2, *m.b2, *m.c2, *m.a3, *m.b3, *m.c3, p);
+  };
+  constexpr int s2 = KernelCfg<MODE, 2, EPI_WARPS>::SMEM, s1 = KernelCfg<MODE, 1, EPI_WARPS>::SMEM;
+  if (cg == 2)
+    return kLong ? go(flce_gemm_kernel<MODE, true, 2, false, EPI_WARPS, false, false, kScore>, s2, 2)
+                 : go(flce_gemm_kernel<MODE, false, 2, false, EPI_WARPS, false, false, kScore>, s2, 2);
+  return kLong ? go(flce_gemm_kernel<MODE, true, 1, false, EPI_WARPS, false, false, kScore>, s1, 1)
+               : go(flce_gemm_kernel<MODE, false, 1, false, EPI_WARPS, false, false, kScore>, s1, 1);
+}
+template <int MODE, int kScore>
+cudaError_t launch_scored(int cg, bool kLong, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
+                          const GemmParams& p, int workers, cudaStream_t st) {
+  return launch_scored<MODE, kScore>(cg, kLong, Maps{&a, &b, &c, &a, &b, &c, &a, &b, &c}, p, workers, st);
+}
+
 // The dW GEMM with a bf16 result.
 template <int EW>
 cudaError_t launch_dw16_t(int cg, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const GemmParams& p,
@@ -557,15 +579,19 @@ flce_status slab_dh_dw(const DhDwStage& a, const GemmParams& p, int rows, int bl
 flce_status pipe_block(const DhDwStage& a, const GemmParams& p, int rows, int block, const CUtensorMap& A_dl,
                        const CUtensorMap& W_k, const CUtensorMap& D_st, const CUtensorMap& D_k,
                        const CUtensorMap& D_mn, const CUtensorMap& B_dw, unsigned* dep, unsigned* dep_zero,
-                       bool listed, cudaStream_t st) {
+                       bool listed, bool scored, cudaStream_t st) {
   GemmParams q = pipe_params(*a.plan, p, a.H, a.tm, rows, block);
   q.dH_part = a.dh_part;
   q.pp_dep = dep;
   q.pp_dep_zero = dep_zero;
   ProfScope ps(K_PIPE, st);
+  const Maps maps{&D_k, a.W_mn, a.dhp_map, &D_mn, &B_dw, a.dW_map, &A_dl, &W_k, &D_st};
+  if (scored) {
+    FLCE_CUDA_TRY((launch_scored<MODE_PIPE, SCORE_ENTROPY>(a.cg, a.kLong, maps, q, a.workers, st)));
+    return FLCE_OK;
+  }
   if (listed) {
-    FLCE_CUDA_TRY(launch_listed<MODE_PIPE>(
-        a.cg, a.kLong, Maps{&D_k, a.W_mn, a.dhp_map, &D_mn, &B_dw, a.dW_map, &A_dl, &W_k, &D_st}, q, a.workers, st));
+    FLCE_CUDA_TRY(launch_listed<MODE_PIPE>(a.cg, a.kLong, maps, q, a.workers, st));
     return FLCE_OK;
   }
   FLCE_CUDA_TRY(launch_gemm<MODE_PIPE>(a.cg, a.kLong, D_k, *a.W_mn, *a.dhp_map, q, a.workers, st, &D_mn, &B_dw,
@@ -630,6 +656,15 @@ struct TopkCall {
   long long* bcnt = nullptr;
   float2* gemv = nullptr;  // [CTAs][N] partials of the few-row forward
   bool split_scale = false;   // the one-call dlogits take the power of two of their scale
+  flce_bf16* dW16 = nullptr;  // dW in bf16 straight from the GEMM (one row block), instead of dW
+};
+
+// ---- scores: what the backward of the log-probability and the entropy adds to
+// the tiled backward
+struct ScoreGrads {
+  const float* entropy = nullptr;    // [N], of the forward
+  const float* g_logp = nullptr;     // [N] gradients, each may be null
+  const float* g_entropy = nullptr;
   flce_bf16* dW16 = nullptr;  // dW in bf16 straight from the GEMM (one row block), instead of dW
 };
 

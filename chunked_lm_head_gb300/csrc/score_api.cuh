@@ -1,0 +1,306 @@
+// libflce host side: the entry points of the scores -- log-probability and
+// entropy with their gradients, and the likeliest words (row kernels in
+// score.cuh, the forward and the tiled backward in gemm.cuh and flce.cu).
+#pragma once
+
+namespace {
+
+// Words from the logits themselves, or from chunk records.  A chunk that two of
+// the K words share costs 32 products, so the records serve while chunks are
+// many: about K^2 / 2 / chunks of them are shared.  Below 8 K chunks the logits
+// are kept, at 4 bytes instead of 1/4 byte a column.
+bool score_dense(int64_t V, int64_t k) { return ceil_div(V, 32) < 8 * k; }
+
+constexpr size_t kScoreBlockBytes = size_t(256) << 20;  // of records or logits held at once
+
+struct ScorePlan {
+  bool gemv = false, dense = false;
+  long long rows = 0;  // of a launch
+  int S = 1;           // partials of a row
+  long long ld = 0;    // row pitch of the records (float2) or logits (fp32)
+  FwdPlan f;
+};
+ScorePlan score_plan(int64_t N, int64_t H, int64_t V, int64_t k, int workers, int tm) {
+  ScorePlan q;
+  q.gemv = topk_gemv_for(N, H);
+  q.dense = k > 0 && score_dense(V, k);
+  // both cover whole tiles
+  q.ld = k == 0 ? 0 : q.dense ? round_up(V, BN) : round_up(V, BN) / 32;
+  q.rows = fwd_block_rows(N, tm);
+  if (k > 0 && !q.gemv) {
+    const long long fit = static_cast<long long>(kScoreBlockBytes / (static_cast<size_t>(q.ld) * (q.dense ? 4 : 8)));
+    q.rows = std::min(q.rows, std::max<long long>(tm, fit / tm * tm));
+  }
+  q.f = plan_forward(q.rows, H, V, workers, tm);
+  q.S = q.gemv ? topk_gemv_ctas(V) : q.f.S;
+  return q;
+}
+
+struct ScoreLayout {
+  size_t zt = 0, part = 0, z = 0, rec = 0, bad = 0, idx = 0, blk = 0, count = 0, hc = 0, total = 0;
+};
+ScoreLayout score_layout(int64_t N, int64_t H, int64_t V, int64_t k, const ScorePlan& q) {
+  ScoreLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  const size_t n = static_cast<size_t>(std::max<int64_t>(N, 1)), rows = static_cast<size_t>(std::max(1LL, q.rows));
+  L.zt = take(k == 0 ? n * 4 : 0);
+  L.part = take(rows * q.S * 16);
+  L.z = take(k > 0 && (q.dense || q.gemv) ? rows * round_up(V, BN) * 4 : 0);
+  L.rec = take(k > 0 && !q.dense ? rows * q.ld * 8 : 0);
+  L.bad = take(256);
+  if (!q.gemv && N >= skip_min_rows()) {
+    L.idx = take(n * 4);
+    L.blk = take(static_cast<size_t>(ceil_div(N, COMPACT_ROWS_PER_BLOCK)) * 4);
+    L.count = take(256);
+    L.hc = take(rows * H * 2);
+  }
+  L.total = o;
+  return L;
+}
+
+// How far a record or logit of the forward can be off the row's exact logits,
+// relative to their largest magnitude: each of H / 16 steps cuts its running sum
+// by less than one unit of its last place, 2^-23 of it; the running sum may be 4
+// times the row's largest logit (and the few-row forward's rounded sums are off
+// by less); the column in a record's low bits changes it by 2^-18.
+float score_slack(int64_t H) {
+  return static_cast<float>(4.0 * static_cast<double>(ceil_div(H, UMMA_K)) / 8388608.0 + 1.0 / 131072.0);
+}
+
+flce_status score_rows(const ScorePlan& q, bool kLong, const ScoreRows& rows, const float4* part, const float2* rec,
+                       const float* z, const flce_bf16* h, const flce_bf16* W, const GemmParams& tf,
+                       const int64_t* targets, long long ignore, const float* zt, const ScoreOut& out,
+                       cudaStream_t st) {
+  ProfScope ps(K_SCORE, st);
+  if (out.k == 0) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(rows.rows, SMALL_THREADS / 32)));
+    auto go = [&](auto kern) {
+      return launch_dependent(kern, grid, SMALL_THREADS, 0, st, part, q.S, rows, zt, targets, ignore, tf.V, out);
+    };
+    FLCE_CUDA_TRY(kLong ? go(score_row_kernel<true>) : go(score_row_kernel<false>));
+    return FLCE_OK;
+  }
+  SelectParams p{};
+  p.h = h;
+  p.W = W;
+  p.part = part;
+  p.rec = rec;
+  p.z = z;
+  p.S = q.S;
+  p.ld = static_cast<int>(q.ld);
+  p.H = tf.H;
+  p.V = tf.V;
+  p.rows = rows;
+  p.targets = targets;
+  p.ignore = ignore;
+  p.slack = score_slack(tf.H);
+  p.tf_softcap = tf.tf_softcap;
+  p.tf_a = tf.tf_a;
+  p.tf_b = tf.tf_b;
+  p.out = out;
+  auto go = [&](auto kern, int threads) {
+    return launch_dependent(kern, dim3(static_cast<unsigned>(rows.rows)), threads, 0, st, p);
+  };
+  if (q.dense)
+    FLCE_CUDA_TRY((kLong ? go(score_select_kernel<256, true, true>, 256) : go(score_select_kernel<256, true, false>, 256)));
+  else
+    FLCE_CUDA_TRY((kLong ? go(score_select_kernel<256, false, true>, 256)
+                         : go(score_select_kernel<256, false, false>, 256)));
+  return FLCE_OK;
+}
+
+flce_status score_gemv(const ScorePlan& q, const GemmParams& p, const flce_bf16* h, const flce_bf16* W, float* z,
+                       float2* rec, const int64_t* targets, float* zt, float4* part, cudaStream_t st) {
+  const int ldz = static_cast<int>(round_up(p.V, BN));
+  {
+    ProfScope ps(K_FWD, st);
+    auto go = [&](auto kern, int nr) -> cudaError_t {
+      const size_t smem = static_cast<size_t>(nr) * p.H * 4;
+      cudaError_t e =
+          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGemvMaxSmem));
+      if (e != cudaSuccess) return e;
+      return launch_dependent(kern, dim3(q.S), 32 * TOPK_GEMV_WARPS, smem, st, h, W, p.N, p.H, p.V, z, ldz, targets, zt,
+                              p.tf_softcap, p.tf_a, p.tf_b, part);
+    };
+    FLCE_CUDA_TRY(p.N == 1   ? go(score_gemv_kernel<1>, 1)
+                  : p.N == 2 ? go(score_gemv_kernel<2>, 2)
+                             : go(score_gemv_kernel<4>, 4));
+  }
+  if (rec == nullptr) return FLCE_OK;
+  ProfScope ps(K_SCORE, st);
+  const long long units = static_cast<long long>(p.N) * ceil_div(p.V, 32);
+  FLCE_CUDA_TRY(launch_dependent(score_record_kernel, dim3(static_cast<unsigned>(ceil_div(units, SMALL_THREADS / 32))),
+                                 SMALL_THREADS, 0, st, static_cast<const float*>(z), p.N, p.V, ldz, rec,
+                                 static_cast<int>(q.ld)));
+  return FLCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t flce_score_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k) {
+  if (!topk_sizes_ok(N, H, V) || k < 0 || k > SCORE_MAX_K || k > V) return 0;
+  const int cg = cta_group();
+  return score_layout(N, H, V, k, score_plan(N, H, V, k, device_workers(cg), BM * cg)).total;
+}
+
+flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* targets, int64_t N, int64_t H, int64_t V,
+                       int64_t k, int64_t ignore_index, const flce_logit_transform* transform, float* out_logp,
+                       float* out_lse, float* out_entropy, int64_t* out_ids, float* out_logprobs, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!topk_sizes_ok(N, H, V) || k < 0 || k > V) return FLCE_ERR_INVALID_ARG;
+  GemmParams tfp{};
+  if (!transform_params(transform, tfp)) return FLCE_ERR_INVALID_ARG;
+  // (an empty tensor has no address)
+  if (N > 0 && !out_logp && !out_lse && !out_entropy && !out_ids && !out_logprobs) return FLCE_ERR_INVALID_ARG;
+  if (N > 0 && ((out_logp && !targets) || ((out_ids || out_logprobs) != (k > 0)))) return FLCE_ERR_INVALID_ARG;
+  if (N > 0 && (!h || !W)) return FLCE_ERR_INVALID_ARG;
+  if (k > SCORE_MAX_K || H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(targets, 8) || !aligned(out_logp, 4) || !aligned(out_lse, 4) ||
+      !aligned(out_entropy, 4) || !aligned(out_ids, 8) || !aligned(out_logprobs, 4))
+    return FLCE_ERR_UNSUPPORTED;
+  if (N == 0) return FLCE_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int cg = cta_group(), tm = BM * cg;
+  const int workers = device_workers(cg);
+  const ScorePlan q = score_plan(N, H, V, k, workers, tm);
+  const ScoreLayout L = score_layout(N, H, V, k, q);
+  Workspace ws;
+  flce_status s = get_workspace(ws, workspace, workspace_bytes, L.total, st);
+  if (s != FLCE_OK) return s;
+  uint8_t* wb = static_cast<uint8_t*>(ws.ptr);
+  float* zt = k == 0 ? reinterpret_cast<float*>(wb + L.zt) : nullptr;
+  float4* part = reinterpret_cast<float4*>(wb + L.part);
+  float* z = k > 0 && (q.dense || q.gemv) ? reinterpret_cast<float*>(wb + L.z) : nullptr;
+  float2* rec = k > 0 && !q.dense ? reinterpret_cast<float2*>(wb + L.rec) : nullptr;
+  const int Ni = static_cast<int>(N);
+  if (targets != nullptr && validate_on()) {
+    int* bad = reinterpret_cast<int*>(wb + L.bad);
+    FLCE_CUDA_TRY(cudaMemsetAsync(bad, 0, sizeof(int), st));
+    prep_kernel<<<static_cast<int>(ceil_div(N, SMALL_THREADS)), SMALL_THREADS, 0, st>>>(
+        targets, Ni, static_cast<int>(V), ignore_index, nullptr, bad);
+    FLCE_CUDA_TRY(cudaGetLastError());
+    int nbad = 0;
+    FLCE_CUDA_TRY(cudaMemcpyAsync(&nbad, bad, sizeof(int), cudaMemcpyDeviceToHost, st));
+    FLCE_CUDA_TRY(cudaStreamSynchronize(st));
+    if (nbad != 0) return FLCE_ERR_BAD_TARGET;
+  }
+  const ScoreOut out{out_logp, out_lse, out_entropy, out_ids, out_logprobs, static_cast<int>(k)};
+  const bool kLong = q.rows * std::max<long long>(q.ld, q.S) >= INT_MAX;
+  GemmParams p{};
+  p.n_tiles = q.f.n_tiles;
+  p.k_blocks = q.f.k_blocks;
+  p.cols = q.f.S;
+  p.n_per_unit = q.f.tps;
+  p.kb_per_split = q.f.k_blocks;
+  p.k_splits = 1;
+  p.N = Ni;
+  p.H = static_cast<int>(H);
+  p.V = static_cast<int>(V);
+  p.targets = targets;
+  p.ignore_index = ignore_index;
+  p.zt = zt;
+  p.tf_softcap = tfp.tf_softcap;
+  p.tf_a = tfp.tf_a;
+  p.tf_b = tfp.tf_b;
+  p.tf_d = tfp.tf_d;
+  p.score_part = part;
+  p.rec = rec;
+  p.z = q.dense ? z : nullptr;
+  p.rec_ld = static_cast<int>(q.ld);
+  if (q.gemv) {
+    s = score_gemv(q, p, h, W, z, rec, targets, zt, part, st);
+    if (s != FLCE_OK) return s;
+    return score_rows(q, kLong, ScoreRows{0, Ni, nullptr, nullptr, 0}, part, rec, z, h, W, p, targets, ignore_index, zt,
+                      out, st);
+  }
+  // the rows without a target to score are left out, as flce_forward_ex2 does
+  const bool skip = targets != nullptr && compact_on() && L.hc != 0;
+  int* idx = reinterpret_cast<int*>(wb + L.idx);
+  int* count = reinterpret_cast<int*>(wb + L.count);
+  uint16_t* hc = reinterpret_cast<uint16_t*>(wb + L.hc);
+  if (skip) {
+    s = list_valid_rows(targets, Ni, ignore_index, reinterpret_cast<int*>(wb + L.blk), idx, count, false, st);
+    if (s != FLCE_OK) return s;
+    ProfScope ps(K_SCORE, st);
+    const long long grid = std::min<long long>(ceil_div(N, SMALL_THREADS / 32), 8LL * device_sms());
+    score_skipped_kernel<<<static_cast<unsigned>(grid), SMALL_THREADS, 0, st>>>(targets, ignore_index, Ni, out);
+    FLCE_CUDA_TRY(cudaGetLastError());
+  }
+  CUtensorMap tA, tB;
+  if (!make_map(&tA, skip ? hc : h, H, skip ? q.rows : N, H, BK, BM) || !make_map(&tB, W, H, V, H, BK, BN / cg))
+    return FLCE_ERR_CUDA;
+  int* err = nullptr;
+  FLCE_CUDA_TRY(cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_device_error));
+  p.err = err;
+  for (long long row0 = 0; row0 < N; row0 += q.rows) {
+    GemmParams g = p;
+    g.tf_a *= 1.f + mma_cut(H);
+    g.row0 = static_cast<int>(row0);
+    g.rows = static_cast<int>(std::min(q.rows, N - row0));
+    g.rows_cap = g.rows;
+    g.m_tiles = static_cast<int>(ceil_div(g.rows, tm));
+    g.num_units = g.m_tiles * q.f.S;
+    g.group_m = std::min(16, g.m_tiles);
+    ScoreRows rows{g.row0, g.rows, nullptr, nullptr, 0};
+    if (skip) {
+      g.row0 = 0;
+      g.row_idx = idx;
+      g.dyn_count = count;
+      g.chunk_first = static_cast<int>(row0);
+      rows = ScoreRows{0, g.rows, idx, count, g.chunk_first};
+      s = gather_rows(h, H, idx, count, Ni, row0, q.rows, hc, st);
+      if (s != FLCE_OK) return s;
+    }
+    {
+      ProfScope ps(K_FWD, st);
+      const int w = std::min(g.num_units, workers);
+      FLCE_CUDA_TRY(k > 0 ? (launch_scored<MODE_FWD, SCORE_TOP>(cg, kLong, tA, tB, tB, g, w, st))
+                          : (launch_scored<MODE_FWD, SCORE_ENTROPY>(cg, kLong, tA, tB, tB, g, w, st)));
+    }
+    s = score_rows(q, kLong, rows, part, rec, z, h, W, p, targets, ignore_index, zt, out, st);
+    if (s != FLCE_OK) return s;
+  }
+  return FLCE_OK;
+}
+
+size_t flce_score_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t chunk_rows, int32_t dW_type) {
+  return flce_topk_kd_backward_workspace_bytes(N, H, V, chunk_rows, dW_type);
+}
+
+flce_status flce_score_backward(const flce_bf16* h, const flce_bf16* W, const int64_t* targets, const float* lse,
+                                const float* entropy, const float* g_logp, const float* g_entropy, flce_bf16* dH,
+                                void* dW, int32_t dW_type, int64_t N, int64_t H, int64_t V, int64_t chunk_rows,
+                                int64_t ignore_index, const flce_logit_transform* transform, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (!topk_sizes_ok(N, H, V) || !topk_dw_ok(dW, dW_type)) return FLCE_ERR_INVALID_ARG;
+  GemmParams tfp{};
+  if (!transform_params(transform, tfp) || (N > 0 && !dH && !dW)) return FLCE_ERR_INVALID_ARG;
+  if (N > 0 && (!h || !W || !targets || !lse || !entropy)) return FLCE_ERR_INVALID_ARG;
+  if (H % 8 != 0 || !aligned(dW, 16) || !aligned(dH, 16) || !aligned(h, 16) || !aligned(W, 16) ||
+      !aligned(targets, 8) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4))
+    return FLCE_ERR_UNSUPPORTED;
+  if (N == 0 && !dW) return FLCE_OK;
+  const bool bf16 = dW != nullptr && dW_type == FLCE_BF16;
+  const TopkGrad tg = topk_grad(dW ? dW_type : FLCE_F32, N, H, V, bf16 ? topk_bwd_rows(N, H, V, chunk_rows) : 0);
+  ScoreGrads sc{entropy, g_logp, g_entropy, bf16 && !tg.scratch ? static_cast<flce_bf16*>(dW) : nullptr};
+  const size_t inner = align256(flce_workspace_bytes(N, H, V, chunk_rows));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Workspace ws;
+  flce_status s = get_workspace(ws, workspace, workspace_bytes, inner + tg.bytes, st);
+  if (s != FLCE_OK) return s;
+  float* sum = tg.scratch ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws.ptr) + inner)
+                          : bf16 ? nullptr : static_cast<float*>(dW);
+  s = backward_impl(h, W, targets, nullptr, lse, 1.f, dH, sum, N, H, V, chunk_rows, ignore_index, transform, ws.ptr,
+                    inner, stream, nullptr, nullptr, nullptr, &sc);
+  if (s != FLCE_OK || !tg.scratch) return s;
+  return topk_round_dw(sum, V * H, dW, nullptr, 1.f, st);
+}
+
+}  // extern "C"

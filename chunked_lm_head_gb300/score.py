@@ -1,0 +1,139 @@
+"""Scores of the LM head's distribution softmax(f(h W^T)), from PyTorch.
+
+``selective_log_softmax_entropy`` gives the log-probability of each row's target
+and the entropy, differentiable in both; ``top_logprobs`` the K likeliest words
+of each row with their log-probabilities.  ``score_forward`` and
+``score_backward`` are the calls below them.  Every arithmetic step runs in
+libflce's CUDA kernels (include/flce.h states the formulas); this module checks
+tensor properties, allocates outputs and passes pointers.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import _lib
+from .api import IGNORE_INDEX, _first_order
+from .topk import _DW, _workspace
+
+
+def _on(x):
+    """The device of x as the current one, for the length of a call."""
+    return contextlib.nullcontext() if x.device.index == torch.cuda.current_device() else torch.cuda.device(x.device)
+
+
+def _check(h, W, targets):
+    for x in (h, W):
+        if not x.is_cuda or x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_contiguous():
+            raise ValueError("h and W must be contiguous 2-D bfloat16 CUDA tensors")
+    if W.shape[1] != h.shape[1] or W.device != h.device:
+        raise ValueError("expected h[N,H] and W[V,H] on one device")
+    if targets is not None and (targets.dtype != torch.int64 or targets.shape != (h.shape[0],) or
+                                targets.device != h.device or not targets.is_contiguous()):
+        raise ValueError("targets must be a contiguous int64 [N] tensor on h's device")
+
+
+def _row_vector(x, h, name):
+    if x is not None and (x.dtype != torch.float32 or x.shape != (h.shape[0],) or x.device != h.device or
+                          not x.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 [N] tensor on h's device")
+
+
+def score_forward(h, W, targets=None, k: int = 0, ignore_index: int = IGNORE_INDEX, transform=None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """dict(logp[N] or None, lse[N], entropy[N] f32, ids[N,k] i64 or None,
+    logprobs[N,k] f32 or None) on device.
+
+    logp: log-probability of each row's target (None without targets).  k > 0
+    (at most 128 and V): the k words of largest logit in descending order, ties
+    to the lowest index, and their log-probabilities; the order is that of the
+    exact sums h W^T.  A row whose target is ignore_index is skipped: zeros, and
+    ids of -1.  A row with a logit that is NaN or +infinity: NaN, ids of -1.
+    transform: as in forward()."""
+    _check(h, W, targets)
+    (N, H), V, dev = h.shape, W.shape[0], h.device
+    if not 0 <= k <= V:
+        raise ValueError("k must be between 0 and the vocabulary")
+    with _on(h):
+        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        entropy = torch.empty_like(lse)
+        logp = None if targets is None else torch.empty_like(lse)
+        ids = torch.empty((N, k), dtype=torch.int64, device=dev) if k else None
+        words = torch.empty((N, k), dtype=torch.float32, device=dev) if k else None
+        ws, ws_bytes = _workspace(workspace, _lib.flce_score_workspace_bytes(N, H, V, k), stream, dev)
+        _lib.check("flce_score", _lib.flce_score(h, W, targets, N, H, V, k, ignore_index, transform, logp, lse, entropy,
+                                                 ids, words, ws, ws_bytes, stream))
+    return {"logp": logp, "lse": lse, "entropy": entropy, "ids": ids, "logprobs": words}
+
+
+def score_backward(h, W, targets, lse, entropy, grad_logp=None, grad_entropy=None, chunk_rows: int = 256,
+                   ignore_index: int = IGNORE_INDEX, transform=None, need_dH: bool = True, need_dW: bool = True,
+                   workspace: torch.Tensor | None = None, stream=None, dW_dtype=torch.float32):
+    """(dH[N,H] bf16 or None, dW[V,H] of dW_dtype (float32 or bfloat16) or None)
+    of sum_i grad_logp[i] logp[i] + grad_entropy[i] entropy[i] (either may be
+    None: zero), from the forward's lse and entropy."""
+    _check(h, W, targets)
+    if targets is None:
+        raise ValueError("targets are needed")
+    if dW_dtype not in _DW:
+        raise ValueError("dW_dtype must be float32 or bfloat16")
+    for x, name in ((lse, "lse"), (entropy, "entropy"), (grad_logp, "grad_logp"), (grad_entropy, "grad_entropy")):
+        _row_vector(x, h, name)
+    (N, H), V, dev = h.shape, W.shape[0], h.device
+    with _on(h):
+        dH = torch.empty_like(h) if need_dH else None
+        dW = torch.empty((V, H), dtype=dW_dtype, device=dev) if need_dW else None
+        ws, ws_bytes = _workspace(workspace, _lib.flce_score_backward_workspace_bytes(N, H, V, chunk_rows, _DW[dW_dtype]),
+                                  stream, dev)
+        _lib.check("flce_score_backward", _lib.flce_score_backward(
+            h, W, targets, lse, entropy, grad_logp, grad_entropy, dH, dW, _DW[dW_dtype], N, H, V, chunk_rows,
+            ignore_index, transform, ws, ws_bytes, stream))
+    return dH, dW
+
+
+class SelectiveLogSoftmaxEntropy(torch.autograd.Function):
+    """selective_log_softmax_entropy with the logits recomputed in the backward."""
+
+    @staticmethod
+    def forward(ctx, h, W, targets, chunk_rows, ignore_index, transform):
+        ctx.set_materialize_grads(False)  # no zeros for an output without a gradient
+        out = score_forward(h, W, targets, 0, ignore_index, transform)
+        ctx.save_for_backward(h, W, targets, out["lse"], out["entropy"])
+        ctx.chunk_rows, ctx.ignore_index, ctx.transform = chunk_rows, ignore_index, transform
+        return out["logp"], out["entropy"]
+
+    @staticmethod
+    def backward(ctx, grad_logp, grad_entropy):
+        need_h, need_W = ctx.needs_input_grad[:2]
+        if (grad_logp is None and grad_entropy is None) or not (need_h or need_W):
+            return (None,) * 6
+        h, W, targets, lse, entropy = ctx.saved_tensors
+        ga, ge = (None if g is None else g.detach().to(torch.float32).contiguous() for g in (grad_logp, grad_entropy))
+        dH, dW = score_backward(h.detach(), W.detach(), targets, lse, entropy.detach(), ga, ge, ctx.chunk_rows,
+                                ctx.ignore_index, ctx.transform, need_h, need_W, dW_dtype=W.dtype)
+        return _first_order((dH, dW), (h, W, grad_logp, grad_entropy)) + (None,) * 4
+
+
+def selective_log_softmax_entropy(h, W, targets, chunk_rows: int = 256, ignore_index: int = IGNORE_INDEX,
+                                  transform=None):
+    """(logp[N], entropy[N]) fp32: log-probability of each row's target and entropy
+    (natural units) of softmax(f(h W^T)), both differentiable in h and W; 0 on
+    rows whose target is ignore_index.  For policy losses with an entropy term:
+    both come out of one pass over the head, and both gradients of another."""
+    if targets is None:
+        raise ValueError("targets are needed")
+    if not torch.is_grad_enabled() or not (h.requires_grad or W.requires_grad):
+        out = score_forward(h, W, targets, 0, ignore_index, transform)
+        return out["logp"], out["entropy"]
+    return SelectiveLogSoftmaxEntropy.apply(h, W, targets, chunk_rows, ignore_index, transform)
+
+
+def top_logprobs(h, W, k: int, targets=None, ignore_index: int = IGNORE_INDEX, transform=None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """score_forward with k words: the alternatives of a sampled token, or the
+    lists (ids, logprobs, and a log-sum-exp of 0) that topk_distill_loss takes
+    of a teacher.  Not differentiable."""
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    return score_forward(h, W, targets, k, ignore_index, transform, workspace, stream)

@@ -40,8 +40,8 @@
  *   - Not thread-safe for concurrent calls from several host threads while
  *     profiling is enabled.
  *   - CUDA graphs: flce_forward(_ex), flce_backward(_ex),
- *     flce_forward_backward, the distillation (two heads or top logits), norm
- *     and e4m3 entry points can be captured into a CUDA graph and replayed
+ *     flce_forward_backward, the distillation (two heads or top logits), norms,
+ *     score and e4m3 entry points can be captured into a CUDA graph and replayed
  *     when they are given a caller workspace, FLCE_VALIDATE is unset,
  *     profiling is off, and one eager call of the same kind has run on the
  *     device first (it sets kernel attributes and caches the device's
@@ -701,6 +701,93 @@ FLCE_API flce_status flce_rms_norm_backward(const flce_bf16* dy, const void* s, 
                                             int64_t N, int64_t H, flce_bf16* dx, float* dr, void* dweight,
                                             void* workspace, size_t workspace_bytes, void* stream);
 FLCE_API size_t flce_rms_norm_backward_workspace_bytes(int64_t N, int64_t H);
+
+/*
+ * Layer norm in front of the LM head, with the residual's addition (an addition
+ * of this library).  Per row, with s the residual stream as it is stored,
+ *   s    = round(x + residual)      (residual's type; s = x without one)
+ *   mean = mean_j s_j,  rstd = 1 / sqrt(mean_j (s_j - mean)^2 + eps)
+ *   y_j  = (s_j - mean) * rstd * (weight_j + weight_offset) + bias_j.
+ *   bias     [H] of weight's type, or NULL.
+ *   out_mean, out_rstd [N] fp32 or NULL (flce_layer_norm_backward needs both).
+ * The other arguments, and the sizes, alignments and strides, as flce_rms_norm.
+ */
+FLCE_API flce_status flce_layer_norm(const flce_bf16* x, int64_t ldx, const void* residual, int64_t ldr,
+                                     int32_t residual_type, const void* weight, const void* bias,
+                                     int32_t weight_type, float weight_offset, float eps, int64_t N,
+                                     int64_t H, flce_bf16* out_y, void* out_residual, float* out_mean,
+                                     float* out_rstd, void* stream);
+
+/*
+ * Gradients of flce_layer_norm, with g_j = dy_j (weight_j + weight_offset) and
+ * n_j = (s_j - mean) rstd:
+ *   d_j       = ds_j + rstd (g_j - mean_k g_k - n_j mean_k(g_k n_k))
+ *   dweight_j = sum_rows dy_j n_j,  dbias_j = sum_rows dy_j
+ * dweight, dbias [H] of weight_type; dx, dr, dweight and dbias may each be NULL,
+ * not all.  The other arguments as flce_rms_norm_backward.  The sums are fp32 in a
+ * fixed order: same inputs, same bits.  Workspace (for dweight and dbias):
+ * flce_layer_norm_backward_workspace_bytes, or NULL (stream-ordered allocation).
+ */
+FLCE_API flce_status flce_layer_norm_backward(const flce_bf16* dy, const void* s, int64_t lds,
+                                              int32_t s_type, const void* ds, const void* weight,
+                                              int32_t weight_type, float weight_offset, const float* mean,
+                                              const float* rstd, int64_t N, int64_t H, flce_bf16* dx,
+                                              float* dr, void* dweight, void* dbias, void* workspace,
+                                              size_t workspace_bytes, void* stream);
+FLCE_API size_t flce_layer_norm_backward_workspace_bytes(int64_t N, int64_t H);
+
+/*
+ * Scores of the head's distribution p = softmax(f(z)) (an addition of this
+ * library): log-probability of given tokens, entropy, and the k likeliest words,
+ * in one pass over W.  Per row i, with u = f(z[i,:]),
+ *   lse      = log sum_v e^u_v
+ *   logp     = u_t - lse,             t = targets[i]
+ *   entropy  = -sum_v p_v log p_v     (natural units)
+ *   ids      = the k words of largest z in descending order, ties to the lowest
+ *              index (of equal sums; the order is that of the sums of h W^T to
+ *              about 2^-45, not of the tensor cores' fp32 ones)
+ *   logprobs = u_ids - lse.
+ *   targets  [N] int64 or NULL.  A row whose target is ignore_index is skipped:
+ *            its outputs are 0 and its ids -1.  A target outside [0,V) gives a
+ *            NaN logp (or FLCE_ERR_BAD_TARGET as in flce_forward).
+ *   k        0, or 1 .. min(128, V) (above 128: FLCE_ERR_UNSUPPORTED).
+ *   out_logp (needs targets), out_lse, out_entropy [N] fp32, each may be NULL;
+ *   out_ids [N,k] int64 and out_logprobs [N,k] fp32: NULL exactly when k is 0,
+ *            else one of them may be.  At least one output.
+ * A row with a logit z that is NaN or +infinity (with a soft-cap, any infinity),
+ * or none above -infinity: NaN, ids of -1.  N <= 2^31 - 65,537.  Workspace:
+ * flce_score_workspace_bytes(N, H, V, k), or NULL (stream-ordered allocation); it
+ * holds at most about 256 MB of the rows' chunk maxima (or, where V < 256 k,
+ * logits) at once.
+ */
+FLCE_API flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* targets, int64_t N,
+                                int64_t H, int64_t V, int64_t k, int64_t ignore_index,
+                                const flce_logit_transform* transform, float* out_logp, float* out_lse,
+                                float* out_entropy, int64_t* out_ids, float* out_logprobs,
+                                void* workspace, size_t workspace_bytes, void* stream);
+FLCE_API size_t flce_score_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k);
+
+/*
+ * Gradients of sum_i g_logp[i] logp[i] + g_entropy[i] entropy[i]:
+ *   D[i,v] = (g_logp ([v == t] - p_v) - g_entropy p_v (log p_v + entropy)) f'(z)
+ *   dH = D W,  dW = D^T h
+ * with the logits recomputed block by block as in flce_backward (chunk_rows
+ * bounds the dlogits held at once).  lse, entropy [N] from flce_score; g_logp,
+ * g_entropy [N] fp32, each may be NULL (zero).  Rows whose target is
+ * ignore_index have no gradient; a target outside [0,V) has no one-hot term.
+ *   dH [N,H] bf16, dW [V,H] of dW_type (FLCE_F32 or FLCE_BF16); either may be
+ *   NULL, not both.
+ * Workspace: flce_score_backward_workspace_bytes, or NULL (stream-ordered
+ * allocation).
+ */
+FLCE_API flce_status flce_score_backward(const flce_bf16* h, const flce_bf16* W, const int64_t* targets,
+                                         const float* lse, const float* entropy, const float* g_logp,
+                                         const float* g_entropy, flce_bf16* dH, void* dW, int32_t dW_type,
+                                         int64_t N, int64_t H, int64_t V, int64_t chunk_rows,
+                                         int64_t ignore_index, const flce_logit_transform* transform,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+FLCE_API size_t flce_score_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t chunk_rows,
+                                                    int32_t dW_type);
 
 /*
  * Forward that allocates nothing (no counterpart on the source pages: the
