@@ -126,9 +126,10 @@ SIGNATURES = {
                                                 _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
     "flce_layer_norm_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64]),
     "flce_score": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp,
-                                  _c_vp, _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
+                                  _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
+    "flce_score_state_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64]),
     "flce_score_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64]),
-    "flce_score_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+    "flce_score_backward": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
                                            ctypes.c_int32, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp,
                                            ctypes.c_size_t, _c_vp]),
     "flce_score_backward_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int32]),
@@ -585,21 +586,25 @@ def flce_layer_norm_backward_workspace_bytes(N, H) -> int:
 
 
 def flce_score(h, W, targets, N, H, V, k, ignore_index, transform, out_logp, out_lse, out_entropy, out_ids,
-               out_logprobs, workspace=None, workspace_bytes=0, stream=None) -> int:
+               out_logprobs, state=None, workspace=None, workspace_bytes=0, stream=None) -> int:
     """Raw C call of the head's scores."""
     tp, keep = _tf_ptr(transform)
     return load().flce_score(_ptr(h), _ptr(W), _ptr(targets), N, H, V, k, ignore_index, tp, _ptr(out_logp),
-                             _ptr(out_lse), _ptr(out_entropy), _ptr(out_ids), _ptr(out_logprobs), _ptr(workspace),
-                             workspace_bytes, _stream_handle(stream))
+                             _ptr(out_lse), _ptr(out_entropy), _ptr(out_ids), _ptr(out_logprobs), _ptr(state),
+                             _ptr(workspace), workspace_bytes, _stream_handle(stream))
 
 
-def flce_score_backward(h, W, targets, lse, entropy, g_logp, g_entropy, dH, dW, dW_type, N, H, V, chunk_rows,
+def flce_score_backward(h, W, targets, lse, entropy, g_logp, g_entropy, state, dH, dW, dW_type, N, H, V, chunk_rows,
                         ignore_index, transform, workspace=None, workspace_bytes=0, stream=None) -> int:
     """Raw C call of the scores' gradients."""
     tp, keep = _tf_ptr(transform)
     return load().flce_score_backward(_ptr(h), _ptr(W), _ptr(targets), _ptr(lse), _ptr(entropy), _ptr(g_logp),
-                                      _ptr(g_entropy), _ptr(dH), _ptr(dW), dW_type, N, H, V, chunk_rows, ignore_index,
-                                      tp, _ptr(workspace), workspace_bytes, _stream_handle(stream))
+                                      _ptr(g_entropy), _ptr(state), _ptr(dH), _ptr(dW), dW_type, N, H, V, chunk_rows,
+                                      ignore_index, tp, _ptr(workspace), workspace_bytes, _stream_handle(stream))
+
+
+def flce_score_state_bytes(N, H, V, chunk_rows) -> int:
+    return int(load().flce_score_state_bytes(N, H, V, chunk_rows))
 
 
 def flce_score_workspace_bytes(N, H, V, k) -> int:

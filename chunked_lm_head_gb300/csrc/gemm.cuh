@@ -273,12 +273,13 @@ struct GemmParams {
   const int* out_count;
   // DW: the rows of h repeat after this many K blocks (0: they do not)
   int dw_h_blocks;
-  int ld_mx;  // FUSED_FWD with listed columns: row pitch of mx, a multiple of 8 that covers whole tiles
-  // scores (the kernel's kScore).  The forward: per row of the pass and split
-  // [rows][cols] a partial (ScorePart), and per row and 32-column chunk
-  // [rows][rec_ld] its record (score_key).  The dlogits units: each row's entropy
-  // and the gradients of its log-probability and entropy ([N], a gradient may be
-  // null: zero)
+  int ld_mx;  // FUSED_FWD with listed columns or scores: row pitch of mx, a multiple of 8 that covers whole tiles
+  // scores (the kernel's kScore).  The forwards: per row of the pass, split and
+  // column part [rows][cols][2] a partial (ScorePart), and per row and 32-column
+  // chunk [rows][rec_ld] its record (score_key); FUSED_FWD instead the chunks'
+  // maxima in mx and the logits relative to them, fp16, through tmC.  The dlogits
+  // units: each row's entropy and the gradients of its log-probability and
+  // entropy ([N], a gradient may be null: zero)
   float4* score_part;
   float2* rec;
   float* z;    // in the records' place: the logits [rows][rec_ld], fp32
@@ -288,10 +289,12 @@ struct GemmParams {
   const float* g_entropy;
 };
 
-// Which epilogues a kernel has beside its mode's.
+// Which epilogues a kernel has beside its mode's.  (They run 8 epilogue warps
+// but in PIPE: 32 columns' exponentials, products and records take as long as
+// the MMAs over a hidden size of 1,000 with 4.)
 enum Score : int {
   SCORE_NONE = 0,
-  SCORE_ENTROPY = 1,  // entropy beside the log-sum-exp (forward) and its gradient (dlogits units)
+  SCORE_ENTROPY = 1,  // entropy beside the log-sum-exp (forwards) and its gradient (dlogits units)
   SCORE_TOP = 2       // forward: entropy, and what the likeliest words are found from (chunk records, or logits)
 };
 
@@ -784,6 +787,14 @@ __device__ __forceinline__ void mma_commit_all(uint32_t bar) {
     umma_commit_pair_mc(bar, 0x3);  // the barrier at this offset in both CTAs
 }
 
+// tanh as 1 - 2 / (1 + e^2x), by the SFU's exponential and reciprocal: off by at
+// most 2^-21.5 absolutely (both are good to 2^-22, the quotient is at most 2),
+// which a soft-capped logit, cap tanh(z / cap), has anyway from a z of its size.
+// A fifth of tanhf's instructions.
+__device__ __forceinline__ float cap_tanh(float x) {
+  return fmaf(-1.f, __fdividef(2.f, 1.f + ex2_approx(2.f * kLog2e * x)), 1.f);
+}
+
 // v[j] for a run-time j in [0, 32) without dynamic register indexing (which
 // would move v to local memory): a 5-level select tree on the bits of j.
 __device__ __forceinline__ float select32(const float (&v)[32], int j) {
@@ -1121,8 +1132,9 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
     const int r = q * 32 + lane;       // accumulator row owned by this thread
     // columns of the tile this warp takes: all, or one half (8 epilogue warps)
     static_assert(EW == EPI_WARPS || (EW == 2 * EPI_WARPS && wide_epilogue_mode<MODE>()) ||
+                      (EW == 2 * EPI_WARPS && kScore != SCORE_NONE && MODE != MODE_PIPE) ||
                       (EW == 4 * EPI_WARPS && MODE == MODE_DW),
-                  "8 epilogue warps: dW, DHDW, the two-head dlogits and the Jensen-Shannon terms; "
+                  "8 epilogue warps: dW, DHDW, the two-head dlogits, the Jensen-Shannon terms and the scores; "
                   "16: dW only");
     constexpr int kColParts = EW / 4;
     constexpr int kChunks = K::TILE_N / 32 / kColParts;
@@ -1155,8 +1167,9 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
       float scale = 0.f, nl2 = 0.f, nlt = 0.f;              // DLOGITS / KD_DLOGITS
       static_assert(kScore == SCORE_NONE || (!kF8 && !kSp && !kOut16), "scores: bf16 operands, no listed columns");
       static_assert(kScore == SCORE_NONE || MODE == MODE_FWD ||
-                        (kScore == SCORE_ENTROPY && (MODE == MODE_DLOGITS || MODE == MODE_PIPE)),
-                    "scores: the forward and, for the entropy, the dlogits units");
+                        (kScore == SCORE_ENTROPY &&
+                         (MODE == MODE_FUSED_FWD || MODE == MODE_DLOGITS || MODE == MODE_PIPE)),
+                    "scores: the forwards and, for the entropy, the dlogits units");
       float run_ent = 0.f, run_abs = 0.f;                   // FWD scores: sum 2^(x - m) (m - x), a largest |z|
       float sc_a = 0.f, sc_b = 0.f, sc_t = 0.f;             // DLOGITS scores: D = p (sc_a log2 p + sc_b) + onehot sc_t
       float2 rec_even = make_float2(0.f, 0.f);
@@ -1261,7 +1274,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
           }
           const int col0 = n * K::TILE_N + c * 32;
-          if constexpr (MODE == MODE_FWD && kScore != SCORE_NONE) {
+          if constexpr ((MODE == MODE_FWD || MODE == MODE_FUSED_FWD) && kScore != SCORE_NONE) {
             // entropy = log S + C / S with S = sum 2^(x - m) and C = ln 2 sum
             // 2^(x - m) (m - x), which holds for any m: every term is positive
             // where m is the row's maximum, and nothing cancels (lse - sum p x
@@ -1293,7 +1306,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
             if (p.tf_softcap) {
               // (an infinite logit, which tanh would hide, becomes NaN: 0 z)
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], 0.f, p.tf_b * tanhf(p.tf_a * v[j]));
+              for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], 0.f, p.tf_b * cap_tanh(p.tf_a * v[j]));
             }
             if (nc < 32) {
 #pragma unroll
@@ -1304,23 +1317,65 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
 #pragma unroll
             for (int j = 1; j < 32; ++j) cm = fmaxf(cm, v[j]);
             const float nm = fmaxf(run_m, cm * l2a);
-            if (nm != -INFINITY) {
+            // the exponentials' reference: the row's maximum so far, or (kept
+            // logits) the chunk's own
+            const float ref = MODE == MODE_FUSED_FWD ? (cm != -INFINITY ? cm * l2a : 0.f) : nm;
+            uint32_t pk[16];
+            if (MODE == MODE_FUSED_FWD || nm != -INFINITY) {
               float2 a = both(0.f), e = both(0.f);
 #pragma unroll
               for (int j = 0; j < 32; j += 2) {
-                const float2 x = fma2(make_float2(v[j], v[j + 1]), both(l2a), both(-nm));
+                const float2 x = fma2(make_float2(v[j], v[j + 1]), both(l2a), both(-ref));
                 const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                 a = add2(a, w);
                 // (a logit of -infinity has no share: 0, not 0 times infinity)
                 e = fma2(w, make_float2(fmaxf(x.x, -1000.f), fmaxf(x.y, -1000.f)), e);
+                if constexpr (MODE == MODE_FUSED_FWD) pk[j / 2] = pack_f16x2(x.x, x.y);
+              }
+              if constexpr (MODE == MODE_FUSED_FWD) {
+                // from the chunk's reference to the row's (a chunk without a
+                // maximum is empty, or NaN)
+                const float down = cm != -INFINITY && cm == cm ? nm - ref : 0.f;
+                const float f = ex2_approx(-down);
+                const float s = a.x + a.y;
+                e = make_float2(-fmaf(down, s, -(e.x + e.y)) * f, 0.f);
+                a = make_float2(s * f, 0.f);
               }
               const float up = run_m != -INFINITY ? nm - run_m : 0.f;
-              const float r = ex2_approx(run_m - nm);
+              const float r = run_m != -INFINITY ? ex2_approx(run_m - nm) : 0.f;
               run_ent = fmaf(fmaf(up, run_s, run_ent), r, -(e.x + e.y));
               run_s = fmaf(run_s, r, a.x + a.y);
               run_m = nm;
             } else if (cm != cm) {
               run_s = cm;  // NaN throughout, without a maximum so far
+            }
+            if constexpr (MODE == MODE_FUSED_FWD) {
+              // the logits, log2 relative to the chunk's largest, in fp16: exact
+              // to 2^-12 of that distance, so the likely words of a chunk keep
+              // their probability and its logarithm to far less than the
+              // dlogits' own rounding.  Two chunks fill a 32-row x 64-column box
+              // that TMA stores; the maxima leave four at a time
+              const int half = c & 1;
+              const uint32_t box =
+                  out_stage + (warp - 2) * (kBoxes * OUT_BOX_BYTES) + ((c >> 1) % kBoxes) * OUT_BOX_BYTES;
+              if (half == 0) {
+                if (lane == 0) bulk_wait_read<kBoxes - 1>();  // the copy that last used this box has read it
+                __syncwarp();
+              }
+              stage_bf16_half(box, lane, half, pk);
+              if (half == 1) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  const int lrow0 = t.m * C::TM + rank * BM + q * 32;
+                  const int x = col0 - 32;  // first column of the box
+                  if (x < p.ldD && lrow0 < p.rows_cap) tma_store_2d(&tmC, box, x, lrow0);
+                  bulk_commit();
+                }
+              }
+              sp_mx = make_float4(sp_mx.y, sp_mx.z, sp_mx.w, ref);
+              if ((c & 3) == 3 && row_ok)
+                *reinterpret_cast<float4*>(p.mx + static_cast<idx_t>(lr) * p.ld_mx + (col0 / 32 - 3)) = sp_mx;
             }
             if constexpr (kScore == SCORE_ENTROPY) {
               const long long tj = tgt - col0;
@@ -1497,7 +1552,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                     for (int e = 0; e < 2; ++e) {
                       float x, slope = lin_a;
                       if (p.tf_softcap) {
-                        const float th = tanhf(p.tf_a * v[j + e]);
+                        const float th = cap_tanh(p.tf_a * v[j + e]);
                         x = fmaf(p.tf_b * th, kLog2e, nl2);
                         slope = p.tf_d * (1.f - th * th);
                       } else {
@@ -1575,9 +1630,10 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
               // two chunks fill one 32 x 64 box; TMA writes it (rows of the
               // box past the live rows hold zeros: their scale is 0)
               const int half = c & 1;
-              const uint32_t box = out_stage + (warp - 2) * (2 * OUT_BOX_BYTES) + ((c >> 1) & 1) * OUT_BOX_BYTES;
+              const uint32_t box =
+                  out_stage + (warp - 2) * (kBoxes * OUT_BOX_BYTES) + ((c >> 1) % kBoxes) * OUT_BOX_BYTES;
               if (half == 0) {
-                if (lane == 0) bulk_wait_read<1>();  // the copy that last used this box has read it
+                if (lane == 0) bulk_wait_read<kBoxes - 1>();  // the copy that last used this box has read it
                 __syncwarp();
               }
               stage_bf16_half(box, lane, half, pk);
@@ -1874,9 +1930,11 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
         }
         __syncwarp();
       }
-      if constexpr (MODE == MODE_FWD && kScore != SCORE_NONE) {
+      if constexpr ((MODE == MODE_FWD || MODE == MODE_FUSED_FWD) && kScore != SCORE_NONE) {
+        // (a slot for each column part)
         if (ok && row_ok)
-          p.score_part[static_cast<idx_t>(lr) * p.cols + t.split] = make_float4(run_m, run_s, run_ent, run_abs);
+          p.score_part[(static_cast<idx_t>(lr) * p.cols + t.split) * kColParts + (warp - 2) / 4] =
+              make_float4(run_m, run_s, run_ent, run_abs);
       } else if constexpr (MODE == MODE_FWD || MODE == MODE_FUSED_FWD) {
         if (ok && row_ok)
           p.partials[static_cast<idx_t>(t.split) * p.N + grow] = make_float2(run_m, run_s);
@@ -1899,7 +1957,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
   }
 
   if constexpr (MODE == MODE_DW || MODE == MODE_DH || MODE == MODE_DH2 || MODE == MODE_DHDW || MODE == MODE_DLOGITS ||
-                MODE == MODE_PIPE || (MODE == MODE_FUSED_FWD && kSp)) {
+                MODE == MODE_PIPE || (MODE == MODE_FUSED_FWD && (kSp || kScore != SCORE_NONE))) {
     if (warp >= 2 && lane == 0) bulk_wait_all();  // output boxes written before the CTA retires
   }
   __syncthreads();

@@ -254,21 +254,24 @@ cudaError_t launch_listed(int cg, bool kLong, const CUtensorMap& a, const CUtens
   return launch_listed<MODE>(cg, kLong, Maps{&a, &b, &c, &a, &b, &c, &a, &b, &c}, p, workers, st);
 }
 
-// A launch with the scores' epilogue: MODE_FWD, MODE_DLOGITS or MODE_PIPE.
+// A launch with the scores' epilogue: MODE_FWD, MODE_FUSED_FWD, MODE_DLOGITS or
+// MODE_PIPE.
+constexpr int kScoreParts = 2;  // column parts (partial slots) of the forwards' 8 epilogue warps
 template <int MODE, int kScore>
 cudaError_t launch_scored(int cg, bool kLong, const Maps& m, const GemmParams& p, int workers, cudaStream_t st) {
+  constexpr int EW = (MODE == MODE_PIPE ? 1 : kScoreParts) * EPI_WARPS;
   auto go = [&](auto kern, int smem, int grid_mult) -> cudaError_t {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_persistent(kern, grid_mult * grid_workers(workers), grid_mult, kernel_threads<MODE>(EPI_WARPS), smem,
-                             st, *m.a, *m.b, *m.c, *m.a2, *m.b2, *m.c2, *m.a3, *m.b3, *m.c3, p);
+    return launch_persistent(kern, grid_mult * grid_workers(workers), grid_mult, kernel_threads<MODE>(EW), smem, st,
+                             *m.a, *m.b, *m.c, *m.a2, *m.b2, *m.c2, *m.a3, *m.b3, *m.c3, p);
   };
-  constexpr int s2 = KernelCfg<MODE, 2, EPI_WARPS>::SMEM, s1 = KernelCfg<MODE, 1, EPI_WARPS>::SMEM;
+  constexpr int s2 = KernelCfg<MODE, 2, EW>::SMEM, s1 = KernelCfg<MODE, 1, EW>::SMEM;
   if (cg == 2)
-    return kLong ? go(flce_gemm_kernel<MODE, true, 2, false, EPI_WARPS, false, false, kScore>, s2, 2)
-                 : go(flce_gemm_kernel<MODE, false, 2, false, EPI_WARPS, false, false, kScore>, s2, 2);
-  return kLong ? go(flce_gemm_kernel<MODE, true, 1, false, EPI_WARPS, false, false, kScore>, s1, 1)
-               : go(flce_gemm_kernel<MODE, false, 1, false, EPI_WARPS, false, false, kScore>, s1, 1);
+    return kLong ? go(flce_gemm_kernel<MODE, true, 2, false, EW, false, false, kScore>, s2, 2)
+                 : go(flce_gemm_kernel<MODE, false, 2, false, EW, false, false, kScore>, s2, 2);
+  return kLong ? go(flce_gemm_kernel<MODE, true, 1, false, EW, false, false, kScore>, s1, 1)
+               : go(flce_gemm_kernel<MODE, false, 1, false, EW, false, false, kScore>, s1, 1);
 }
 template <int MODE, int kScore>
 cudaError_t launch_scored(int cg, bool kLong, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,

@@ -50,11 +50,17 @@ __device__ __forceinline__ ScorePart score_join(const ScorePart& a, const ScoreP
 }
 
 // A row's S partials joined by a warp, in a fixed order; the same in all lanes.
+// (Eight of a lane's are read at once: the joins wait on one another.)
 __device__ __forceinline__ ScorePart score_join_row(const float4* part, int S, int lane) {
   ScorePart a{-INFINITY, 0.f, 0.f, 0.f};
-  for (int s = lane; s < S; s += 32) {
-    const float4 q = part[s];
-    a = score_join(a, ScorePart{q.x, q.y, q.z, q.w});
+  for (int s0 = lane; s0 < S; s0 += 256) {
+    float4 q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      q[e] = s0 + 32 * e < S ? part[s0 + 32 * e] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (s0 + 32 * e < S) a = score_join(a, ScorePart{q[e].x, q[e].y, q[e].z, q[e].w});
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
@@ -153,24 +159,37 @@ __device__ __forceinline__ float2 two_add(float2 x, float2 y) {
 
 // sum_k h_k w_k of two bf16 rows by a warp, as a rounded value and what the
 // rounding leaves out: products of bf16 are exact in fp32, each step of the sum
-// hands its rounding error to a second sum.  The same in all lanes.
+// hands its rounding error to a second sum.  The same in all lanes.  1,024
+// elements are read at once: a word's row is somewhere else in memory each time.
 __device__ __forceinline__ float2 exact_dot(const uint16_t* __restrict__ h, const uint16_t* __restrict__ w, int H,
                                             int lane) {
   float2 hi = both(0.f), lo = both(0.f);
   const float2 minus = both(-1.f);
-#pragma unroll 2
-  for (int k = lane * 8; k < H; k += 256) {
-    Raw8<uint16_t> a, b;
-    a.q[0] = __ldg(reinterpret_cast<const uint4*>(h + k));
-    b.q[0] = __ldg(reinterpret_cast<const uint4*>(w + k));
+  for (int k0 = lane * 8; k0 < H; k0 += 1024) {
+    Raw8<uint16_t> a[4], b[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 p = mul2(a.pair(e), b.pair(e));
-      const float2 s = add2(hi, p);
-      const float2 y = fma2(hi, minus, s);                         // s - hi
-      const float2 x = fma2(y, minus, s);                          // s - y
-      lo = add2(lo, add2(fma2(x, minus, hi), fma2(y, minus, p)));  // (hi - x) + (p - y)
-      hi = s;
+    for (int g = 0; g < 4; ++g) {
+      const int k = k0 + 256 * g;
+      if (k < H) {
+        b[g].q[0] = __ldg(reinterpret_cast<const uint4*>(w + k));
+        a[g].q[0] = __ldg(reinterpret_cast<const uint4*>(h + k));
+      } else {
+        b[g].zero();
+        a[g].zero();
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (k0 - lane * 8 + 256 * g >= H) break;  // (the whole warp)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 p = mul2(a[g].pair(e), b[g].pair(e));
+        const float2 s = add2(hi, p);
+        const float2 y = fma2(hi, minus, s);                         // s - hi
+        const float2 x = fma2(y, minus, s);                          // s - y
+        lo = add2(lo, add2(fma2(x, minus, hi), fma2(y, minus, p)));  // (hi - x) + (p - y)
+        hi = s;
+      }
     }
   }
   float2 d = two_add(make_float2(hi.x, lo.x), make_float2(hi.y, lo.y));
@@ -206,9 +225,9 @@ struct SelectParams {
 };
 
 // The K likeliest words of a row on a CTA of T threads.
-//   1. Each thread takes the largest of its records (kDense: of its logits); the
-//      K-th largest of the threads' is a lower bound of the K-th largest logit,
-//      close to it (K words on T threads seldom share one).
+//   1. Each of 256 groups of threads takes the largest of its records (kDense: of
+//      its logits); the K-th largest of the groups' is a lower bound of the K-th
+//      largest logit, close to it (K words on 256 groups seldom share one).
 //   2. Candidates: the words that reach the bound, less what both can be off by.
 //      Of a chunk whose second largest reaches it too, all 32.
 //   3. Their logits again, a warp to a word, and a rank for each by counting.
@@ -216,6 +235,8 @@ struct SelectParams {
 // through it in runs, in index order, with the K best so far kept and the bound
 // raised to theirs.
 constexpr int SELECT_CAP = 1024;  // words of the list: more than SCORE_MAX_K and a chunk
+constexpr int SELECT_GROUPS = 256;
+static_assert(SELECT_GROUPS >= SCORE_MAX_K && SELECT_CAP >= SCORE_MAX_K + 32, "the list and the groups hold K");
 
 template <int T, bool kDense, bool kLong>
 __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__ SelectParams p) {
@@ -223,10 +244,10 @@ __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__
   using idx_t = typename std::conditional<kLong, long long, int>::type;
   __shared__ float2 val[SELECT_CAP];
   __shared__ int word[SELECT_CAP];
-  __shared__ __align__(16) float tops[T];
+  __shared__ __align__(16) float tops[SELECT_GROUPS];
   __shared__ int sums[T / 32];
   __shared__ int found;
-  __shared__ float bound;
+  __shared__ float bound, largest;
   __shared__ float2 target_z;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int K = p.out.k;
@@ -259,26 +280,30 @@ __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__
   float top = -INFINITY;
 #pragma unroll 4
   for (int c = t; c < units; c += T) top = fmaxf(top, unit(c).x);
-  tops[t] = top;
+#pragma unroll
+  for (int off = 1; off < T / SELECT_GROUPS; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (t % (T / SELECT_GROUPS) == 0) tops[t / (T / SELECT_GROUPS)] = top;
   if (t == 0) found = 0;
   const bool want_target = tgt >= 0 && tgt < p.V && p.out.logp != nullptr;
-  if (want_target && warp == T / 32 - 1) {
-    const float2 z = exact_dot(h, p.W + tgt * p.H, p.H, lane);
-    if (lane == 0) target_z = z;
+  __syncthreads();
+  if (t < SELECT_GROUPS) {
+    const float mine = tops[t];
+    int rank = 0;
+    float most = -INFINITY;
+    for (int q = 0; q < SELECT_GROUPS; q += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(tops + q);
+      rank += (o.x > mine || (o.x == mine && q < t)) + (o.y > mine || (o.y == mine && q + 1 < t)) +
+              (o.z > mine || (o.z == mine && q + 2 < t)) + (o.w > mine || (o.w == mine && q + 3 < t));
+      most = fmaxf(fmaxf(most, fmaxf(o.x, o.y)), fmaxf(o.z, o.w));
+    }
+    if (rank == K - 1) {
+      bound = mine;
+      largest = most;
+    }
   }
   __syncthreads();
-  int rank = 0;
-  float most = -INFINITY;
-  for (int q = 0; q < T; q += 4) {
-    const float4 o = *reinterpret_cast<const float4*>(tops + q);
-    rank += (o.x > top || (o.x == top && q < t)) + (o.y > top || (o.y == top && q + 1 < t)) +
-            (o.z > top || (o.z == top && q + 2 < t)) + (o.w > top || (o.w == top && q + 3 < t));
-    most = fmaxf(fmaxf(most, fmaxf(o.x, o.y)), fmaxf(o.z, o.w));
-  }
-  if (rank == K - 1) bound = top;
-  __syncthreads();
-  // (K threads with a record: K chunks; else every word is a candidate)
-  const float low = bound;
+  // (K groups with a record: K chunks; else every word is a candidate)
+  const float low = bound, most = largest;
   const float size = fmaxf(whole.top < INFINITY ? whole.top : 0.f, fmaxf(fabsf(most), low > -INFINITY ? fabsf(low) : 0.f));
   const float off = p.slack * size + 1e-43f;
   float reach = low - 2.f * off;
@@ -296,11 +321,14 @@ __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__
       word[at] = 32 * c + 31 - static_cast<int>(__float_as_uint(q.x) & 31u);
     }
   };
-  // the logits of the words [from, total), then the best K of all in order at the list's front
+  // the logits of the words [from, total) (and, the first time, of the target),
+  // then the best K of all in order at the list's front
   auto settle = [&](int from, int total) {
-    for (int e = from + warp; e < total; e += T / 32) {
-      const float2 z = exact_dot(h, p.W + static_cast<long long>(word[e]) * p.H, p.H, lane);
-      if (lane == 0) val[e] = z;
+    const int extra = from == 0 && want_target ? 1 : 0;
+    for (int e = from + warp; e < total + extra; e += T / 32) {
+      const long long v = e < total ? word[e] : tgt;
+      const float2 z = exact_dot(h, p.W + v * p.H, p.H, lane);
+      if (lane == 0) (e < total ? val[e] : target_z) = z;
     }
     __syncthreads();
     constexpr int PER = (SELECT_CAP + T - 1) / T;
@@ -387,6 +415,115 @@ __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__
     if (p.out.lse) p.out.lse[i] = r.x;
     if (p.out.entropy) p.out.entropy[i] = r.y;
     if (p.out.logp && !want_target) p.out.logp[i] = __int_as_float(0x7fc00000);
+  }
+}
+
+// dlogits of the scores from the forward's kept logits: with x = log2 p_v = E_v +
+// mx - lse log2 e (E: fp16, relative to its chunk's maximum mx),
+//   D_v = -p_v (ga + ge (x ln 2 + entropy)) f'(z) + [v = t] ga f'(z)
+// The target's column is formed from its own fp32 logit zt: 1 - p_t is small where
+// the target is likely, and E's p_t would not do.  Rows and columns as
+// topk_dlogits_kernel: row r of E is row ri[r] (r without ri); a CTA takes
+// `steps` runs of TOPK_DL_COLS columns, a lane 8 neighbouring ones at a time.
+// kLo: D in two bf16 parts, what the first one's rounding leaves out lo rows
+// further on; the rows from `rows` to lo are zeroed.  Bound by memory.
+struct ScoreDlogits {
+  const uint16_t* E;  // [rows][ldD]
+  const float* mx;    // [rows][ld_mx]
+  uint16_t* D;        // [rows][ldD]
+  int ldD, ld_mx, steps, rows, lo, V;
+  const int* ri;
+  const int* count;
+  const int64_t* targets;
+  long long ignore;
+  const float* zt;
+  const float* lse;
+  const float* entropy;
+  const float* g_logp;
+  const float* g_entropy;
+  int tf_softcap;
+  float tf_a, tf_b, tf_d;
+};
+
+template <bool kLong, bool kLo>
+__global__ void __launch_bounds__(SMALL_THREADS) score_dlogits_kernel(const __grid_constant__ ScoreDlogits p) {
+  dependent_start();
+  using idx_t = typename std::conditional<kLong, long long, int>::type;
+  const int r = blockIdx.y;
+  const int n = p.ri != nullptr ? *p.count : p.rows;
+  if (p.ri != nullptr && r >= (n + 63) / 64 * 64) return;
+  const bool inside = r < n;
+  const long long i = !inside ? 0 : p.ri ? p.ri[r] : r;
+  const long long tgt = inside ? p.targets[i] : p.ignore;
+  const float ga = inside && p.g_logp != nullptr ? p.g_logp[i] : 0.f;
+  const float ge = inside && p.g_entropy != nullptr ? p.g_entropy[i] : 0.f;
+  const bool live = inside && tgt != p.ignore && (ga != 0.f || ge != 0.f);
+  uint16_t* row = p.D + static_cast<idx_t>(r) * p.ldD;
+  uint16_t* row2 = row + static_cast<idx_t>(p.lo) * p.ldD;
+  const int c0 = blockIdx.x * p.steps * TOPK_DL_COLS;
+  const int c1 = min(p.ldD, c0 + p.steps * TOPK_DL_COLS);
+  if (!live) {
+    for (int c = c0 + threadIdx.x * 8; c < c1; c += SMALL_THREADS * 8) {
+      *reinterpret_cast<uint4*>(row + c) = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (kLo) *reinterpret_cast<uint4*>(row2 + c) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    return;
+  }
+  const float lse = p.lse[i], ent = p.entropy[i];
+  const float nlse2 = -lse * kLog2e, a = -ge * kLn2, b = -fmaf(ge, ent, ga);
+  const uint16_t* src = p.E + static_cast<idx_t>(r) * p.ldD;
+  const float* rmx = p.mx + static_cast<idx_t>(r) * p.ld_mx;
+  const int first = c0 + (threadIdx.x >> 5) * 1024 + (threadIdx.x & 31) * 8;
+  for (int cs = first; cs < c1; cs += TOPK_DL_COLS) {
+    uint4 q[4];
+    float cm[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = cs + k * 256;
+      if (c < c1) {
+        q[k] = *reinterpret_cast<const uint4*>(src + c);
+        cm[k] = rmx[c / 32];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = cs + k * 256;
+      if (c >= c1) continue;
+      uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+      uint32_t w2[4];
+      const float2 shift = both(cm[k] + nlse2);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = add2(__half22float2(*reinterpret_cast<const __half2*>(&w[e])), shift);
+        const float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        // (p log p is 0 where p is)
+        const float2 f = fma2(make_float2(fmaxf(x.x, -1000.f), fmaxf(x.y, -1000.f)), both(a), both(b));
+        float2 dv = mul2(pr, f);
+        if (p.tf_softcap) {  // f' = d (1 - tanh^2), tanh = u / b
+          const float k2 = kLn2 / p.tf_b;
+          const float2 th = make_float2(fmaf(x.x, k2, lse / p.tf_b), fmaf(x.y, k2, lse / p.tf_b));
+          dv = mul2(dv, make_float2(p.tf_d * fmaxf(0.f, 1.f - th.x * th.x), p.tf_d * fmaxf(0.f, 1.f - th.y * th.y)));
+        } else {
+          dv = mul2(dv, both(p.tf_a));
+        }
+        w[e] = pack_bf16x2(dv.x, dv.y);
+        if constexpr (kLo) w2[e] = bf16x2_rest(dv.x, dv.y, w[e]);
+      }
+      *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      if constexpr (kLo) *reinterpret_cast<uint4*>(row2 + c) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+    }
+  }
+  if (tgt < c0 || tgt >= c1 || tgt >= p.V) return;  // (the whole CTA; c0 >= 0)
+  __syncthreads();  // the target's column after the CTA's own stores
+  if (threadIdx.x == 0) {
+    const float u = p.zt[i], lp = u - lse;
+    const float slope = p.tf_softcap ? p.tf_d * fmaxf(0.f, 1.f - (u / p.tf_b) * (u / p.tf_b)) : p.tf_a;
+    const float pt = expf(lp);
+    // (1 - p_t straight from log p_t)
+    const float dv = (-ga * expm1f(lp) - ge * pt * (fmaxf(lp, -1000.f) + ent)) * slope;
+    const uint32_t w = pack_bf16x2(dv, 0.f);
+    row[tgt] = static_cast<uint16_t>(w & 0xffffu);
+    if constexpr (kLo) row2[tgt] = static_cast<uint16_t>(bf16x2_rest(dv, 0.f, w) & 0xffffu);
   }
 }
 

@@ -13,26 +13,73 @@ bool score_dense(int64_t V, int64_t k) { return ceil_div(V, 32) < 8 * k; }
 
 constexpr size_t kScoreBlockBytes = size_t(256) << 20;  // of records or logits held at once
 
+// Logits kept from the forward for the backward (flce_score's state): of one row
+// block, and at most 32,768 rows (the dlogits pass puts one row per grid row).
+// More than a tile of rows are compacted to the counted ones, as in
+// flce_forward_backward; both calls decide it alike, by the row count alone.
+constexpr int64_t kKeepMaxRows = 32768;
+constexpr int64_t kKeepCompactRows = 2 * BM;
+
+struct KeepLayout {
+  size_t E = 0, mx = 0, zt = 0, idx = 0, count = 0, total = 0;
+  long long ldD = 0, ld_mx = 0;
+};
+KeepLayout keep_layout(int64_t N, int64_t V) {
+  KeepLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  L.ldD = round_up(V, 32);
+  L.ld_mx = fused_ld_mx(V);
+  L.E = take(static_cast<size_t>(N) * L.ldD * 2);
+  L.mx = take(static_cast<size_t>(N) * L.ld_mx * 4);
+  L.zt = take(static_cast<size_t>(N) * 4);
+  if (N > kKeepCompactRows) {
+    L.idx = take(static_cast<size_t>(N) * 4);
+    L.count = take(256);
+  }
+  L.total = o;
+  return L;
+}
+
+// At short rows of h the product costs no more than reading what was kept; but at
+// most 128 rows are kept at any size, since only their dlogits from kept logits
+// take two bf16 parts (fused_lo_rows), and one entry often holds most of so few
+// rows' gradients.
+constexpr int64_t kKeepMinHidden = 512;
+
+// Whether a call of these sizes keeps its logits: they fit the caller's dlogits
+// budget (chunk_rows x V), and reading them costs less than their product again.
+bool keep_pays(int64_t N, int64_t H, int64_t chunk_rows) {
+  return N > 0 && N <= kKeepMaxRows && N <= round_up(std::max<int64_t>(1, chunk_rows), BM) &&
+         (H >= kKeepMinHidden || N <= BM);
+}
+
 struct ScorePlan {
-  bool gemv = false, dense = false;
+  bool gemv = false, dense = false, keep = false;
   long long rows = 0;  // of a launch
   int S = 1;           // partials of a row
   long long ld = 0;    // row pitch of the records (float2) or logits (fp32)
   FwdPlan f;
 };
-ScorePlan score_plan(int64_t N, int64_t H, int64_t V, int64_t k, int workers, int tm) {
+ScorePlan score_plan(int64_t N, int64_t H, int64_t V, int64_t k, bool keep, int workers, int tm) {
   ScorePlan q;
-  q.gemv = topk_gemv_for(N, H);
+  q.keep = keep;
+  q.gemv = !keep && topk_gemv_for(N, H);
   q.dense = k > 0 && score_dense(V, k);
   // both cover whole tiles
   q.ld = k == 0 ? 0 : q.dense ? round_up(V, BN) : round_up(V, BN) / 32;
-  q.rows = fwd_block_rows(N, tm);
+  q.rows = keep ? std::max<int64_t>(N, 1) : fwd_block_rows(N, tm);
   if (k > 0 && !q.gemv) {
     const long long fit = static_cast<long long>(kScoreBlockBytes / (static_cast<size_t>(q.ld) * (q.dense ? 4 : 8)));
     q.rows = std::min(q.rows, std::max<long long>(tm, fit / tm * tm));
   }
-  q.f = plan_forward(q.rows, H, V, workers, tm);
-  q.S = q.gemv ? topk_gemv_ctas(V) : q.f.S;
+  // (a row has kScoreParts partials of 16 bytes to a split: four times the 8 that the cap counts)
+  q.f = plan_forward(q.rows, H, V, workers, tm, kFwdPartialsCap / 4);
+  q.S = q.gemv ? topk_gemv_ctas(V) : kScoreParts * q.f.S;
   return q;
 }
 
@@ -53,7 +100,7 @@ ScoreLayout score_layout(int64_t N, int64_t H, int64_t V, int64_t k, const Score
   L.z = take(k > 0 && (q.dense || q.gemv) ? rows * round_up(V, BN) * 4 : 0);
   L.rec = take(k > 0 && !q.dense ? rows * q.ld * 8 : 0);
   L.bad = take(256);
-  if (!q.gemv && N >= skip_min_rows()) {
+  if (q.keep ? N > kKeepCompactRows : !q.gemv && N >= skip_min_rows()) {
     L.idx = take(n * 4);
     L.blk = take(static_cast<size_t>(ceil_div(N, COMPACT_ROWS_PER_BLOCK)) * 4);
     L.count = take(256);
@@ -106,11 +153,14 @@ flce_status score_rows(const ScorePlan& q, bool kLong, const ScoreRows& rows, co
   auto go = [&](auto kern, int threads) {
     return launch_dependent(kern, dim3(static_cast<unsigned>(rows.rows)), threads, 0, st, p);
   };
-  if (q.dense)
-    FLCE_CUDA_TRY((kLong ? go(score_select_kernel<256, true, true>, 256) : go(score_select_kernel<256, true, false>, 256)));
-  else
-    FLCE_CUDA_TRY((kLong ? go(score_select_kernel<256, false, true>, 256)
-                         : go(score_select_kernel<256, false, false>, 256)));
+  // with a row to an SM, or fewer, a row's latency counts: more warps to its words
+  const bool few = rows.rows <= device_sms();
+  auto of = [&](auto dense) -> cudaError_t {
+    constexpr bool D = decltype(dense)::value;
+    if (kLong) return go(score_select_kernel<256, D, true>, 256);
+    return few ? go(score_select_kernel<1024, D, false>, 1024) : go(score_select_kernel<256, D, false>, 256);
+  };
+  FLCE_CUDA_TRY(q.dense ? of(std::true_type{}) : of(std::false_type{}));
   return FLCE_OK;
 }
 
@@ -147,13 +197,22 @@ extern "C" {
 size_t flce_score_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k) {
   if (!topk_sizes_ok(N, H, V) || k < 0 || k > SCORE_MAX_K || k > V) return 0;
   const int cg = cta_group();
-  return score_layout(N, H, V, k, score_plan(N, H, V, k, device_workers(cg), BM * cg)).total;
+  const int workers = device_workers(cg);
+  auto of = [&](bool keep) {
+    return score_layout(N, H, V, k, score_plan(N, H, V, k, keep, workers, BM * cg)).total;
+  };
+  return k == 0 && N <= kKeepMaxRows ? std::max(of(false), of(true)) : of(false);
+}
+
+size_t flce_score_state_bytes(int64_t N, int64_t H, int64_t V, int64_t chunk_rows) {
+  if (!topk_sizes_ok(N, H, V) || !keep_pays(N, H, chunk_rows)) return 0;
+  return keep_layout(N, V).total;
 }
 
 flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* targets, int64_t N, int64_t H, int64_t V,
                        int64_t k, int64_t ignore_index, const flce_logit_transform* transform, float* out_logp,
-                       float* out_lse, float* out_entropy, int64_t* out_ids, float* out_logprobs, void* workspace,
-                       size_t workspace_bytes, void* stream) {
+                       float* out_lse, float* out_entropy, int64_t* out_ids, float* out_logprobs, void* state,
+                       void* workspace, size_t workspace_bytes, void* stream) {
   if (!topk_sizes_ok(N, H, V) || k < 0 || k > V) return FLCE_ERR_INVALID_ARG;
   GemmParams tfp{};
   if (!transform_params(transform, tfp)) return FLCE_ERR_INVALID_ARG;
@@ -161,7 +220,8 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
   if (N > 0 && !out_logp && !out_lse && !out_entropy && !out_ids && !out_logprobs) return FLCE_ERR_INVALID_ARG;
   if (N > 0 && ((out_logp && !targets) || ((out_ids || out_logprobs) != (k > 0)))) return FLCE_ERR_INVALID_ARG;
   if (N > 0 && (!h || !W)) return FLCE_ERR_INVALID_ARG;
-  if (k > SCORE_MAX_K || H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
+  if (state && N > 0 && (k != 0 || !targets)) return FLCE_ERR_INVALID_ARG;
+  if (k > SCORE_MAX_K || H % 8 != 0 || (state && N > kKeepMaxRows) || !aligned(state, 256)) return FLCE_ERR_UNSUPPORTED;
   if (!aligned(h, 16) || !aligned(W, 16) || !aligned(targets, 8) || !aligned(out_logp, 4) || !aligned(out_lse, 4) ||
       !aligned(out_entropy, 4) || !aligned(out_ids, 8) || !aligned(out_logprobs, 4))
     return FLCE_ERR_UNSUPPORTED;
@@ -169,13 +229,16 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int cg = cta_group(), tm = BM * cg;
   const int workers = device_workers(cg);
-  const ScorePlan q = score_plan(N, H, V, k, workers, tm);
+  const bool keep = state != nullptr;
+  const ScorePlan q = score_plan(N, H, V, k, keep, workers, tm);
   const ScoreLayout L = score_layout(N, H, V, k, q);
+  const KeepLayout K = keep_layout(N, V);
+  uint8_t* kb = static_cast<uint8_t*>(state);
   Workspace ws;
   flce_status s = get_workspace(ws, workspace, workspace_bytes, L.total, st);
   if (s != FLCE_OK) return s;
   uint8_t* wb = static_cast<uint8_t*>(ws.ptr);
-  float* zt = k == 0 ? reinterpret_cast<float*>(wb + L.zt) : nullptr;
+  float* zt = keep ? reinterpret_cast<float*>(kb + K.zt) : k == 0 ? reinterpret_cast<float*>(wb + L.zt) : nullptr;
   float4* part = reinterpret_cast<float4*>(wb + L.part);
   float* z = k > 0 && (q.dense || q.gemv) ? reinterpret_cast<float*>(wb + L.z) : nullptr;
   float2* rec = k > 0 && !q.dense ? reinterpret_cast<float2*>(wb + L.rec) : nullptr;
@@ -192,7 +255,7 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
     if (nbad != 0) return FLCE_ERR_BAD_TARGET;
   }
   const ScoreOut out{out_logp, out_lse, out_entropy, out_ids, out_logprobs, static_cast<int>(k)};
-  const bool kLong = q.rows * std::max<long long>(q.ld, q.S) >= INT_MAX;
+  const bool kLong = q.rows * std::max<long long>({q.ld, q.S, keep ? K.ldD : 0}) >= INT_MAX;
   GemmParams p{};
   p.n_tiles = q.f.n_tiles;
   p.k_blocks = q.f.k_blocks;
@@ -221,9 +284,9 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
                       out, st);
   }
   // the rows without a target to score are left out, as flce_forward_ex2 does
-  const bool skip = targets != nullptr && compact_on() && L.hc != 0;
-  int* idx = reinterpret_cast<int*>(wb + L.idx);
-  int* count = reinterpret_cast<int*>(wb + L.count);
+  const bool skip = targets != nullptr && (keep || compact_on()) && L.hc != 0;
+  int* idx = reinterpret_cast<int*>(keep ? kb + K.idx : wb + L.idx);
+  int* count = reinterpret_cast<int*>(keep ? kb + K.count : wb + L.count);
   uint16_t* hc = reinterpret_cast<uint16_t*>(wb + L.hc);
   if (skip) {
     s = list_valid_rows(targets, Ni, ignore_index, reinterpret_cast<int*>(wb + L.blk), idx, count, false, st);
@@ -236,6 +299,13 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
   CUtensorMap tA, tB;
   if (!make_map(&tA, skip ? hc : h, H, skip ? q.rows : N, H, BK, BM) || !make_map(&tB, W, H, V, H, BK, BN / cg))
     return FLCE_ERR_CUDA;
+  CUtensorMap tE;  // the kept logits
+  if (keep) {
+    if (!make_map(&tE, kb + K.E, K.ldD, N, K.ldD, 64, 32)) return FLCE_ERR_CUDA;
+    p.mx = reinterpret_cast<float*>(kb + K.mx);
+    p.ldD = static_cast<int>(K.ldD);
+    p.ld_mx = static_cast<int>(K.ld_mx);
+  }
   int* err = nullptr;
   FLCE_CUDA_TRY(cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_device_error));
   p.err = err;
@@ -261,8 +331,9 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
     {
       ProfScope ps(K_FWD, st);
       const int w = std::min(g.num_units, workers);
-      FLCE_CUDA_TRY(k > 0 ? (launch_scored<MODE_FWD, SCORE_TOP>(cg, kLong, tA, tB, tB, g, w, st))
-                          : (launch_scored<MODE_FWD, SCORE_ENTROPY>(cg, kLong, tA, tB, tB, g, w, st)));
+      FLCE_CUDA_TRY(keep    ? (launch_scored<MODE_FUSED_FWD, SCORE_ENTROPY>(cg, kLong, tA, tB, tE, g, w, st))
+                    : k > 0 ? (launch_scored<MODE_FWD, SCORE_TOP>(cg, kLong, tA, tB, tB, g, w, st))
+                            : (launch_scored<MODE_FWD, SCORE_ENTROPY>(cg, kLong, tA, tB, tB, g, w, st)));
     }
     s = score_rows(q, kLong, rows, part, rec, z, h, W, p, targets, ignore_index, zt, out, st);
     if (s != FLCE_OK) return s;
@@ -270,29 +341,174 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
   return FLCE_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// The backward from kept logits: the second half of flce_forward_backward's step
+// over one row block.  D may take two bf16 parts (fused_lo_rows).
+struct KeepBwdPlan {
+  FusedPlan fp;
+  size_t D = 0, dh_part = 0, hc = 0, total = 0;
+};
+KeepBwdPlan keep_bwd_plan(int64_t N, int64_t H, int64_t V, int workers, int tm) {
+  KeepBwdPlan k;
+  k.fp = plan_fused(N, H, V, std::max<long long>(2 * BM, round_up(N, BM)), workers, tm, OneCall::kListed);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  const size_t d_rows = static_cast<size_t>(k.fp.lo > 0 ? 2 * k.fp.lo : N);
+  k.D = take(d_rows * k.fp.ldD * 2);
+  k.dh_part = take(k.fp.b.dh_f32 ? static_cast<size_t>(k.fp.b.dh_splits) * k.fp.R * H * 4 : 0);
+  k.hc = take(N > kKeepCompactRows ? static_cast<size_t>(N) * H * 2 : 0);
+  k.total = o;
+  return k;
+}
+
+flce_status score_backward_kept(const flce_bf16* h, const flce_bf16* W, const int64_t* targets, const float* lse,
+                                const ScoreGrads& sc, uint8_t* state, flce_bf16* dH, float* dW, int64_t N, int64_t H,
+                                int64_t V, int64_t ignore_index, const GemmParams& tfp, uint8_t* wb, cudaStream_t st) {
+  const int cg = cta_group(), tm = BM * cg, workers = device_workers(cg);
+  const KeepLayout K = keep_layout(N, V);
+  const KeepBwdPlan kp = keep_bwd_plan(N, H, V, workers, tm);
+  const FusedPlan& fp = kp.fp;
+  const int Ni = static_cast<int>(N);
+  const bool compact = N > kKeepCompactRows;
+  uint16_t* D = reinterpret_cast<uint16_t*>(wb + kp.D);
+  uint16_t* hc = reinterpret_cast<uint16_t*>(wb + kp.hc);
+  float* dh_part = fp.b.dh_f32 ? reinterpret_cast<float*>(wb + kp.dh_part) : nullptr;
+  const int* idx = compact ? reinterpret_cast<const int*>(state + K.idx) : nullptr;
+  const int* count = compact ? reinterpret_cast<const int*>(state + K.count) : nullptr;
+  const bool kLong = std::max<long long>(N, 2 * fp.lo) * fp.ldD >= INT_MAX || N * H >= INT_MAX || V * H >= INT_MAX ||
+                     static_cast<long long>(fp.b.dh_splits) * fp.R * H >= INT_MAX;
+  if (compact && dH) FLCE_CUDA_TRY(cudaMemsetAsync(dH, 0, static_cast<size_t>(N) * H * 2, st));
+  if (compact) {
+    const flce_status sg = gather_rows(h, H, idx, count, Ni, 0, N, hc, st);
+    if (sg != FLCE_OK) return sg;
+  }
+  {
+    ProfScope ps(K_DLOGITS, st);
+    const long long runs = ceil_div(fp.ldD, TOPK_DL_COLS);
+    const int steps = static_cast<int>(std::max<long long>(1, std::min<long long>(4, runs * N / (16LL * device_sms()))));
+    ScoreDlogits d{};
+    d.E = reinterpret_cast<const uint16_t*>(state + K.E);
+    d.mx = reinterpret_cast<const float*>(state + K.mx);
+    d.D = D;
+    d.ldD = static_cast<int>(fp.ldD);
+    d.ld_mx = static_cast<int>(K.ld_mx);
+    d.steps = steps;
+    d.rows = Ni;
+    d.lo = static_cast<int>(fp.lo);
+    d.V = static_cast<int>(V);
+    d.ri = idx;
+    d.count = count;
+    d.targets = targets;
+    d.ignore = ignore_index;
+    d.zt = reinterpret_cast<const float*>(state + K.zt);
+    d.lse = lse;
+    d.entropy = sc.entropy;
+    d.g_logp = sc.g_logp;
+    d.g_entropy = sc.g_entropy;
+    d.tf_softcap = tfp.tf_softcap;
+    d.tf_a = tfp.tf_a;
+    d.tf_b = tfp.tf_b;
+    d.tf_d = tfp.tf_d;
+    const dim3 grid(static_cast<unsigned>(ceil_div(runs, steps)), static_cast<unsigned>(std::max<long long>(N, fp.lo)));
+    auto go = [&](auto kern) { return launch_dependent(kern, grid, SMALL_THREADS, 0, st, d); };
+    if (fp.lo > 0)
+      FLCE_CUDA_TRY((kLong ? go(score_dlogits_kernel<true, true>) : go(score_dlogits_kernel<false, true>)));
+    else
+      FLCE_CUDA_TRY((kLong ? go(score_dlogits_kernel<true, false>) : go(score_dlogits_kernel<false, false>)));
+  }
+  int* err = nullptr;
+  FLCE_CUDA_TRY(cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_device_error));
+  const int d_rows = fp.lo > 0 ? static_cast<int>(2 * fp.lo) : Ni;
+  CUtensorMap W_mn, B_dw, dW_map, dhp_map, D_k, D_mn;
+  if (!make_map(&W_mn, W, H, V, H, 64, BK) || !make_map(&B_dw, compact ? hc : h, H, N, H, 64, BK) ||
+      !make_map(&D_k, D, fp.ldD, d_rows, fp.ldD, BK, BM) || !make_map(&D_mn, D, fp.ldD, d_rows, fp.ldD, 64, BK))
+    return FLCE_ERR_CUDA;
+  if (dW && !make_map_t(&dW_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dW, H, V, H, 32, 32)) return FLCE_ERR_CUDA;
+  if (sc.dW16 && !make_map(&dW_map, sc.dW16, H, V, H, 64, 32)) return FLCE_ERR_CUDA;
+  if (dH && fp.b.dh_f32 &&
+      !make_map_t(&dhp_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dh_part, H, fp.b.dh_splits * fp.R, H, 32, 32))
+    return FLCE_ERR_CUDA;
+  GemmParams p{};
+  p.N = Ni;
+  p.H = static_cast<int>(H);
+  p.V = static_cast<int>(V);
+  p.ldD = static_cast<int>(fp.ldD);
+  p.D = D;
+  p.dH = dH;
+  p.dH_part = dh_part;
+  p.dW = dW;
+  p.err = err;
+  p.rows = d_rows;
+  p.rows_cap = static_cast<int>(fp.R);
+  p.row_idx = idx;
+  p.dyn_count = count;
+  // (dlogits in two parts: both parts' rows, against the rows of h twice; the
+  // parts of a dH row are sums of its reduction like the k-splits')
+  p.dw_h_blocks = static_cast<int>(fp.lo / BK);
+  BwdPlan reduce = fp.b;
+  if (fp.lo > 0) {
+    reduce.dh_splits *= 2;
+    reduce.R = fp.lo;
+  }
+  const DhDwStage stage{cg, workers, tm, kLong, &fp.b, H, V, dh_part, dH, dW, &W_mn, &dW_map, &dhp_map,
+                        sc.dW16 != nullptr};
+  DhDwStage finish = stage;
+  finish.plan = &reduce;
+  const flce_status s = slab_dh_dw(stage, p, d_rows, 0, 0, 0, static_cast<int>(V), D_k, D_mn, B_dw, st);
+  if (s != FLCE_OK) return s;
+  return block_dh_finish(finish, 0, Ni, idx, count, 0, st);
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t flce_score_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t chunk_rows, int32_t dW_type) {
-  return flce_topk_kd_backward_workspace_bytes(N, H, V, chunk_rows, dW_type);
+  const size_t again = flce_topk_kd_backward_workspace_bytes(N, H, V, chunk_rows, dW_type);
+  if (again == 0 || !keep_pays(N, H, chunk_rows)) return again;
+  const int cg = cta_group();
+  return std::max(again, keep_bwd_plan(N, H, V, device_workers(cg), BM * cg).total);
 }
 
 flce_status flce_score_backward(const flce_bf16* h, const flce_bf16* W, const int64_t* targets, const float* lse,
-                                const float* entropy, const float* g_logp, const float* g_entropy, flce_bf16* dH,
-                                void* dW, int32_t dW_type, int64_t N, int64_t H, int64_t V, int64_t chunk_rows,
-                                int64_t ignore_index, const flce_logit_transform* transform, void* workspace,
-                                size_t workspace_bytes, void* stream) {
+                                const float* entropy, const float* g_logp, const float* g_entropy, const void* state,
+                                flce_bf16* dH, void* dW, int32_t dW_type, int64_t N, int64_t H, int64_t V,
+                                int64_t chunk_rows, int64_t ignore_index, const flce_logit_transform* transform,
+                                void* workspace, size_t workspace_bytes, void* stream) {
   if (!topk_sizes_ok(N, H, V) || !topk_dw_ok(dW, dW_type)) return FLCE_ERR_INVALID_ARG;
   GemmParams tfp{};
   if (!transform_params(transform, tfp) || (N > 0 && !dH && !dW)) return FLCE_ERR_INVALID_ARG;
   if (N > 0 && (!h || !W || !targets || !lse || !entropy)) return FLCE_ERR_INVALID_ARG;
   if (H % 8 != 0 || !aligned(dW, 16) || !aligned(dH, 16) || !aligned(h, 16) || !aligned(W, 16) ||
-      !aligned(targets, 8) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4))
+      !aligned(targets, 8) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) ||
+      !aligned(g_entropy, 4) || !aligned(state, 256) || (state && N > kKeepMaxRows))
     return FLCE_ERR_UNSUPPORTED;
   if (N == 0 && !dW) return FLCE_OK;
-  const bool bf16 = dW != nullptr && dW_type == FLCE_BF16;
-  const TopkGrad tg = topk_grad(dW ? dW_type : FLCE_F32, N, H, V, bf16 ? topk_bwd_rows(N, H, V, chunk_rows) : 0);
-  ScoreGrads sc{entropy, g_logp, g_entropy, bf16 && !tg.scratch ? static_cast<flce_bf16*>(dW) : nullptr};
-  const size_t inner = align256(flce_workspace_bytes(N, H, V, chunk_rows));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dW != nullptr && dW_type == FLCE_BF16;
+  ScoreGrads sc{entropy, g_logp, g_entropy, nullptr};
   Workspace ws;
+  if (state && N > 0) {
+    const int cg = cta_group();
+    flce_status s = get_workspace(ws, workspace, workspace_bytes,
+                                  keep_bwd_plan(N, H, V, device_workers(cg), BM * cg).total, st);
+    if (s != FLCE_OK) return s;
+    if (bf16) sc.dW16 = static_cast<flce_bf16*>(dW);
+    // (the state is read alone)
+    return score_backward_kept(h, W, targets, lse, sc, static_cast<uint8_t*>(const_cast<void*>(state)), dH,
+                               bf16 ? nullptr : static_cast<float*>(dW), N, H, V, ignore_index, tfp,
+                               static_cast<uint8_t*>(ws.ptr), st);
+  }
+  const TopkGrad tg = topk_grad(dW ? dW_type : FLCE_F32, N, H, V, bf16 ? topk_bwd_rows(N, H, V, chunk_rows) : 0);
+  if (bf16 && !tg.scratch) sc.dW16 = static_cast<flce_bf16*>(dW);
+  const size_t inner = align256(flce_workspace_bytes(N, H, V, chunk_rows));
   flce_status s = get_workspace(ws, workspace, workspace_bytes, inner + tg.bytes, st);
   if (s != FLCE_OK) return s;
   float* sum = tg.scratch ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws.ptr) + inner)

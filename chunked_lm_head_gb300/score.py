@@ -41,38 +41,47 @@ def _row_vector(x, h, name):
 
 
 def score_forward(h, W, targets=None, k: int = 0, ignore_index: int = IGNORE_INDEX, transform=None,
-                  workspace: torch.Tensor | None = None, stream=None):
+                  workspace: torch.Tensor | None = None, stream=None, keep_rows: int = 0):
     """dict(logp[N] or None, lse[N], entropy[N] f32, ids[N,k] i64 or None,
-    logprobs[N,k] f32 or None) on device.
+    logprobs[N,k] f32 or None, state) on device.
 
     logp: log-probability of each row's target (None without targets).  k > 0
     (at most 128 and V): the k words of largest logit in descending order, ties
     to the lowest index, and their log-probabilities; the order is that of the
     exact sums h W^T.  A row whose target is ignore_index is skipped: zeros, and
     ids of -1.  A row with a logit that is NaN or +infinity: NaN, ids of -1.
-    transform: as in forward()."""
+    transform: as in forward().
+
+    keep_rows > 0 (with targets, k = 0): where N fits into as many rows, and it
+    pays, state holds the logits in 16 bits (N V 2 bytes) for score_backward,
+    which then needs no product again (else None)."""
     _check(h, W, targets)
     (N, H), V, dev = h.shape, W.shape[0], h.device
     if not 0 <= k <= V:
         raise ValueError("k must be between 0 and the vocabulary")
+    if keep_rows and (k or targets is None):
+        raise ValueError("keep_rows goes with targets and without words")
     with _on(h):
         lse = torch.empty(N, dtype=torch.float32, device=dev)
         entropy = torch.empty_like(lse)
         logp = None if targets is None else torch.empty_like(lse)
         ids = torch.empty((N, k), dtype=torch.int64, device=dev) if k else None
         words = torch.empty((N, k), dtype=torch.float32, device=dev) if k else None
+        nbytes = _lib.flce_score_state_bytes(N, H, V, keep_rows) if keep_rows else 0
+        state = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         ws, ws_bytes = _workspace(workspace, _lib.flce_score_workspace_bytes(N, H, V, k), stream, dev)
         _lib.check("flce_score", _lib.flce_score(h, W, targets, N, H, V, k, ignore_index, transform, logp, lse, entropy,
-                                                 ids, words, ws, ws_bytes, stream))
-    return {"logp": logp, "lse": lse, "entropy": entropy, "ids": ids, "logprobs": words}
+                                                 ids, words, state, ws, ws_bytes, stream))
+    return {"logp": logp, "lse": lse, "entropy": entropy, "ids": ids, "logprobs": words, "state": state}
 
 
 def score_backward(h, W, targets, lse, entropy, grad_logp=None, grad_entropy=None, chunk_rows: int = 256,
                    ignore_index: int = IGNORE_INDEX, transform=None, need_dH: bool = True, need_dW: bool = True,
-                   workspace: torch.Tensor | None = None, stream=None, dW_dtype=torch.float32):
+                   workspace: torch.Tensor | None = None, stream=None, dW_dtype=torch.float32, state=None):
     """(dH[N,H] bf16 or None, dW[V,H] of dW_dtype (float32 or bfloat16) or None)
     of sum_i grad_logp[i] logp[i] + grad_entropy[i] entropy[i] (either may be
-    None: zero), from the forward's lse and entropy."""
+    None: zero), from the forward's lse and entropy, and its state (of the same
+    h, W, targets, ignore_index and transform) or the logits recomputed."""
     _check(h, W, targets)
     if targets is None:
         raise ValueError("targets are needed")
@@ -81,25 +90,31 @@ def score_backward(h, W, targets, lse, entropy, grad_logp=None, grad_entropy=Non
     for x, name in ((lse, "lse"), (entropy, "entropy"), (grad_logp, "grad_logp"), (grad_entropy, "grad_entropy")):
         _row_vector(x, h, name)
     (N, H), V, dev = h.shape, W.shape[0], h.device
+    if state is not None and (state.device != dev or not state.is_contiguous() or not N or
+                              state.numel() * state.element_size() != _lib.flce_score_state_bytes(N, H, V, N)):
+        raise ValueError("state must come from score_forward of the same sizes")
+    if state is not None:
+        chunk_rows = max(chunk_rows, N)  # the kept rows are one block
     with _on(h):
         dH = torch.empty_like(h) if need_dH else None
         dW = torch.empty((V, H), dtype=dW_dtype, device=dev) if need_dW else None
         ws, ws_bytes = _workspace(workspace, _lib.flce_score_backward_workspace_bytes(N, H, V, chunk_rows, _DW[dW_dtype]),
                                   stream, dev)
         _lib.check("flce_score_backward", _lib.flce_score_backward(
-            h, W, targets, lse, entropy, grad_logp, grad_entropy, dH, dW, _DW[dW_dtype], N, H, V, chunk_rows,
+            h, W, targets, lse, entropy, grad_logp, grad_entropy, state, dH, dW, _DW[dW_dtype], N, H, V, chunk_rows,
             ignore_index, transform, ws, ws_bytes, stream))
     return dH, dW
 
 
 class SelectiveLogSoftmaxEntropy(torch.autograd.Function):
-    """selective_log_softmax_entropy with the logits recomputed in the backward."""
+    """selective_log_softmax_entropy with its backward, from kept logits where the
+    rows fit chunk_rows, else recomputing them."""
 
     @staticmethod
-    def forward(ctx, h, W, targets, chunk_rows, ignore_index, transform):
+    def forward(ctx, h, W, targets, chunk_rows, ignore_index, transform, recompute):
         ctx.set_materialize_grads(False)  # no zeros for an output without a gradient
-        out = score_forward(h, W, targets, 0, ignore_index, transform)
-        ctx.save_for_backward(h, W, targets, out["lse"], out["entropy"])
+        out = score_forward(h, W, targets, 0, ignore_index, transform, keep_rows=0 if recompute else chunk_rows)
+        ctx.save_for_backward(h, W, targets, out["lse"], out["entropy"], out["state"])
         ctx.chunk_rows, ctx.ignore_index, ctx.transform = chunk_rows, ignore_index, transform
         return out["logp"], out["entropy"]
 
@@ -107,26 +122,30 @@ class SelectiveLogSoftmaxEntropy(torch.autograd.Function):
     def backward(ctx, grad_logp, grad_entropy):
         need_h, need_W = ctx.needs_input_grad[:2]
         if (grad_logp is None and grad_entropy is None) or not (need_h or need_W):
-            return (None,) * 6
-        h, W, targets, lse, entropy = ctx.saved_tensors
+            return (None,) * 7
+        h, W, targets, lse, entropy, state = ctx.saved_tensors
         ga, ge = (None if g is None else g.detach().to(torch.float32).contiguous() for g in (grad_logp, grad_entropy))
         dH, dW = score_backward(h.detach(), W.detach(), targets, lse, entropy.detach(), ga, ge, ctx.chunk_rows,
-                                ctx.ignore_index, ctx.transform, need_h, need_W, dW_dtype=W.dtype)
-        return _first_order((dH, dW), (h, W, grad_logp, grad_entropy)) + (None,) * 4
+                                ctx.ignore_index, ctx.transform, need_h, need_W, dW_dtype=W.dtype, state=state)
+        return _first_order((dH, dW), (h, W, grad_logp, grad_entropy)) + (None,) * 5
 
 
 def selective_log_softmax_entropy(h, W, targets, chunk_rows: int = 256, ignore_index: int = IGNORE_INDEX,
-                                  transform=None):
+                                  transform=None, recompute: bool = False):
     """(logp[N], entropy[N]) fp32: log-probability of each row's target and entropy
     (natural units) of softmax(f(h W^T)), both differentiable in h and W; 0 on
     rows whose target is ignore_index.  For policy losses with an entropy term:
-    both come out of one pass over the head, and both gradients of another."""
+    both come out of one pass over the head, and both gradients of another.
+
+    chunk_rows bounds the rows of dlogits that the backward holds.  A call of at
+    most that many rows keeps its logits until then, 2 bytes each, and the
+    backward saves their product; recompute=True keeps nothing."""
     if targets is None:
         raise ValueError("targets are needed")
     if not torch.is_grad_enabled() or not (h.requires_grad or W.requires_grad):
         out = score_forward(h, W, targets, 0, ignore_index, transform)
         return out["logp"], out["entropy"]
-    return SelectiveLogSoftmaxEntropy.apply(h, W, targets, chunk_rows, ignore_index, transform)
+    return SelectiveLogSoftmaxEntropy.apply(h, W, targets, chunk_rows, ignore_index, transform, recompute)
 
 
 def top_logprobs(h, W, k: int, targets=None, ignore_index: int = IGNORE_INDEX, transform=None,

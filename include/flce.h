@@ -754,6 +754,10 @@ FLCE_API size_t flce_layer_norm_backward_workspace_bytes(int64_t N, int64_t H);
  *   out_logp (needs targets), out_lse, out_entropy [N] fp32, each may be NULL;
  *   out_ids [N,k] int64 and out_logprobs [N,k] fp32: NULL exactly when k is 0,
  *            else one of them may be.  At least one output.
+ *   state    NULL, or flce_score_state_bytes bytes, 256-byte aligned (with targets
+ *            and k = 0, N <= 32,768): what flce_score_backward reads in place of
+ *            the product again -- the logits, 2 bytes each, relative to the
+ *            largest of 32.
  * A row with a logit z that is NaN or +infinity (with a soft-cap, any infinity),
  * or none above -infinity: NaN, ids of -1.  N <= 2^31 - 65,537.  Workspace:
  * flce_score_workspace_bytes(N, H, V, k), or NULL (stream-ordered allocation); it
@@ -763,29 +767,37 @@ FLCE_API size_t flce_layer_norm_backward_workspace_bytes(int64_t N, int64_t H);
 FLCE_API flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* targets, int64_t N,
                                 int64_t H, int64_t V, int64_t k, int64_t ignore_index,
                                 const flce_logit_transform* transform, float* out_logp, float* out_lse,
-                                float* out_entropy, int64_t* out_ids, float* out_logprobs,
+                                float* out_entropy, int64_t* out_ids, float* out_logprobs, void* state,
                                 void* workspace, size_t workspace_bytes, void* stream);
 FLCE_API size_t flce_score_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k);
+/* Bytes of the state where keeping it pays: the rows fit the backward's dlogits
+ * budget (N <= chunk_rows rounded up to 128, and 32,768) and the product costs
+ * more than reading them (H >= 512; or, for the gradients' precision, N <= 128).
+ * Else 0: pass no state. */
+FLCE_API size_t flce_score_state_bytes(int64_t N, int64_t H, int64_t V, int64_t chunk_rows);
 
 /*
  * Gradients of sum_i g_logp[i] logp[i] + g_entropy[i] entropy[i]:
  *   D[i,v] = (g_logp ([v == t] - p_v) - g_entropy p_v (log p_v + entropy)) f'(z)
  *   dH = D W,  dW = D^T h
- * with the logits recomputed block by block as in flce_backward (chunk_rows
- * bounds the dlogits held at once).  lse, entropy [N] from flce_score; g_logp,
+ * with the logits from state (of flce_score with the same h, W, targets,
+ * ignore_index and transform; it is left as it was), or without one recomputed
+ * block by block as in flce_backward (chunk_rows bounds the dlogits held at
+ * once).  lse, entropy [N] from flce_score; g_logp,
  * g_entropy [N] fp32, each may be NULL (zero).  Rows whose target is
  * ignore_index have no gradient; a target outside [0,V) has no one-hot term.
  *   dH [N,H] bf16, dW [V,H] of dW_type (FLCE_F32 or FLCE_BF16); either may be
  *   NULL, not both.
- * Workspace: flce_score_backward_workspace_bytes, or NULL (stream-ordered
- * allocation).
+ * Workspace: flce_score_backward_workspace_bytes (with a state, of the chunk_rows
+ * that flce_score_state_bytes took), or NULL (stream-ordered allocation).
  */
 FLCE_API flce_status flce_score_backward(const flce_bf16* h, const flce_bf16* W, const int64_t* targets,
                                          const float* lse, const float* entropy, const float* g_logp,
-                                         const float* g_entropy, flce_bf16* dH, void* dW, int32_t dW_type,
-                                         int64_t N, int64_t H, int64_t V, int64_t chunk_rows,
-                                         int64_t ignore_index, const flce_logit_transform* transform,
-                                         void* workspace, size_t workspace_bytes, void* stream);
+                                         const float* g_entropy, const void* state, flce_bf16* dH, void* dW,
+                                         int32_t dW_type, int64_t N, int64_t H, int64_t V,
+                                         int64_t chunk_rows, int64_t ignore_index,
+                                         const flce_logit_transform* transform, void* workspace,
+                                         size_t workspace_bytes, void* stream);
 FLCE_API size_t flce_score_backward_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t chunk_rows,
                                                     int32_t dW_type);
 

@@ -89,21 +89,35 @@ def check(out, h, W, targets, r, k=0, tf=None, what=""):
         assert bool(same.all()), (what, "ids", int((~same).sum()))
 
 
-def check_grads(dH, dW, h, W, targets, r, ga, ge, tf=None, what=""):
+def chunk_distance(u):
+    """[N, V] how far each u is below the largest of its 32 columns."""
+    N, V = u.shape
+    pad = torch.nn.functional.pad(u, (0, -V % 32), value=-math.inf).view(N, -1, 32)
+    return (pad.amax(2, keepdim=True) - pad).view(N, -1)[:, :V]
+
+
+def check_grads(dH, dW, h, W, targets, r, ga, ge, tf=None, what="", kept=False):
     """Against D W and D^T h: D rounded to bf16 once (2^-8 of each value, half a
-    step) after the errors of p and log p, the sums' cuts, the outputs' rounding."""
+    step) after the errors of p and log p, the sums' cuts, the outputs' rounding.
+    kept: logits in fp16 relative to the largest of their 32 columns (2^-11 of that
+    distance, and 2^-25 where it is below fp16's range), and the dlogits of at
+    most 128 rows in two parts (2^-16)."""
     D, onehot = dlogits(r, targets, ga, ge)
     on = r["on"][:, None]
     e = logit_error(h, r, tf)[:, None]
     mag = lambda g: 0.0 if g is None else torch.where(on, g.double().abs()[:, None], 0.0)  # noqa: E731
     # p's relative error: that of u and lse, and 2^-19 as above; log p's: the same, absolute
     rel = 2 * e + 2.0 ** -18
+    half_d = 2.0 ** -8
+    if kept:
+        rel = rel + 2.0 ** -11 * chunk_distance(r["u"]) + 2.0 ** -24
+        half_d = 2.0 ** -16 if h.shape[0] <= 128 else half_d
     terms = r["q"] * (mag(ga) + mag(ge) * ((r["logq"] + r["entropy"][:, None]).abs() + 1)) * r["slope"]
     # (a soft-cap's slope, 1 - tanh^2, loses bits where tanh is near 1: 2^-21 of 1)
     if tf and tf.get("softcap"):
         terms = terms + (r["q"] * mag(ge) * (r["logq"].abs() + 1) + (r["q"] + onehot) * mag(ga)) * 2.0 ** -2 / tf.get(
             "temperature", 1.0)
-    dD = 1.01 * 2.0 ** -8 * D.abs() + rel * terms
+    dD = 1.01 * half_d * D.abs() + rel * terms
     for name, got, want, err, absolute in (
             ("dH", dH, D @ W.double(), dD @ W.double().abs(), D.abs() @ W.double().abs()),
             ("dW", dW, D.t() @ h.double(), dD.t() @ h.double().abs(), D.t().abs() @ h.double().abs())):

@@ -216,12 +216,86 @@ def test_gradients_match_the_definition(N, H, V, chunk, tf, which):
     with torch.no_grad():
         r = R.reference(h, W, t, 0, tf)
         R.check(dict(logp=logp, entropy=entropy), h, W, t, r, tf=tf)
-        R.check_grads(dH, dW, h, W, t, r, ga, ge, tf)
+        R.check_grads(dH, dW, h, W, t, r, ga, ge, tf, kept=N <= 128)
         out = flce.score_forward(h, W, t, transform=tf)
         dH32, dW32 = flce.score_backward(h, W, t, out["lse"], out["entropy"], ga, ge, chunk, transform=tf)
-        assert torch.equal(dH32, dH)
-        assert torch.equal(dW32.bfloat16(), dW)
-        R.check_grads(None, dW32, h, W, t, r, ga, ge, tf)
+        if N > 128:  # (else the first were from kept logits)
+            assert torch.equal(dH32, dH)
+            assert torch.equal(dW32.bfloat16(), dW)
+        R.check_grads(dH32, dW32, h, W, t, r, ga, ge, tf)
+    assert _lib.flce_device_status() == 0
+
+
+KEPT = [(1, 512, 1000), (3, 64, 1000), (128, 72, 5003), (4, 520, 5003), (64, 512, 3001), (65, 1096, 2000), (128, 512, 9000), (129, 512, 3000),
+        (300, 1000, 9001), (700, 512, 20001), (2049, 512, 1000)]
+
+
+@pytest.mark.parametrize("which", ["both", "logp", "entropy"])
+@pytest.mark.parametrize("tf", TFS[:3], ids=["none", "temperature", "softcap"])
+@pytest.mark.parametrize("N,H,V", KEPT)
+def test_gradients_from_kept_logits(N, H, V, tf, which):
+    """Rows on both sides of the two-part dlogits and of the row compaction."""
+    h, W, t, ga, ge = make(N, H, V, seed=22, mask=0.2)
+    ga = None if which == "entropy" else ga
+    ge = None if which == "logp" else ge
+    out = flce.score_forward(h, W, t, transform=tf, keep_rows=N)
+    assert out["state"] is not None
+    before = out["state"].clone()
+    r = R.reference(h, W, t, 0, tf)
+    R.check(out, h, W, t, r, tf=tf)
+    for dt in (torch.float32, BF16):
+        dH, dW = flce.score_backward(h, W, t, out["lse"], out["entropy"], ga, ge, transform=tf, state=out["state"],
+                                     dW_dtype=dt)
+        assert _lib.flce_device_status() == 0
+        R.check_grads(dH, dW, h, W, t, r, ga, ge, tf, kept=True)
+    one = flce.score_backward(h, W, t, out["lse"], out["entropy"], ga, ge, transform=tf, state=out["state"],
+                              need_dW=False)
+    assert one[1] is None and torch.equal(one[0], dH)
+    assert torch.equal(out["state"], before)  # it can be read again
+
+
+def test_kept_and_recomputed_through_autograd():
+    N, H, V = 200, 512, 9001
+    h, W, t, ga, ge = make(N, H, V, seed=23, mask=0.2)
+    h.requires_grad_(True)
+    W.requires_grad_(True)
+    with torch.no_grad():
+        r = R.reference(h, W, t)
+    for kw, kept in ((dict(chunk_rows=256), True), (dict(chunk_rows=256, recompute=True), False),
+                     (dict(chunk_rows=128), False)):
+        logp, entropy = flce.selective_log_softmax_entropy(h, W, t, **kw)
+        grads = torch.autograd.grad((logp, entropy), (h, W), (ga, ge), retain_graph=True)
+        again = torch.autograd.grad((logp, entropy), (h, W), (ga, ge))
+        with torch.no_grad():
+            R.check_grads(*grads, h, W, t, r, ga, ge, kept=kept)
+        assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+def test_likely_targets_keep_their_gradient():
+    """1 - p of a target with p = 0.999: 16-bit logits alone would be off by a tenth of it."""
+    N, H, V = 32, 512, 3000
+    h, W, t, ga, ge = make(N, H, V, seed=24)
+    t[:] = torch.arange(N, device="cuda") * 90 + 7
+    W[t] = (0.04 * h.float()).bfloat16()  # logits about 20 against a log-sum-exp of 12.5 of the others
+    r = R.reference(h, W, t)
+    assert bool(((1 - r["logp"].exp()) < 0.02).all())
+    out = flce.score_forward(h, W, t, keep_rows=N)
+    dH, dW = flce.score_backward(h, W, t, out["lse"], out["entropy"], ga, None, state=out["state"])
+    R.check_grads(dH, dW, h, W, t, r, ga, None, kept=True)
+    D, _ = R.dlogits(r, t, ga, None)
+    for got, want in ((dH, D @ W.double()), (dW, D.t() @ h.double())):
+        assert float((got.double() - want).norm() / want.norm()) < 5e-3
+
+
+@pytest.mark.parametrize("option,value", [("cta_group", 1), ("compact", 0), ("fwd_splits", 3), ("dh_splits", 2)])
+def test_options_leave_kept_logits_right(flce_opts, option, value):
+    h, W, t, ga, ge = make(400, 512, 9001, seed=25, mask=0.3)
+    r = R.reference(h, W, t)
+    out = flce.score_forward(h, W, t, keep_rows=512)
+    flce_opts.set(option, value)  # between forward and backward, and then for both
+    for o in (out, flce.score_forward(h, W, t, keep_rows=512)):
+        dH, dW = flce.score_backward(h, W, t, o["lse"], o["entropy"], ga, ge, state=o["state"])
+        R.check_grads(dH, dW, h, W, t, r, ga, ge, kept=True)
     assert _lib.flce_device_status() == 0
 
 
@@ -300,14 +374,14 @@ def test_two_calls_at_once():
                 assert torch.equal(o[k], w[k]), k
 
 
-@pytest.mark.parametrize("N", [2, 150, 2100])
-def test_capture_and_replay(N):
-    h, W, t, ga, ge = make(N, 64, 9001, seed=16, mask=0.2)
+@pytest.mark.parametrize("N,H", [(2, 64), (150, 64), (2100, 64), (2, 512), (300, 512)])
+def test_capture_and_replay(N, H):
+    h, W, t, ga, ge = make(N, H, 9001, seed=16, mask=0.2)
 
     def step():
         x, y = h.detach().requires_grad_(True), W.detach().requires_grad_(True)  # leaves of this step's own
         o = flce.top_logprobs(h, W, 6, t)
-        logp, entropy = flce.selective_log_softmax_entropy(x, y, t)
+        logp, entropy = flce.selective_log_softmax_entropy(x, y, t, chunk_rows=512)
         return [o[k] for k in ("ids", "logprobs", "lse", "entropy", "logp")] + [logp.detach(), entropy.detach()] + list(
             torch.autograd.grad((logp, entropy), (x, y), (ga, ge)))
 
@@ -319,8 +393,8 @@ def test_capture_and_replay(N):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         captured = step()
-    h.copy_(make(N, 64, 9001, seed=17)[0])
-    t.copy_(make(N, 64, 9001, seed=18, mask=0.5)[2])
+    h.copy_(make(N, H, 9001, seed=17)[0])
+    t.copy_(make(N, H, 9001, seed=18, mask=0.5)[2])
     graph.replay()
     torch.cuda.synchronize()
     captured = [c.clone() for c in captured]
@@ -378,6 +452,8 @@ def test_refusals_of_the_torch_checks():
                  lambda: flce.score_backward(h, W, t, o["lse"].double(), o["entropy"], ga, ge),
                  lambda: flce.score_backward(h, W, t, o["lse"], o["entropy"], ga[:3], ge),
                  lambda: flce.score_backward(h, W, None, o["lse"], o["entropy"], ga, ge),
+                 lambda: flce.score_backward(h, W, t, o["lse"], o["entropy"], ga, ge, state=ga),
+                 lambda: flce.score_forward(h, W, keep_rows=8), lambda: flce.score_forward(h, W, t, 3, keep_rows=8),
                  lambda: flce.score_backward(h, W, t, o["lse"], o["entropy"], ga, ge, dW_dtype=torch.float16)):
         with pytest.raises(ValueError):
             call()

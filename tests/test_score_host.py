@@ -12,12 +12,14 @@ D = _lib.DTYPES
 OK, INVALID, UNSUPPORTED = 0, 1, 3
 
 
-def fwd(h=P, W=P, t=P, N=4, H=64, V=1000, k=0, tf=None, logp=P, lse=P, ent=P, ids=None, words=None, ws=None, wb=0):
-    return _lib.flce_score(h, W, t, N, H, V, k, -100, tf, logp, lse, ent, ids, words, ws, wb, 0)
+def fwd(h=P, W=P, t=P, N=4, H=64, V=1000, k=0, tf=None, logp=P, lse=P, ent=P, ids=None, words=None, st=None, ws=None,
+        wb=0):
+    return _lib.flce_score(h, W, t, N, H, V, k, -100, tf, logp, lse, ent, ids, words, st, ws, wb, 0)
 
 
-def bwd(h=P, W=P, t=P, lse=P, ent=P, ga=P, ge=P, dH=P, dW=P, dt=D["f32"], N=4, H=64, V=1000, tf=None, ws=None, wb=0):
-    return _lib.flce_score_backward(h, W, t, lse, ent, ga, ge, dH, dW, dt, N, H, V, 256, -100, tf, ws, wb, 0)
+def bwd(h=P, W=P, t=P, lse=P, ent=P, ga=P, ge=P, st=None, dH=P, dW=P, dt=D["f32"], N=4, H=64, V=1000, tf=None, ws=None,
+        wb=0):
+    return _lib.flce_score_backward(h, W, t, lse, ent, ga, ge, st, dH, dW, dt, N, H, V, 256, -100, tf, ws, wb, 0)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -30,6 +32,8 @@ def bwd(h=P, W=P, t=P, lse=P, ent=P, ga=P, ge=P, dH=P, dW=P, dt=D["f32"], N=4, H
     (dict(W=P + 8), UNSUPPORTED), (dict(t=P + 4), UNSUPPORTED), (dict(logp=P + 2), UNSUPPORTED),
     (dict(lse=P + 1), UNSUPPORTED), (dict(ent=P + 2), UNSUPPORTED), (dict(k=3, ids=P + 4), UNSUPPORTED),
     (dict(k=3, words=P + 2), UNSUPPORTED),
+    (dict(st=P, k=3, ids=P), INVALID), (dict(st=P, t=None, logp=None), INVALID), (dict(st=P + 16), UNSUPPORTED),
+    (dict(st=P, N=32769), UNSUPPORTED), (dict(st=P, ws=P, wb=64), INVALID),
     (dict(N=0), OK), (dict(N=0, h=None, W=None, t=None), OK), (dict(N=0, k=5, ids=P), OK),
 ])
 def test_forward_refusals(kw, want):
@@ -42,6 +46,8 @@ def test_forward_refusals(kw, want):
     (dict(dt=D["f16"]), INVALID), (dict(tf={"temperature": -1.0}), INVALID), (dict(ws=P, wb=64), INVALID),
     (dict(H=12), UNSUPPORTED), (dict(dW=P + 8), UNSUPPORTED), (dict(dH=P + 2), UNSUPPORTED),
     (dict(ga=P + 2), UNSUPPORTED), (dict(ge=P + 2), UNSUPPORTED), (dict(t=P + 4), UNSUPPORTED),
+    (dict(st=P + 128), UNSUPPORTED), (dict(st=P, N=32769), UNSUPPORTED), (dict(st=P, ws=P, wb=64), INVALID),
+    (dict(st=P, dH=None, dW=None), INVALID), (dict(N=0, dW=None), OK), (dict(N=0, dH=None, dW=None), OK),
 ])
 def test_backward_refusals(kw, want):
     assert bwd(**kw) == want
@@ -59,6 +65,12 @@ def test_sizes():
     b = _lib.flce_score_backward_workspace_bytes
     assert b(4096, 512, 20000, 4096, D["bf16"]) == b(4096, 512, 20000, 4096, D["f32"])
     assert b(8192, 512, 20000, 256, D["bf16"]) >= 20000 * 512 * 4
+    # the kept logits: 2 bytes a column and 1/8 for the chunks' maxima, where the rows fit the budget
+    s = _lib.flce_score_state_bytes
+    assert 0 < s(4096, 1024, 20000, 4096) <= 4096 * (20256 * 2.25 + 16) + 4096
+    assert s(4096, 1024, 20000, 3968) == 0 and s(4096, 64, 20000, 4096) == 0 and s(0, 1024, 20000, 4096) == 0
+    assert s(128, 64, 20000, 128) > 0 and s(129, 64, 20000, 256) == 0
+    assert s(40000, 1024, 20000, 40000) == 0 and s(5, 1024, 20000, 1) > 0 and s(-1, 1024, 20000, 4096) == 0
 
 
 def test_torch_checks():
