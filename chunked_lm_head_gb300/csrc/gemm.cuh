@@ -281,7 +281,8 @@ struct GemmParams {
   // units: each row's entropy and the gradients of its log-probability and
   // entropy ([N], a gradient may be null: zero)
   float4* score_part;
-  float2* rec;
+  float2* rec;   // the two largest
+  float* rec3;   // the third
   float* z;    // in the records' place: the logits [rows][rec_ld], fp32
   int rec_ld;  // covers whole tiles
   const float* entropy;
@@ -844,10 +845,10 @@ __device__ __forceinline__ int list_lower_bound(const int* ids, int k, int v) {
   return lo;
 }
 
-// The record of a 32-column chunk of raw logits: its largest and its second
-// largest, each with 31 - its column in the low 5 bits of its fp32 value (off by
-// at most 2^-18 of itself).  The select kernel has to look at a chunk's other
-// columns only where the second is near the words it keeps.
+// The record of a 32-column chunk of raw logits: its three largest, each with 31 -
+// its column in the low 5 bits of its fp32 value (off by at most 2^-18 of itself).
+// The select kernel has to look at a chunk's other columns only where the third is
+// near the words it keeps.
 __device__ __forceinline__ float score_key(float z, int j) {
   return __uint_as_float((__float_as_uint(z) & ~31u) | static_cast<uint32_t>(31 - j));
 }
@@ -1172,7 +1173,8 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                     "scores: the forwards and, for the entropy, the dlogits units");
       float run_ent = 0.f, run_abs = 0.f;                   // FWD scores: sum 2^(x - m) (m - x), a largest |z|
       float sc_a = 0.f, sc_b = 0.f, sc_t = 0.f;             // DLOGITS scores: D = p (sc_a log2 p + sc_b) + onehot sc_t
-      float2 rec_even = make_float2(0.f, 0.f);
+      float2 rec_even = make_float2(0.f, 0.f);              // TOP: the even chunk's record
+      float rec_third = 0.f;
       // linear transform folded into the exp2 prescale, the gathered target
       // logit and the dlogits scale (soft-capped logits are formed explicitly)
       const float lin_a = p.tf_softcap ? 1.f : p.tf_a;
@@ -1289,19 +1291,24 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                   dst[g] = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
               }
             } else if constexpr (kScore == SCORE_TOP) {
-              float m1 = -INFINITY, m2 = -INFINITY;
+              float m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 const float key = nc == 32 || j < nc ? score_key(v[j], j) : -INFINITY;
-                m2 = fmaxf(m2, fminf(m1, key));
+                const float less = fminf(m1, key);
                 m1 = fmaxf(m1, key);
+                m3 = fmaxf(m3, fminf(m2, less));
+                m2 = fmaxf(m2, less);
               }
               // two chunks' records leave together
-              if ((c & 1) == 0)
+              if ((c & 1) == 0) {
                 rec_even = make_float2(m1, m2);
-              else if (row_ok)
-                *reinterpret_cast<float4*>(p.rec + static_cast<idx_t>(lr) * p.rec_ld + (col0 / 32 - 1)) =
-                    make_float4(rec_even.x, rec_even.y, m1, m2);
+                rec_third = m3;
+              } else if (row_ok) {
+                const idx_t at = static_cast<idx_t>(lr) * p.rec_ld + (col0 / 32 - 1);
+                *reinterpret_cast<float4*>(p.rec + at) = make_float4(rec_even.x, rec_even.y, m1, m2);
+                *reinterpret_cast<float2*>(p.rec3 + at) = make_float2(rec_third, m3);
+              }
             }
             if (p.tf_softcap) {
               // (an infinite logit, which tanh would hide, becomes NaN: 0 z)

@@ -7,7 +7,7 @@
 //     S = sum_v e^(u_v - m),  C = sum_v e^(u_v - m) (m - u_v)   (any m)
 //   the K words with the largest z (f increases), ties to the lowest index
 // The forward GEMM leaves a partial (m, S, C) per row and vocabulary split and,
-// for the words, the two largest z of every 32-column chunk (gemm.cuh,
+// for the words, the three largest z of every 32-column chunk (gemm.cuh,
 // score_key).
 //
 // The words' order.  The tensor cores' fp32 sums are off by some 1e-6 of the
@@ -157,48 +157,62 @@ __device__ __forceinline__ float2 two_add(float2 x, float2 y) {
   return make_float2(s.x, s.y + (x.y + y.y));
 }
 
-// sum_k h_k w_k of two bf16 rows by a warp, as a rounded value and what the
-// rounding leaves out: products of bf16 are exact in fp32, each step of the sum
-// hands its rounding error to a second sum.  The same in all lanes.  1,024
-// elements are read at once: a word's row is somewhere else in memory each time.
-__device__ __forceinline__ float2 exact_dot(const uint16_t* __restrict__ h, const uint16_t* __restrict__ w, int H,
-                                            int lane) {
-  float2 hi = both(0.f), lo = both(0.f);
+// sum_k h_k w_k of a bf16 row with NW others by a warp, each as a rounded value
+// and what the rounding leaves out: products of bf16 are exact in fp32, each step
+// of the sum hands its rounding error to a second sum.  The same in all lanes.
+// 1,024 elements of each are read at once: a word's row is somewhere else in
+// memory each time.
+template <int NW>
+__device__ __forceinline__ void exact_dots(const uint16_t* __restrict__ h, const uint16_t* const (&w)[NW], int H,
+                                           int lane, float2 (&out)[NW]) {
+  float2 hi[NW], lo[NW];
+#pragma unroll
+  for (int i = 0; i < NW; ++i) hi[i] = lo[i] = both(0.f);
   const float2 minus = both(-1.f);
   for (int k0 = lane * 8; k0 < H; k0 += 1024) {
-    Raw8<uint16_t> a[4], b[4];
+    Raw8<uint16_t> a[4], b[NW][4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int k = k0 + 256 * g;
-      if (k < H) {
-        b[g].q[0] = __ldg(reinterpret_cast<const uint4*>(w + k));
-        a[g].q[0] = __ldg(reinterpret_cast<const uint4*>(h + k));
-      } else {
-        b[g].zero();
-        a[g].zero();
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        if (k < H)
+          b[i][g].q[0] = __ldg(reinterpret_cast<const uint4*>(w[i] + k));
+        else
+          b[i][g].zero();
       }
+      if (k < H)
+        a[g].q[0] = __ldg(reinterpret_cast<const uint4*>(h + k));
+      else
+        a[g].zero();
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       if (k0 - lane * 8 + 256 * g >= H) break;  // (the whole warp)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 p = mul2(a[g].pair(e), b[g].pair(e));
-        const float2 s = add2(hi, p);
-        const float2 y = fma2(hi, minus, s);                         // s - hi
-        const float2 x = fma2(y, minus, s);                          // s - y
-        lo = add2(lo, add2(fma2(x, minus, hi), fma2(y, minus, p)));  // (hi - x) + (p - y)
-        hi = s;
+        const float2 x = a[g].pair(e);
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          const float2 p = mul2(x, b[i][g].pair(e));
+          const float2 s = add2(hi[i], p);
+          const float2 y = fma2(hi[i], minus, s);                                // s - hi
+          const float2 r = fma2(y, minus, s);                                    // s - y
+          lo[i] = add2(lo[i], add2(fma2(r, minus, hi[i]), fma2(y, minus, p)));  // (hi - r) + (p - y)
+          hi[i] = s;
+        }
       }
     }
   }
-  float2 d = two_add(make_float2(hi.x, lo.x), make_float2(hi.y, lo.y));
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-    d = two_add(d, make_float2(__shfl_xor_sync(0xffffffffu, d.x, off), __shfl_xor_sync(0xffffffffu, d.y, off)));
-  // (a sum that is not finite has no rest; one that is NaN comes last)
-  if (!(fabsf(d.x) < INFINITY)) return make_float2(d.x == INFINITY ? d.x : -INFINITY, 0.f);
-  return two_sum(d.x, d.y);
+  for (int i = 0; i < NW; ++i) {
+    float2 d = two_add(make_float2(hi[i].x, lo[i].x), make_float2(hi[i].y, lo[i].y));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      d = two_add(d, make_float2(__shfl_xor_sync(0xffffffffu, d.x, off), __shfl_xor_sync(0xffffffffu, d.y, off)));
+    // (a sum that is not finite has no rest; one that is NaN comes last)
+    out[i] = !(fabsf(d.x) < INFINITY) ? make_float2(d.x == INFINITY ? d.x : -INFINITY, 0.f) : two_sum(d.x, d.y);
+  }
 }
 
 // Whether word (a, i) comes before word (b, j): the larger logit, then the lower index.
@@ -208,11 +222,21 @@ __device__ __forceinline__ bool word_before(float2 a, int i, float2 b, int j) {
   return i < j;
 }
 
+// A float's bits in an unsigned order, and back (both infinities included).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u ^ ((u & 0x80000000u) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+}
+
 struct SelectParams {
   const uint16_t* h;   // [N][H]
   const uint16_t* W;   // [V][H]
   const float4* part;  // [rows][S]
-  const float2* rec;   // [rows][ld] chunk records, or
+  const float2* rec;   // [rows][ld] chunk records: the two largest,
+  const float* rec3;   // [rows][ld] and the third; or
   const float* z;      // [rows][ld] logits
   int S, ld, H, V;
   ScoreRows rows;
@@ -225,30 +249,33 @@ struct SelectParams {
 };
 
 // The K likeliest words of a row on a CTA of T threads.
-//   1. Each of 256 groups of threads takes the largest of its records (kDense: of
-//      its logits); the K-th largest of the groups' is a lower bound of the K-th
-//      largest logit, close to it (K words on 256 groups seldom share one).
-//   2. Candidates: the words that reach the bound, less what both can be off by.
-//      Of a chunk whose second largest reaches it too, all 32.
-//   3. Their logits again, a warp to a word, and a rank for each by counting.
+//   1. Each thread takes the largest of its records (kDense: of its logits).  The
+//      K-th largest of the threads', to 8 bits, by bisection with one counting
+//      barrier a bit, is a lower bound of the K-th largest logit.
+//   2. Listed are the words that reach the bound, less what both can be off by; of
+//      a chunk whose third largest does too, all 32.  The K-th largest of the
+//      listed is a better bound, and drops those that it rules out.
+//   3. The logits of what is left, K words and their near ties, two words to a
+//      warp at a time, and a rank for each by counting.
 // More candidates than the list holds (logits that are nearly all equal) go
 // through it in runs, in index order, with the K best so far kept and the bound
 // raised to theirs.
-constexpr int SELECT_CAP = 1024;  // words of the list: more than SCORE_MAX_K and a chunk
-constexpr int SELECT_GROUPS = 256;
-static_assert(SELECT_GROUPS >= SCORE_MAX_K && SELECT_CAP >= SCORE_MAX_K + 32, "the list and the groups hold K");
+constexpr int SELECT_CAP = 1024;  // words of the list
+static_assert(SELECT_CAP >= SCORE_MAX_K + 32, "the list holds K words and a chunk");
 
 template <int T, bool kDense, bool kLong>
 __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__ SelectParams p) {
+  static_assert(T >= SCORE_MAX_K, "K threads have a largest record each");
   dependent_start();
   using idx_t = typename std::conditional<kLong, long long, int>::type;
   __shared__ float2 val[SELECT_CAP];
+  __shared__ __align__(16) float near[SELECT_CAP + 4];  // the records' logits
   __shared__ int word[SELECT_CAP];
-  __shared__ __align__(16) float tops[SELECT_GROUPS];
   __shared__ int sums[T / 32];
-  __shared__ int found;
-  __shared__ float bound, largest;
+  __shared__ int found, kept_words, whole_chunks;
+  __shared__ float best_k;
   __shared__ float2 target_z;
+  __shared__ ScorePart row_part;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int K = p.out.k;
   const int j = blockIdx.x;
@@ -259,19 +286,12 @@ __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__
     score_no_row(p.out, i, 0.f, t, T);
     return;
   }
-  const ScorePart whole = score_join_row(p.part + static_cast<idx_t>(j) * p.S, p.S, lane);
-  const float2 r = score_of(whole);
-  if (r.x != r.x) {  // (the same in every warp)
-    score_no_row(p.out, i, r.x, t, T);
-    return;
-  }
   // a unit: a chunk and its record, or (kDense) a word and its logit
   const int units = kDense ? p.V : (p.V + 31) / 32;
   const idx_t base = static_cast<idx_t>(j) * p.ld;
   auto unit = [&](int c) {
     if constexpr (kDense) {
-      const float z = p.z[base + c];
-      return make_float2(z, z);
+      return make_float2(p.z[base + c], -INFINITY);
     } else {
       return p.rec[base + c];
     }
@@ -280,58 +300,68 @@ __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__
   float top = -INFINITY;
 #pragma unroll 4
   for (int c = t; c < units; c += T) top = fmaxf(top, unit(c).x);
-#pragma unroll
-  for (int off = 1; off < T / SELECT_GROUPS; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (t % (T / SELECT_GROUPS) == 0) tops[t / (T / SELECT_GROUPS)] = top;
-  if (t == 0) found = 0;
-  const bool want_target = tgt >= 0 && tgt < p.V && p.out.logp != nullptr;
-  __syncthreads();
-  if (t < SELECT_GROUPS) {
-    const float mine = tops[t];
-    int rank = 0;
-    float most = -INFINITY;
-    for (int q = 0; q < SELECT_GROUPS; q += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(tops + q);
-      rank += (o.x > mine || (o.x == mine && q < t)) + (o.y > mine || (o.y == mine && q + 1 < t)) +
-              (o.z > mine || (o.z == mine && q + 2 < t)) + (o.w > mine || (o.w == mine && q + 3 < t));
-      most = fmaxf(fmaxf(most, fmaxf(o.x, o.y)), fmaxf(o.z, o.w));
-    }
-    if (rank == K - 1) {
-      bound = mine;
-      largest = most;
+  if (warp == 0) {
+    const ScorePart w = score_join_row(p.part + static_cast<idx_t>(j) * p.S, p.S, lane);
+    if (lane == 0) {
+      row_part = w;
+      found = kept_words = whole_chunks = 0;
     }
   }
-  __syncthreads();
-  // (K groups with a record: K chunks; else every word is a candidate)
-  const float low = bound, most = largest;
-  const float size = fmaxf(whole.top < INFINITY ? whole.top : 0.f, fmaxf(fabsf(most), low > -INFINITY ? fabsf(low) : 0.f));
-  const float off = p.slack * size + 1e-43f;
+  const uint32_t mine = ordered(top);
+  uint32_t prefix = 0;
+#pragma unroll 1
+  for (uint32_t bit = 0x80000000u; bit >= 0x8000u; bit >>= 1)
+    if (__syncthreads_count(mine >= (prefix | bit)) >= K) prefix |= bit;
+  const ScorePart whole = row_part;
+  const float2 r = score_of(whole);
+  if (r.x != r.x) {
+    score_no_row(p.out, i, r.x, t, T);
+    return;
+  }
+  // (fewer than K threads with a record above -infinity: every word is a candidate)
+  const float low = prefix > ordered(-INFINITY) ? unordered(prefix) : -INFINITY;
+  // the magnitude that records near the bound are off in proportion to
+  const float off =
+      p.slack * fmaxf(whole.top < INFINITY ? whole.top : 0.f, low > -INFINITY ? fabsf(low) : 0.f) + 1e-43f;
   float reach = low - 2.f * off;
+  const bool want_target = tgt >= 0 && tgt < p.V && p.out.logp != nullptr;
   // words of a unit that are still in the running
   auto words_of = [&](int c, float2 q) {
     if (!(q.x >= reach)) return 0;
-    return !kDense && q.y >= reach ? min(32, p.V - 32 * c) : 1;
+    if (kDense) return 1;
+    if (reach == -INFINITY) return min(32, p.V - 32 * c);  // (also words whose logit is -infinity, which records leave out)
+    if (!(q.y >= reach)) return 1;
+    return p.rec3[base + c] >= reach ? min(32, p.V - 32 * c) : 2;
   };
   auto put = [&](int at, int c, float2 q, int n) {
-    if constexpr (kDense) {
+    if (kDense) {
       word[at] = c;
-    } else if (q.y >= reach) {
+      near[at] = q.x;
+    } else if (n > 2 || reach == -INFINITY) {
       for (int e = 0; e < n; ++e) word[at + e] = 32 * c + e;
     } else {
       word[at] = 32 * c + 31 - static_cast<int>(__float_as_uint(q.x) & 31u);
+      near[at] = q.x;
+      if (n == 2) {
+        word[at + 1] = 32 * c + 31 - static_cast<int>(__float_as_uint(q.y) & 31u);
+        near[at + 1] = q.y;
+      }
     }
   };
   // the logits of the words [from, total) (and, the first time, of the target),
   // then the best K of all in order at the list's front
+  constexpr int PER = (SELECT_CAP + T - 1) / T;
   auto settle = [&](int from, int total) {
-    const int extra = from == 0 && want_target ? 1 : 0;
-    for (int e = from + warp; e < total + extra; e += T / 32) {
-      const long long v = e < total ? word[e] : tgt;
-      const float2 z = exact_dot(h, p.W + v * p.H, p.H, lane);
-      if (lane == 0) (e < total ? val[e] : target_z) = z;
+    const int end = total + (from == 0 && want_target ? 1 : 0);
+    for (int e = from + 2 * warp; e < end; e += 2 * (T / 32)) {
+      const long long v0 = e < total ? word[e] : tgt;
+      const long long v1 = e + 1 < total ? word[e + 1] : e + 1 < end ? tgt : v0;
+      const uint16_t* const w[2] = {p.W + v0 * p.H, p.W + v1 * p.H};
+      float2 z[2];
+      exact_dots<2>(h, w, p.H, lane, z);
+      if (lane < 2 && e + lane < end) (e + lane < total ? val[e + lane] : target_z) = lane == 0 ? z[0] : z[1];
     }
     __syncthreads();
-    constexpr int PER = (SELECT_CAP + T - 1) / T;
     float2 v[PER];
     int w[PER], place[PER];
 #pragma unroll
@@ -342,6 +372,7 @@ __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__
         v[q] = val[e];
         w[q] = word[e];
         int before = 0;
+#pragma unroll 4
         for (int o = 0; o < total; ++o) before += word_before(val[o], word[o], v[q], w[q]) ? 1 : 0;
         place[q] = before;
       }
@@ -362,11 +393,43 @@ __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__
     if (n > 0) {
       const int at = atomicAdd(&found, n);  // (the order within the list does not matter)
       if (at <= SELECT_CAP - n) put(at, c, q, n);
+      if (n > 2 || (!kDense && reach == -INFINITY)) whole_chunks = 1;
     }
   }
   __syncthreads();
-  if (found <= SELECT_CAP) {
-    settle(0, found);
+  int listed = found;
+  if (listed <= SELECT_CAP) {
+    // the better bound (words of whole chunks have no record of their own)
+    if (listed > K && whole_chunks == 0) {
+      if (t < 4) near[listed + t] = -INFINITY;
+      __syncthreads();
+      float m[PER];
+      int w[PER];
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int e = t + q * T;
+        m[q] = -INFINITY;
+        if (e < listed) {
+          m[q] = near[e];
+          w[q] = word[e];
+          int above = 0, equal = 0;
+          for (int o = 0; o < listed; o += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(near + o);
+            above += (x.x > m[q]) + (x.y > m[q]) + (x.z > m[q]) + (x.w > m[q]);
+            equal += (x.x == m[q]) + (x.y == m[q]) + (x.z == m[q]) + (x.w == m[q]);
+          }
+          if (above < K && above + equal >= K) best_k = m[q];  // (one value, whoever writes it)
+        }
+      }
+      __syncthreads();
+      const float again = best_k - 2.f * off;
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if (t + q * T < listed && m[q] >= again) word[atomicAdd(&kept_words, 1)] = w[q];
+      __syncthreads();
+      listed = kept_words;
+    }
+    settle(0, listed);
   } else {
     // kept: words at the list's front that are settled; total: those in the list
     int kept = 0, total = 0;
@@ -399,7 +462,7 @@ __global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__
       }
     }
   }
-  // (the list holds K words at least: K chunks reach the bound, or there is none and all V do)
+  // (the list holds K words at least: K records reach the bound, or there is none and all V words do)
   for (int e = t; e <= K; e += T) {
     if (e == K && !want_target) break;
     const float z = e < K ? val[e].x : target_z.x;
@@ -529,21 +592,28 @@ __global__ void __launch_bounds__(SMALL_THREADS) score_dlogits_kernel(const __gr
 
 // Chunk records of N rows of logits (the few-row forward's), a warp to a chunk.
 __global__ void __launch_bounds__(SMALL_THREADS)
-    score_record_kernel(const float* z, int N, int V, int ldz, float2* rec, int ld) {
+    score_record_kernel(const float* z, int N, int V, int ldz, float2* rec, float* rec3, int ld) {
   dependent_start();
   const int chunks = (V + 31) / 32, lane = threadIdx.x & 31;
   const long long u = static_cast<long long>(blockIdx.x) * (SMALL_THREADS / 32) + (threadIdx.x >> 5);
   if (u >= static_cast<long long>(N) * chunks) return;
   const int r = static_cast<int>(u / chunks), c = static_cast<int>(u - static_cast<long long>(r) * chunks);
   const int v = 32 * c + lane;
-  float m1 = v < V ? score_key(z[static_cast<long long>(r) * ldz + v], lane) : -INFINITY, m2 = -INFINITY;
+  float m1 = v < V ? score_key(z[static_cast<long long>(r) * ldz + v], lane) : -INFINITY;
+  float m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    const float a = __shfl_xor_sync(0xffffffffu, m1, off), b = __shfl_xor_sync(0xffffffffu, m2, off);
+    const float a = __shfl_xor_sync(0xffffffffu, m1, off), b = __shfl_xor_sync(0xffffffffu, m2, off),
+                d = __shfl_xor_sync(0xffffffffu, m3, off);
+    // of two descending triples
+    m3 = fmaxf(fmaxf(m3, d), fmaxf(fminf(m1, b), fminf(m2, a)));
     m2 = fmaxf(fmaxf(m2, b), fminf(m1, a));
     m1 = fmaxf(m1, a);
   }
-  if (lane == 0) rec[static_cast<long long>(r) * ld + c] = make_float2(m1, m2);
+  if (lane == 0) {
+    rec[static_cast<long long>(r) * ld + c] = make_float2(m1, m2);
+    rec3[static_cast<long long>(r) * ld + c] = m3;
+  }
 }
 
 // The forward of at most TOPK_GEMV_ROWS rows, as topk_gemv_kernel (a warp takes 4

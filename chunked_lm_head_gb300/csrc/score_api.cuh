@@ -5,11 +5,11 @@
 
 namespace {
 
-// Words from the logits themselves, or from chunk records.  A chunk that two of
+// Words from the logits themselves, or from chunk records.  A chunk that three of
 // the K words share costs 32 products, so the records serve while chunks are
-// many: about K^2 / 2 / chunks of them are shared.  Below 8 K chunks the logits
-// are kept, at 4 bytes instead of 1/4 byte a column.
-bool score_dense(int64_t V, int64_t k) { return ceil_div(V, 32) < 8 * k; }
+// many: about K^3 / 6 / chunks^2 of them are shared.  Below 4 K chunks (K / 96
+// shared ones) the logits are held, at 4 bytes instead of 3/8 byte a column.
+bool score_dense(int64_t V, int64_t k) { return ceil_div(V, 32) < 4 * k; }
 
 constexpr size_t kScoreBlockBytes = size_t(256) << 20;  // of records or logits held at once
 
@@ -74,7 +74,7 @@ ScorePlan score_plan(int64_t N, int64_t H, int64_t V, int64_t k, bool keep, int 
   q.ld = k == 0 ? 0 : q.dense ? round_up(V, BN) : round_up(V, BN) / 32;
   q.rows = keep ? std::max<int64_t>(N, 1) : fwd_block_rows(N, tm);
   if (k > 0 && !q.gemv) {
-    const long long fit = static_cast<long long>(kScoreBlockBytes / (static_cast<size_t>(q.ld) * (q.dense ? 4 : 8)));
+    const long long fit = static_cast<long long>(kScoreBlockBytes / (static_cast<size_t>(q.ld) * (q.dense ? 4 : 12)));
     q.rows = std::min(q.rows, std::max<long long>(tm, fit / tm * tm));
   }
   // (a row has kScoreParts partials of 16 bytes to a split: four times the 8 that the cap counts)
@@ -84,7 +84,7 @@ ScorePlan score_plan(int64_t N, int64_t H, int64_t V, int64_t k, bool keep, int 
 }
 
 struct ScoreLayout {
-  size_t zt = 0, part = 0, z = 0, rec = 0, bad = 0, idx = 0, blk = 0, count = 0, hc = 0, total = 0;
+  size_t zt = 0, part = 0, z = 0, rec = 0, rec3 = 0, bad = 0, idx = 0, blk = 0, count = 0, hc = 0, total = 0;
 };
 ScoreLayout score_layout(int64_t N, int64_t H, int64_t V, int64_t k, const ScorePlan& q) {
   ScoreLayout L;
@@ -99,6 +99,7 @@ ScoreLayout score_layout(int64_t N, int64_t H, int64_t V, int64_t k, const Score
   L.part = take(rows * q.S * 16);
   L.z = take(k > 0 && (q.dense || q.gemv) ? rows * round_up(V, BN) * 4 : 0);
   L.rec = take(k > 0 && !q.dense ? rows * q.ld * 8 : 0);
+  L.rec3 = take(k > 0 && !q.dense ? rows * q.ld * 4 : 0);
   L.bad = take(256);
   if (q.keep ? N > kKeepCompactRows : !q.gemv && N >= skip_min_rows()) {
     L.idx = take(n * 4);
@@ -120,7 +121,7 @@ float score_slack(int64_t H) {
 }
 
 flce_status score_rows(const ScorePlan& q, bool kLong, const ScoreRows& rows, const float4* part, const float2* rec,
-                       const float* z, const flce_bf16* h, const flce_bf16* W, const GemmParams& tf,
+                       const float* rec3, const float* z, const flce_bf16* h, const flce_bf16* W, const GemmParams& tf,
                        const int64_t* targets, long long ignore, const float* zt, const ScoreOut& out,
                        cudaStream_t st) {
   ProfScope ps(K_SCORE, st);
@@ -137,6 +138,7 @@ flce_status score_rows(const ScorePlan& q, bool kLong, const ScoreRows& rows, co
   p.W = W;
   p.part = part;
   p.rec = rec;
+  p.rec3 = rec3;
   p.z = z;
   p.S = q.S;
   p.ld = static_cast<int>(q.ld);
@@ -158,14 +160,14 @@ flce_status score_rows(const ScorePlan& q, bool kLong, const ScoreRows& rows, co
   auto of = [&](auto dense) -> cudaError_t {
     constexpr bool D = decltype(dense)::value;
     if (kLong) return go(score_select_kernel<256, D, true>, 256);
-    return few ? go(score_select_kernel<1024, D, false>, 1024) : go(score_select_kernel<256, D, false>, 256);
+    return few ? go(score_select_kernel<512, D, false>, 512) : go(score_select_kernel<256, D, false>, 256);
   };
   FLCE_CUDA_TRY(q.dense ? of(std::true_type{}) : of(std::false_type{}));
   return FLCE_OK;
 }
 
 flce_status score_gemv(const ScorePlan& q, const GemmParams& p, const flce_bf16* h, const flce_bf16* W, float* z,
-                       float2* rec, const int64_t* targets, float* zt, float4* part, cudaStream_t st) {
+                       float2* rec, float* rec3, const int64_t* targets, float* zt, float4* part, cudaStream_t st) {
   const int ldz = static_cast<int>(round_up(p.V, BN));
   {
     ProfScope ps(K_FWD, st);
@@ -186,7 +188,7 @@ flce_status score_gemv(const ScorePlan& q, const GemmParams& p, const flce_bf16*
   const long long units = static_cast<long long>(p.N) * ceil_div(p.V, 32);
   FLCE_CUDA_TRY(launch_dependent(score_record_kernel, dim3(static_cast<unsigned>(ceil_div(units, SMALL_THREADS / 32))),
                                  SMALL_THREADS, 0, st, static_cast<const float*>(z), p.N, p.V, ldz, rec,
-                                 static_cast<int>(q.ld)));
+                                 rec3, static_cast<int>(q.ld)));
   return FLCE_OK;
 }
 
@@ -242,6 +244,7 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
   float4* part = reinterpret_cast<float4*>(wb + L.part);
   float* z = k > 0 && (q.dense || q.gemv) ? reinterpret_cast<float*>(wb + L.z) : nullptr;
   float2* rec = k > 0 && !q.dense ? reinterpret_cast<float2*>(wb + L.rec) : nullptr;
+  float* rec3 = k > 0 && !q.dense ? reinterpret_cast<float*>(wb + L.rec3) : nullptr;
   const int Ni = static_cast<int>(N);
   if (targets != nullptr && validate_on()) {
     int* bad = reinterpret_cast<int*>(wb + L.bad);
@@ -275,13 +278,14 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
   p.tf_d = tfp.tf_d;
   p.score_part = part;
   p.rec = rec;
+  p.rec3 = rec3;
   p.z = q.dense ? z : nullptr;
   p.rec_ld = static_cast<int>(q.ld);
   if (q.gemv) {
-    s = score_gemv(q, p, h, W, z, rec, targets, zt, part, st);
+    s = score_gemv(q, p, h, W, z, rec, rec3, targets, zt, part, st);
     if (s != FLCE_OK) return s;
-    return score_rows(q, kLong, ScoreRows{0, Ni, nullptr, nullptr, 0}, part, rec, z, h, W, p, targets, ignore_index, zt,
-                      out, st);
+    return score_rows(q, kLong, ScoreRows{0, Ni, nullptr, nullptr, 0}, part, rec, rec3, z, h, W, p, targets,
+                      ignore_index, zt, out, st);
   }
   // the rows without a target to score are left out, as flce_forward_ex2 does
   const bool skip = targets != nullptr && (keep || compact_on()) && L.hc != 0;
@@ -335,7 +339,7 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
                     : k > 0 ? (launch_scored<MODE_FWD, SCORE_TOP>(cg, kLong, tA, tB, tB, g, w, st))
                             : (launch_scored<MODE_FWD, SCORE_ENTROPY>(cg, kLong, tA, tB, tB, g, w, st)));
     }
-    s = score_rows(q, kLong, rows, part, rec, z, h, W, p, targets, ignore_index, zt, out, st);
+    s = score_rows(q, kLong, rows, part, rec, rec3, z, h, W, p, targets, ignore_index, zt, out, st);
     if (s != FLCE_OK) return s;
   }
   return FLCE_OK;

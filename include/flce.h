@@ -761,8 +761,8 @@ FLCE_API size_t flce_layer_norm_backward_workspace_bytes(int64_t N, int64_t H);
  * A row with a logit z that is NaN or +infinity (with a soft-cap, any infinity),
  * or none above -infinity: NaN, ids of -1.  N <= 2^31 - 65,537.  Workspace:
  * flce_score_workspace_bytes(N, H, V, k), or NULL (stream-ordered allocation); it
- * holds at most about 256 MB of the rows' chunk maxima (or, where V < 256 k,
- * logits) at once.
+ * holds at most about 256 MB of the rows' largest logits of every 32 (or, where
+ * V < 128 k, all logits) at once.
  */
 FLCE_API flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* targets, int64_t N,
                                 int64_t H, int64_t V, int64_t k, int64_t ignore_index,
