@@ -49,10 +49,11 @@ __device__ __forceinline__ void layer_affine(const LayerParams& p, int c, float2
 }
 
 // One row on a group of T threads, VPT vectors of 8 elements to a thread in
-// registers (H <= 8 T VPT): the row is read once.
+// registers as the stream is stored (H <= 8 T VPT): the row is read once.
 template <class R, int VPT, int MAXT, int CTAS>
 __global__ void __launch_bounds__(MAXT, CTAS) layer_norm_kernel(const __grid_constant__ LayerParams p) {
   constexpr bool kRes = !std::is_same<R, NoResidual>::value;
+  constexpr bool kWide = std::is_same<R, float>::value;
   __shared__ float red[kNormGroups][64];
   const int T = p.T;
   const int group = threadIdx.x / T, t = threadIdx.x - group * T;
@@ -61,32 +62,32 @@ __global__ void __launch_bounds__(MAXT, CTAS) layer_norm_kernel(const __grid_con
   const int nv = p.H / 8;
   const uint16_t* x = p.x + row * p.ldx;
   const long long o = static_cast<long long>(row) * p.H;
-  float2 v[VPT][4];
+  Raw8<typename std::conditional<kWide, float, uint16_t>::type> s[VPT];
   float2 sum2 = both(0.f);
   {
-    Raw8<uint16_t> xr[VPT];
-    Raw8<typename std::conditional<kRes, R, uint16_t>::type> rr[VPT];
+    Raw8<uint16_t> xr[kRes ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (t + i * T) * 8;
       if (t + i * T < nv) {
-        xr[i].load(x + c);
-        if constexpr (kRes) rr[i].load(static_cast<const R*>(p.r) + row * p.ldr + c);
+        if constexpr (kRes) {
+          xr[i].load(x + c);
+          s[i].load(static_cast<const R*>(p.r) + row * p.ldr + c);
+        } else {
+          s[i].load(x + c);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (t + i * T) * 8;
       if (t + i * T < nv) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[i][k] = xr[i].pair(k);
         if constexpr (kRes) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[i][k] = add2(v[i][k], rr[i].pair(k));
-          store8(static_cast<R*>(p.s) + o + c, v[i]);
+          s[i].add(xr[i]);
+          s[i].store(static_cast<R*>(p.s) + o + c);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum2 = add2(sum2, v[i][k]);
+        for (int k = 0; k < 4; ++k) sum2 = add2(sum2, s[i].pair(k));
       }
     }
   }
@@ -99,8 +100,8 @@ __global__ void __launch_bounds__(MAXT, CTAS) layer_norm_kernel(const __grid_con
     if (t + i * T < nv) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        v[i][k] = add2(v[i][k], both(-mean));
-        sum2 = fma2(v[i][k], v[i][k], sum2);
+        const float2 d = add2(s[i].pair(k), both(-mean));
+        sum2 = fma2(d, d, sum2);
       }
     }
   sum = sum2.x + sum2.y;
@@ -114,10 +115,11 @@ __global__ void __launch_bounds__(MAXT, CTAS) layer_norm_kernel(const __grid_con
   for (int i = 0; i < VPT; ++i) {
     const int c = (t + i * T) * 8;
     if (t + i * T < nv) {
+      float2 v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[i][k] = mul2(v[i][k], both(rstd));
-      layer_affine(p, c, v[i]);
-      store8(p.y + o + c, v[i]);
+      for (int k = 0; k < 4; ++k) v[k] = mul2(add2(s[i].pair(k), both(-mean)), both(rstd));
+      layer_affine(p, c, v);
+      store8(p.y + o + c, v);
     }
   }
 }

@@ -22,6 +22,9 @@ cudaError_t launch_layer_warps(const LayerParams& p, cudaStream_t st) {
 
 // The shapes of launch_norm_as: a warp to a row where the row fits its
 // registers, else groups of two vectors to a thread, past 8,192 elements four.
+// Three CTAs of 512 threads to an SM with a bf16 stream (16,384 x 4,096 with a
+// residual 88 us, 16,384 x 6,144 126: two CTAs 105 and 135, four 90 and 131), two
+// with fp32 (125 us; three 127, four 135).
 template <class R>
 cudaError_t launch_layer_as(const LayerParams& p, cudaStream_t st) {
   constexpr bool kRes = !std::is_same<R, NoResidual>::value;
@@ -35,29 +38,41 @@ cudaError_t launch_layer_as(const LayerParams& p, cudaStream_t st) {
     if (p.H <= 2560) return launch_layer_warps<false, 10, 3>(p, st);
     if (p.H <= 4096) return launch_layer_warps<false, 16, 2>(p, st);
   }
-  if (p.H <= 8192) return launch_layer_groups<R, 2, 512, kRes ? 2 : 3>(p, st);
+  if (p.H <= 8192) return launch_layer_groups<R, 2, 512, std::is_same<R, float>::value ? 2 : 3>(p, st);
   if (p.H <= 16384) return launch_layer_groups<R, 4, 512, 2>(p, st);
   return launch_layer_groups<R, 4, 1024, 1>(p, st);
 }
 
-// How the backward runs rows of H (as norm_bwd_shape): one vector to a thread up
-// to 8,192 elements, one CTA of about 1,024 threads.
-NormBwdShape layer_bwd_shape(int64_t N, int64_t H) {
+// How the backward runs rows of H.  A row's latency (its loads, a reduction, its
+// stores) sets the pace, so as many rows as fit are worked on at once, the next
+// two's loads in flight.
+//   bf16 stream, H <= 8,192: two vectors to a thread (a thread's dweight and dbias
+//   take 32 registers), one CTA of up to 640 threads, three rows deep.  us with and
+//   without the dbias (none: no residual):
+//                          640 x 3   640 x 2   896 x 2   one vector, 1,024   two CTAs of 320
+//     16,384 x 4,096       93 / 90   94 / 94   195 / 90      98 / 94             99 / 94
+//     131,072 x 2,560 none 340 / 315 341 / 320 655 / 342     401 / 373           369 / 336
+//     16,384 x 6,144       139       148       295           156                 152
+//   fp32 stream: one vector, 1,024 threads, straight from global memory, whose
+//   second read hits L1 (16,384 x 4,096: 197 us; two vectors 238).
+//   Past 8,192 elements one row to a CTA (4,096 x 12,288: 111 us).
+// Floors of these: 79, 297 (131,072 rows), 119, 158 (fp32) and 59 us.
+NormBwdShape layer_bwd_shape(int64_t N, int64_t H, bool f32) {
   NormBwdShape b;
-  b.vpt = H <= 8192 ? 1 : H <= 16384 ? 2 : 4;
+  b.vpt = f32 ? (H <= 8192 ? 1 : 4) : (H <= 8192 ? 2 : 4);
   b.T = norm_group(H, b.vpt);
-  b.groups = norm_groups(b.T, 1024);
+  b.groups = norm_groups(b.T, b.vpt == 1 ? 1024 : b.vpt == 2 ? 640 : 512);
   b.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(N, b.groups), device_sms())));
   return b;
 }
 
-template <class S, bool kBias, int VPT, int DEPTH>
+template <class S, bool kBias, int VPT, int DEPTH, int MAXT, int CTAS>
 cudaError_t launch_layer_bwd_as(const LayerBwdParams& p, const NormBwdShape& b, cudaStream_t st) {
   const int threads = b.groups * b.T;
   const size_t stage = static_cast<size_t>(threads) * VPT * 8 * (2 + (p.up ? 2 : 1) * sizeof(S));
   const size_t smem =
       std::max(DEPTH * stage, p.part_w || p.part_b ? static_cast<size_t>(b.groups - 1) * p.H * 4 : 0);
-  auto kern = layer_norm_bwd_kernel<S, kBias, VPT, DEPTH, 1024, 1>;
+  auto kern = layer_norm_bwd_kernel<S, kBias, VPT, DEPTH, MAXT, CTAS>;
   if (smem > 32768) {  // (the kernel has 8 KB of its own beside it)
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 204800);
     if (e != cudaSuccess) return e;
@@ -68,10 +83,16 @@ cudaError_t launch_layer_bwd_as(const LayerBwdParams& p, const NormBwdShape& b, 
 
 template <class S, bool kBias>
 cudaError_t launch_layer_bwd(const LayerBwdParams& p, const NormBwdShape& b, cudaStream_t st) {
-  constexpr bool f32 = std::is_same<S, float>::value;
-  if (b.vpt == 1) return launch_layer_bwd_as<S, kBias, 1, f32 ? 0 : 2>(p, b, st);
-  if (b.vpt == 2) return launch_layer_bwd_as<S, kBias, 2, f32 ? 0 : 1>(p, b, st);
-  return launch_layer_bwd_as<S, kBias, 4, 0>(p, b, st);
+  if constexpr (std::is_same<S, float>::value) {
+    if (b.vpt == 1) return launch_layer_bwd_as<S, kBias, 1, 0, 1024, 1>(p, b, st);
+    return launch_layer_bwd_as<S, kBias, 4, 0, 1024, 1>(p, b, st);
+  } else {
+    if (b.vpt == 2)
+      return b.groups * b.T <= 512 ? launch_layer_bwd_as<S, kBias, 2, 3, 512, 1>(p, b, st)
+                                   : launch_layer_bwd_as<S, kBias, 2, 3, 640, 1>(p, b, st);
+    return b.T <= 512 ? launch_layer_bwd_as<S, kBias, 4, 1, 512, 1>(p, b, st)
+                      : launch_layer_bwd_as<S, kBias, 4, 0, 1024, 1>(p, b, st);
+  }
 }
 
 }  // namespace
@@ -119,7 +140,9 @@ flce_status flce_layer_norm(const flce_bf16* x, int64_t ldx, const void* residua
 
 size_t flce_layer_norm_backward_workspace_bytes(int64_t N, int64_t H) {
   if (!norm_sizes_ok(N, H)) return 0;
-  return 2 * align256(static_cast<size_t>(layer_bwd_shape(N, H).ctas) * H * 4);
+  // of either stream type
+  const int ctas = std::max(layer_bwd_shape(N, H, false).ctas, layer_bwd_shape(N, H, true).ctas);
+  return 2 * align256(static_cast<size_t>(ctas) * H * 4);
 }
 
 flce_status flce_layer_norm_backward(const flce_bf16* dy, const void* s, int64_t lds, int32_t s_type,
@@ -142,8 +165,8 @@ flce_status flce_layer_norm_backward(const flce_bf16* dy, const void* s, int64_t
     if (dbias) FLCE_CUDA_TRY(cudaMemsetAsync(dbias, 0, param, st));
     return FLCE_OK;
   }
-  const NormBwdShape b = layer_bwd_shape(N, H);
-  const size_t part = align256(static_cast<size_t>(b.ctas) * H * 4);
+  const NormBwdShape b = layer_bwd_shape(N, H, s_type == FLCE_F32);
+  const size_t part = flce_layer_norm_backward_workspace_bytes(N, H) / 2;
   Workspace ws;
   if (dweight || dbias) {
     const flce_status g = get_workspace(ws, workspace, workspace_bytes, 2 * part, st);

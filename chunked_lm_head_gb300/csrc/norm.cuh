@@ -39,6 +39,30 @@ struct Raw8 {
 #pragma unroll
     for (int k = 0; k < kQuads; ++k) q[k] = make_uint4(0u, 0u, 0u, 0u);
   }
+  // + o, rounded to the element type
+  __device__ __forceinline__ void add(const Raw8<uint16_t>& o) {
+    if constexpr (sizeof(S) == 4) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = add2(pair(k), o.pair(k));
+        uint32_t* w = &q[k / 2].x + 2 * (k % 2);
+        w[0] = __float_as_uint(v.x);
+        w[1] = __float_as_uint(v.y);
+      }
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = add2(pair(k), o.pair(k));
+        w[k] = pack_bf16x2(v.x, v.y);
+      }
+      q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ void store(S* p) const {
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) reinterpret_cast<uint4*>(p)[k] = q[k];
+  }
   __device__ __forceinline__ float2 pair(int k) const {
     if constexpr (sizeof(S) == 4) {
       const uint32_t w[4] = {q[k / 2].x, q[k / 2].y, q[k / 2].z, q[k / 2].w};

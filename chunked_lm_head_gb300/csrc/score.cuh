@@ -263,8 +263,11 @@ struct SelectParams {
 constexpr int SELECT_CAP = 1024;  // words of the list
 static_assert(SELECT_CAP >= SCORE_MAX_K + 32, "the list holds K words and a chunk");
 
+// Bound by the gather of the words' rows and its latency: 64 words of 4,096 rows,
+// 2.2 GB of a 1.24 GB head, take 490 us (three CTAs to an SM; two 580, four with
+// half the loads in flight 560).
 template <int T, bool kDense, bool kLong>
-__global__ void __launch_bounds__(T) score_select_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(T, T == 256 ? 3 : 1) score_select_kernel(const __grid_constant__ SelectParams p) {
   static_assert(T >= SCORE_MAX_K, "K threads have a largest record each");
   dependent_start();
   using idx_t = typename std::conditional<kLong, long long, int>::type;

@@ -11,32 +11,39 @@ import torch
 from . import _lib
 from .api import _first_order
 from .norm import _TYPES, _check, _rows_of
-from .score import _on
+from .score import _elsewhere
 
 
 def _check_all(x, weight, bias, residual):
     ld = _check(x, weight, residual)
     if bias is not None and (bias.dtype != weight.dtype or bias.shape != weight.shape or not bias.is_contiguous()):
         raise ValueError("bias must be contiguous, of weight's shape and type")
-    if any(t is not None and t.device != x.device for t in (weight, bias, residual)):
+    dev = x.get_device()
+    if weight.get_device() != dev or (bias is not None and bias.get_device() != dev) or (
+            residual is not None and residual.get_device() != dev):
         raise ValueError("x, weight, bias and residual must be on one device")
     return ld
 
 
 def _norm(x, weight, bias, residual, eps, weight_offset, need_stats, stream):
-    """(y, stream or None, mean or None, rstd or None)"""
+    """(y, stream or None, stats): stats [2,N] the rows' mean and rstd, or None."""
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return _norm(x, weight, bias, residual, eps, weight_offset, need_stats, stream)
     ldx, ldr = _check_all(x, weight, bias, residual)
     N, H = x.shape
-    with _on(x):
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)  # also for rows out of a wider buffer
-        s = None if residual is None else torch.empty_like(residual, memory_format=torch.contiguous_format)
-        mean = rstd = None
-        if need_stats:
-            mean, rstd = torch.empty((2, N), dtype=torch.float32, device=x.device).unbind(0)
-        _lib.check("flce_layer_norm", _lib.flce_layer_norm(
-            x, ldx, residual, ldr, 0 if residual is None else _TYPES[residual.dtype], weight, bias, _TYPES[weight.dtype],
-            weight_offset, eps, N, H, y, s, mean, rstd, stream))
-    return y, s, mean, rstd
+    y = torch.empty_like(x)  # contiguous, also for rows out of a wider buffer
+    s = None if residual is None else torch.empty_like(residual)
+    stats = mean = rstd = None
+    if need_stats:
+        stats = torch.empty((2, N), dtype=torch.float32, device=x.device)
+        if N:
+            mean = stats.data_ptr()
+            rstd = mean + 4 * N
+    _lib.check("flce_layer_norm", _lib.flce_layer_norm(
+        x, ldx, residual, ldr, 0 if residual is None else _TYPES[residual.dtype], weight, bias, _TYPES[weight.dtype],
+        weight_offset, eps, N, H, y, s, mean, rstd, stream))
+    return y, s, stats
 
 
 def layer_norm_forward(x, weight, bias=None, residual=None, eps: float = 1e-5, weight_offset: float = 0.0, stream=None,
@@ -44,30 +51,32 @@ def layer_norm_forward(x, weight, bias=None, residual=None, eps: float = 1e-5, w
     """dict(y[N,H] bf16, residual[N,H] or None, mean[N], rstd[N] f32 or None) on
     device.  The stream s = round(x + residual) comes back as ``residual``, in the
     residual's type; y = (s - mean) rstd (weight + weight_offset) + bias."""
-    y, s, mean, rstd = _norm(x, weight, bias, residual, eps, weight_offset, need_stats, stream)
+    y, s, stats = _norm(x, weight, bias, residual, eps, weight_offset, need_stats, stream)
+    mean, rstd = (None, None) if stats is None else stats.unbind(0)
     return {"y": y, "residual": s, "mean": mean, "rstd": rstd}
 
 
 def _norm_grads(dy, s, lds, weight, mean, rstd, ds, weight_offset, need_dx, need_dr, need_dweight, need_dbias, workspace,
                 stream):
-    """(dx, dr, dweight, dbias) of checked tensors."""
+    """(dx, dr, dweight, dbias) of checked tensors on the current device."""
     N, H = s.shape
     wide = s.dtype == torch.float32
-    with _on(s):
-        dx = torch.empty_like(dy) if need_dx or (need_dr and not wide) else None
-        dr = torch.empty_like(s, memory_format=torch.contiguous_format) if need_dr and wide else None
-        dw = torch.empty_like(weight) if need_dweight else None
-        db = torch.empty_like(weight) if need_dbias else None
-        if dx is None and dr is None and dw is None and db is None:
-            return None, None, None, None
-        if (need_dweight or need_dbias) and workspace is None and stream is None:
-            # torch's allocator keeps it for the next call
+    dx = torch.empty_like(dy) if need_dx or (need_dr and not wide) else None
+    dr = torch.empty_like(s, memory_format=torch.contiguous_format) if need_dr and wide else None
+    dw = torch.empty_like(weight) if need_dweight else None
+    db = torch.empty_like(weight) if need_dbias else None
+    ws_bytes = 0
+    if need_dweight or need_dbias:
+        if workspace is None and stream is None:  # torch's allocator keeps it for the next call
             workspace = torch.empty(_lib.flce_layer_norm_backward_workspace_bytes(N, H), dtype=torch.uint8,
                                     device=s.device)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _lib.check("flce_layer_norm_backward", _lib.flce_layer_norm_backward(
-            dy, s, lds, _TYPES[s.dtype], ds, weight, _TYPES[weight.dtype], weight_offset, mean, rstd, N, H, dx, dr, dw, db,
-            workspace, ws_bytes, stream))
+        if workspace is not None:
+            ws_bytes = workspace.numel() * workspace.element_size()
+    elif dx is None and dr is None:
+        return None, None, None, None
+    _lib.check("flce_layer_norm_backward", _lib.flce_layer_norm_backward(
+        dy, s, lds, _TYPES[s.dtype], ds, weight, _TYPES[weight.dtype], weight_offset, mean, rstd, N, H, dx, dr, dw, db,
+        workspace, ws_bytes, stream))
     return dx if need_dx else None, (dr if wide else dx) if need_dr else None, dw, db
 
 
@@ -89,6 +98,10 @@ def layer_norm_backward(dy, s, weight, mean, rstd, ds=None, weight_offset: float
         raise ValueError("ds must be a contiguous CUDA tensor of s's shape and type")
     if workspace is not None and workspace.device != s.device:
         raise ValueError("workspace must be a CUDA tensor")
+    if _elsewhere(s):
+        with torch.cuda.device(s.device):
+            return layer_norm_backward(dy, s, weight, mean, rstd, ds, weight_offset, need_dx, need_dr, need_dweight,
+                                       need_dbias, workspace, stream)
     return _norm_grads(dy, s, lds, weight, mean, rstd, ds, weight_offset, need_dx, need_dr, need_dweight, need_dbias,
                        workspace, stream)
 
@@ -99,23 +112,26 @@ class LayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, eps, weight_offset):
         ctx.set_materialize_grads(False)
-        y, s, mean, rstd = _norm(x, weight, bias, residual, eps, weight_offset, True, None)
-        ctx.save_for_backward(x if s is None else s, weight, mean, rstd)
+        y, s, stats = _norm(x, weight, bias, residual, eps, weight_offset, True, None)
+        ctx.save_for_backward(x if s is None else s, weight, stats)
         ctx.weight_offset = weight_offset
         return y if s is None else (y, s)
 
     @staticmethod
     def backward(ctx, dy, ds=None):
-        s, weight, mean, rstd = ctx.saved_tensors
+        s, weight, stats = ctx.saved_tensors
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
         if dy is None:  # only the stream was used
             if ds is None:
                 return (None,) * 6
             return ds.to(torch.bfloat16) if need_x else None, None, None, ds if need_r else None, None, None
-        dx, dr, dw, db = _norm_grads(_rows_of(dy.detach()), s.detach(), s.stride(0) if s.shape[0] > 1 else s.shape[1],
-                                     weight.detach(), mean, rstd, None if ds is None else _rows_of(ds.detach()),
-                                     ctx.weight_offset, need_x, need_r, need_w, need_b, None, None)
-        dx, dw, db, dr = _first_order((dx, dw, db, dr), (s, weight, dy, ds))
+        N, H = s.shape
+        mean = stats.data_ptr() if N else None  # (the backward runs on the device of its tensors)
+        dx, dr, dw, db = _norm_grads(_rows_of(dy), s, s.stride(0) if N > 1 else H, weight, mean, mean and mean + 4 * N,
+                                     None if ds is None else _rows_of(ds), ctx.weight_offset, need_x, need_r, need_w,
+                                     need_b, None, None)
+        if torch.is_grad_enabled():
+            dx, dw, db, dr = _first_order((dx, dw, db, dr), (s, weight, dy, ds))
         return dx, dw, db, dr, None, None
 
 
@@ -124,9 +140,11 @@ def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, weight_of
     residual's type, y = (s - mean(s)) (var(s) + eps)^(-1/2) (weight +
     weight_offset) + bias in bf16.  x [N,H] bf16; residual [N,H] bf16 or fp32;
     weight and bias [H] of one type, bf16 or fp32; differentiable in all four."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias, residual)):
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or
+                                    (bias is not None and bias.requires_grad) or
+                                    (residual is not None and residual.requires_grad)):
         return LayerNormFunction.apply(x, weight, bias, residual, eps, weight_offset)
-    y, s, _, _ = _norm(x, weight, bias, residual, eps, weight_offset, False, None)
+    y, s, _ = _norm(x, weight, bias, residual, eps, weight_offset, False, None)
     return y if s is None else (y, s)
 
 

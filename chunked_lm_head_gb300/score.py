@@ -9,8 +9,6 @@ tensor properties, allocates outputs and passes pointers.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _lib
@@ -18,25 +16,26 @@ from .api import IGNORE_INDEX, _first_order
 from .topk import _DW, _workspace
 
 
-def _on(x):
-    """The device of x as the current one, for the length of a call."""
-    return contextlib.nullcontext() if x.device.index == torch.cuda.current_device() else torch.cuda.device(x.device)
+def _elsewhere(x):
+    """Whether x is on another CUDA device than the current one (whose streams and
+    launches a call would take)."""
+    return x.is_cuda and x.get_device() != torch._C._cuda_getDevice()
 
 
 def _check(h, W, targets):
     for x in (h, W):
         if not x.is_cuda or x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_contiguous():
             raise ValueError("h and W must be contiguous 2-D bfloat16 CUDA tensors")
-    if W.shape[1] != h.shape[1] or W.device != h.device:
+    if W.shape[1] != h.shape[1] or W.get_device() != h.get_device():
         raise ValueError("expected h[N,H] and W[V,H] on one device")
     if targets is not None and (targets.dtype != torch.int64 or targets.shape != (h.shape[0],) or
-                                targets.device != h.device or not targets.is_contiguous()):
+                                targets.get_device() != h.get_device() or not targets.is_contiguous()):
         raise ValueError("targets must be a contiguous int64 [N] tensor on h's device")
 
 
 def _row_vector(x, h, name):
-    if x is not None and (x.dtype != torch.float32 or x.shape != (h.shape[0],) or x.device != h.device or
-                          not x.is_contiguous()):
+    if x is not None and (x.dtype != torch.float32 or x.shape != (h.shape[0],) or
+                          x.get_device() != h.get_device() or not x.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous float32 [N] tensor on h's device")
 
 
@@ -61,18 +60,34 @@ def score_forward(h, W, targets=None, k: int = 0, ignore_index: int = IGNORE_IND
         raise ValueError("k must be between 0 and the vocabulary")
     if keep_rows and (k or targets is None):
         raise ValueError("keep_rows goes with targets and without words")
-    with _on(h):
-        lse = torch.empty(N, dtype=torch.float32, device=dev)
-        entropy = torch.empty_like(lse)
-        logp = None if targets is None else torch.empty_like(lse)
-        ids = torch.empty((N, k), dtype=torch.int64, device=dev) if k else None
-        words = torch.empty((N, k), dtype=torch.float32, device=dev) if k else None
-        nbytes = _lib.flce_score_state_bytes(N, H, V, keep_rows) if keep_rows else 0
-        state = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        ws, ws_bytes = _workspace(workspace, _lib.flce_score_workspace_bytes(N, H, V, k), stream, dev)
-        _lib.check("flce_score", _lib.flce_score(h, W, targets, N, H, V, k, ignore_index, transform, logp, lse, entropy,
-                                                 ids, words, state, ws, ws_bytes, stream))
+    if _elsewhere(h):
+        with torch.cuda.device(h.device):
+            return score_forward(h, W, targets, k, ignore_index, transform, workspace, stream, keep_rows)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
+    entropy = torch.empty_like(lse)
+    logp = None if targets is None else torch.empty_like(lse)
+    ids = torch.empty((N, k), dtype=torch.int64, device=dev) if k else None
+    words = torch.empty((N, k), dtype=torch.float32, device=dev) if k else None
+    nbytes = _lib.flce_score_state_bytes(N, H, V, keep_rows) if keep_rows else 0
+    state = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    ws, ws_bytes = _workspace(workspace, _lib.flce_score_workspace_bytes(N, H, V, k), stream, dev)
+    _lib.check("flce_score", _lib.flce_score(h, W, targets, N, H, V, k, ignore_index, transform, logp, lse, entropy, ids,
+                                             words, state, ws, ws_bytes, stream))
     return {"logp": logp, "lse": lse, "entropy": entropy, "ids": ids, "logprobs": words, "state": state}
+
+
+def _grads(h, W, targets, lse, entropy, grad_logp, grad_entropy, chunk_rows, ignore_index, transform, need_dH, need_dW,
+           workspace, stream, dW_dtype, state):
+    """score_backward of checked tensors on the current device."""
+    (N, H), V, dev = h.shape, W.shape[0], h.device
+    dH = torch.empty_like(h) if need_dH else None
+    dW = torch.empty((V, H), dtype=dW_dtype, device=dev) if need_dW else None
+    kind = _DW[dW_dtype]
+    ws, ws_bytes = _workspace(workspace, _lib.flce_score_backward_workspace_bytes(N, H, V, chunk_rows, kind), stream, dev)
+    _lib.check("flce_score_backward", _lib.flce_score_backward(
+        h, W, targets, lse, entropy, grad_logp, grad_entropy, state, dH, dW, kind, N, H, V, chunk_rows, ignore_index,
+        transform, ws, ws_bytes, stream))
+    return dH, dW
 
 
 def score_backward(h, W, targets, lse, entropy, grad_logp=None, grad_entropy=None, chunk_rows: int = 256,
@@ -95,15 +110,12 @@ def score_backward(h, W, targets, lse, entropy, grad_logp=None, grad_entropy=Non
         raise ValueError("state must come from score_forward of the same sizes")
     if state is not None:
         chunk_rows = max(chunk_rows, N)  # the kept rows are one block
-    with _on(h):
-        dH = torch.empty_like(h) if need_dH else None
-        dW = torch.empty((V, H), dtype=dW_dtype, device=dev) if need_dW else None
-        ws, ws_bytes = _workspace(workspace, _lib.flce_score_backward_workspace_bytes(N, H, V, chunk_rows, _DW[dW_dtype]),
-                                  stream, dev)
-        _lib.check("flce_score_backward", _lib.flce_score_backward(
-            h, W, targets, lse, entropy, grad_logp, grad_entropy, state, dH, dW, _DW[dW_dtype], N, H, V, chunk_rows,
-            ignore_index, transform, ws, ws_bytes, stream))
-    return dH, dW
+    if _elsewhere(h):
+        with torch.cuda.device(dev):
+            return score_backward(h, W, targets, lse, entropy, grad_logp, grad_entropy, chunk_rows, ignore_index,
+                                  transform, need_dH, need_dW, workspace, stream, dW_dtype, state)
+    return _grads(h, W, targets, lse, entropy, grad_logp, grad_entropy, chunk_rows, ignore_index, transform, need_dH,
+                  need_dW, workspace, stream, dW_dtype, state)
 
 
 class SelectiveLogSoftmaxEntropy(torch.autograd.Function):
@@ -124,10 +136,14 @@ class SelectiveLogSoftmaxEntropy(torch.autograd.Function):
         if (grad_logp is None and grad_entropy is None) or not (need_h or need_W):
             return (None,) * 7
         h, W, targets, lse, entropy, state = ctx.saved_tensors
-        ga, ge = (None if g is None else g.detach().to(torch.float32).contiguous() for g in (grad_logp, grad_entropy))
-        dH, dW = score_backward(h.detach(), W.detach(), targets, lse, entropy.detach(), ga, ge, ctx.chunk_rows,
-                                ctx.ignore_index, ctx.transform, need_h, need_W, dW_dtype=W.dtype, state=state)
-        return _first_order((dH, dW), (h, W, grad_logp, grad_entropy)) + (None,) * 5
+        ga = None if grad_logp is None else grad_logp.float().contiguous()
+        ge = None if grad_entropy is None else grad_entropy.float().contiguous()
+        # (the backward runs on the device of its tensors)
+        dH, dW = _grads(h, W, targets, lse, entropy, ga, ge, ctx.chunk_rows, ctx.ignore_index, ctx.transform, need_h,
+                        need_W, None, None, W.dtype, state)
+        if torch.is_grad_enabled():
+            dH, dW = _first_order((dH, dW), (h, W, grad_logp, grad_entropy))
+        return (dH, dW) + (None,) * 5
 
 
 def selective_log_softmax_entropy(h, W, targets, chunk_rows: int = 256, ignore_index: int = IGNORE_INDEX,
