@@ -227,6 +227,33 @@ def load(path: str | None = None, build_if_missing: bool = True) -> ctypes.CDLL:
     return lib
 
 
+_TORCH_OPS = None
+# what the operators call, in bind's order
+_TORCH_ENTRIES = ("flce_layer_norm", "flce_layer_norm_backward", "flce_layer_norm_backward_workspace_bytes", "flce_score",
+                  "flce_score_workspace_bytes", "flce_score_state_bytes", "flce_score_backward",
+                  "flce_score_backward_workspace_bytes", "flce_status_string")
+
+
+def torch_ops():
+    """(layer_norm, score): the differentiable calls as PyTorch operators
+    (csrc/torch_ops.cpp), bound to this library's entry points."""
+    global _TORCH_OPS
+    if _TORCH_OPS is None:
+        import torch
+        lib = load()
+        torch.ops.load_library(_build.build_torch_ops() if not os.path.exists(_build.TORCH_LIB_PATH)
+                               else _build.TORCH_LIB_PATH)
+        torch.ops.flce.bind([ctypes.cast(getattr(lib, name), _c_vp).value for name in _TORCH_ENTRIES])
+        _TORCH_OPS = (torch.ops.flce.layer_norm.default, torch.ops.flce.score.default)
+    return _TORCH_OPS
+
+
+def torch_error(e: RuntimeError) -> RuntimeError:
+    """What an operator raised, as the binding's error where a call failed."""
+    m = re.match(r"(flce_\w+) failed: (FLCE_ERR_\w+)", str(e))
+    return FlceError(m[1], next(k for k, v in STATUS_NAMES.items() if v == m[2])) if m else e
+
+
 def _ptr(x) -> int | None:
     if x is None:
         return None

@@ -1,0 +1,240 @@
+// The differentiable calls of the layer norm and of the scores as PyTorch operators
+// (torch.ops.flce): a training step on few rows is bound by its host work, and of
+// an autograd node in Python 100 us of 250 run on the engine's own thread, whose
+// caches are cold.  Marshalling only, as the ctypes binding: the arithmetic runs
+// behind include/flce.h, whose entry points `bind` takes from the library that the
+// binding has loaded.  The callers in Python have checked the tensors.
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/library.h>
+
+#include <string>
+#include <vector>
+
+#include "flce.h"
+
+namespace {
+
+using at::Tensor;
+using torch::autograd::AutogradContext;
+using torch::autograd::Function;
+using torch::autograd::variable_list;
+
+struct Api {
+  decltype(&flce_layer_norm) layer_norm = nullptr;
+  decltype(&flce_layer_norm_backward) layer_norm_backward = nullptr;
+  decltype(&flce_layer_norm_backward_workspace_bytes) layer_norm_backward_workspace_bytes = nullptr;
+  decltype(&flce_score) score = nullptr;
+  decltype(&flce_score_workspace_bytes) score_workspace_bytes = nullptr;
+  decltype(&flce_score_state_bytes) score_state_bytes = nullptr;
+  decltype(&flce_score_backward) score_backward = nullptr;
+  decltype(&flce_score_backward_workspace_bytes) score_backward_workspace_bytes = nullptr;
+  decltype(&flce_status_string) status_string = nullptr;
+};
+Api g_api;
+
+template <class F>
+void take(F& f, int64_t address) {
+  f = reinterpret_cast<F>(address);
+}
+void bind(at::IntArrayRef a) {
+  TORCH_CHECK(a.size() == 9, "flce: nine entry points are expected");
+  take(g_api.layer_norm, a[0]);
+  take(g_api.layer_norm_backward, a[1]);
+  take(g_api.layer_norm_backward_workspace_bytes, a[2]);
+  take(g_api.score, a[3]);
+  take(g_api.score_workspace_bytes, a[4]);
+  take(g_api.score_state_bytes, a[5]);
+  take(g_api.score_backward, a[6]);
+  take(g_api.score_backward_workspace_bytes, a[7]);
+  take(g_api.status_string, a[8]);
+}
+
+void check(const char* fn, flce_status s) {
+  TORCH_CHECK(s == FLCE_OK, fn, " failed: ", g_api.status_string(s));
+}
+
+int32_t kind(const Tensor& t) { return t.scalar_type() == at::kFloat ? FLCE_F32 : FLCE_BF16; }
+void* data(const Tensor& t) { return t.defined() && t.numel() > 0 ? t.data_ptr() : nullptr; }
+flce_bf16* bf16(const Tensor& t) { return static_cast<flce_bf16*>(data(t)); }
+float* f32(const Tensor& t) { return static_cast<float*>(data(t)); }
+// the current stream of the tensors' device, which is the current one
+void* stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
+// (torch's allocator orders a workspace's reuse on the current stream)
+Tensor bytes(size_t n, const Tensor& like) {
+  return at::empty({static_cast<int64_t>(n)}, like.options().dtype(at::kByte));
+}
+// A gradient as the kernels read it: contiguous, from a 16-byte boundary on (a part
+// of a flat buffer may start anywhere).
+Tensor rows_of(const Tensor& g) {
+  if (!g.defined()) return g;
+  Tensor c = g.contiguous();
+  return reinterpret_cast<uintptr_t>(c.data_ptr()) % 16 == 0 ? c : c.clone();
+}
+
+// Gradients that kernels formed without a graph, tied to the tensors they depend
+// on: differentiating them again is refused, not taken for zero.
+struct NoSecondDerivative : Function<NoSecondDerivative> {
+  static variable_list forward(AutogradContext*, int64_t n, at::TensorList all) {
+    variable_list out;
+    for (int64_t i = 0; i < n; ++i) out.push_back(all[i].view_as(all[i]));
+    return out;
+  }
+  static variable_list backward(AutogradContext*, variable_list) {
+    TORCH_CHECK(false, "this gradient has no second derivative: it comes from a kernel, without a graph");
+  }
+};
+
+// grads (each may be undefined) as a backward returns them: under create_graph
+// tied to the inputs.
+variable_list first_order(variable_list grads, const variable_list& inputs) {
+  if (!at::GradMode::is_enabled()) return grads;
+  std::vector<Tensor> all;
+  for (const Tensor& g : grads)
+    if (g.defined()) all.push_back(g);
+  const int64_t n = static_cast<int64_t>(all.size());
+  if (n == 0) return grads;
+  for (const Tensor& x : inputs)
+    if (x.defined()) all.push_back(x);
+  variable_list tied = NoSecondDerivative::apply(n, at::TensorList(all));
+  size_t k = 0;
+  for (Tensor& g : grads)
+    if (g.defined()) g = tied[k++];
+  return grads;
+}
+
+int64_t row_stride(const Tensor& x) { return x.size(0) > 1 ? x.stride(0) : x.size(1); }
+
+struct LayerNorm : Function<LayerNorm> {
+  static variable_list forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight,
+                               const std::optional<Tensor>& bias, const std::optional<Tensor>& residual, double eps,
+                               double weight_offset) {
+    ctx->set_materialize_grads(false);
+    const int64_t N = x.size(0), H = x.size(1);
+    const Tensor b = bias.value_or(Tensor()), r = residual.value_or(Tensor());
+    Tensor y = at::empty({N, H}, x.options());
+    Tensor s = r.defined() ? at::empty({N, H}, r.options()) : Tensor();
+    Tensor stats = at::empty({2, N}, x.options().dtype(at::kFloat));  // mean, rstd
+    float* mean = f32(stats);
+    check("flce_layer_norm",
+          g_api.layer_norm(bf16(x), row_stride(x), data(r), r.defined() ? row_stride(r) : 0, r.defined() ? kind(r) : 0,
+                           data(weight), data(b), kind(weight), static_cast<float>(weight_offset),
+                           static_cast<float>(eps), N, H, bf16(y), data(s), mean, mean ? mean + N : nullptr, stream()));
+    ctx->save_for_backward({r.defined() ? s : x, weight, stats});
+    ctx->saved_data["offset"] = weight_offset;
+    ctx->saved_data["bias"] = b.defined();
+    ctx->saved_data["residual"] = r.defined();
+    return r.defined() ? variable_list{y, s} : variable_list{y};
+  }
+
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &s = saved[0], &weight = saved[1], &stats = saved[2];
+    const bool has_b = ctx->saved_data["bias"].toBool(), has_r = ctx->saved_data["residual"].toBool();
+    // (edges: the tensors that were there, in order)
+    const bool need_x = ctx->needs_input_grad(0), need_w = ctx->needs_input_grad(1);
+    const bool need_b = has_b && ctx->needs_input_grad(2), need_r = has_r && ctx->needs_input_grad(has_b ? 3 : 2);
+    const Tensor ds0 = grads.size() > 1 ? grads[1] : Tensor();
+    if (!grads[0].defined()) {  // only the stream was used
+      if (!ds0.defined()) return variable_list(6);
+      return {need_x ? ds0.to(at::kBFloat16) : Tensor(), Tensor(), Tensor(), need_r ? ds0 : Tensor(), Tensor(), Tensor()};
+    }
+    const Tensor dy = rows_of(grads[0]), ds = rows_of(ds0);
+    const int64_t N = s.size(0), H = s.size(1);
+    const bool wide = s.scalar_type() == at::kFloat;
+    Tensor dx, dr, dw, db, ws;
+    if (need_x || (need_r && !wide)) dx = at::empty({N, H}, dy.options());
+    if (need_r && wide) dr = at::empty({N, H}, s.options());
+    if (need_w) dw = at::empty({H}, weight.options());
+    if (need_b) db = at::empty({H}, weight.options());
+    if (need_w || need_b) ws = bytes(g_api.layer_norm_backward_workspace_bytes(N, H), s);
+    const float* mean = f32(stats);
+    if (dx.defined() || dr.defined() || dw.defined() || db.defined())
+      check("flce_layer_norm_backward",
+            g_api.layer_norm_backward(bf16(dy), data(s), row_stride(s), kind(s), data(ds), data(weight), kind(weight),
+                                      static_cast<float>(ctx->saved_data["offset"].toDouble()), mean,
+                                      mean ? mean + N : nullptr, N, H, bf16(dx), f32(dr), data(dw), data(db), data(ws),
+                                      ws.defined() ? ws.numel() : 0, stream()));
+    variable_list out{need_x ? dx : Tensor(), dw, db, need_r ? (wide ? dr : dx) : Tensor()};
+    out = first_order(std::move(out), {s, weight, grads[0], ds0});
+    out.resize(6);
+    return out;
+  }
+};
+
+std::vector<Tensor> layer_norm(const Tensor& x, const Tensor& weight, const std::optional<Tensor>& bias,
+                               const std::optional<Tensor>& residual, double eps, double weight_offset) {
+  return LayerNorm::apply(x, weight, bias, residual, eps, weight_offset);
+}
+
+// the four fields of a flce_logit_transform, or nothing
+struct Transform {
+  flce_logit_transform t{};
+  bool given = false;
+  explicit Transform(at::ArrayRef<double> v) : given(v.size() == 4) {
+    if (given)
+      t = {static_cast<float>(v[0]), static_cast<float>(v[1]), static_cast<float>(v[2]), static_cast<float>(v[3])};
+  }
+  const flce_logit_transform* get() const { return given ? &t : nullptr; }
+};
+
+struct Score : Function<Score> {
+  static variable_list forward(AutogradContext* ctx, const Tensor& h, const Tensor& W, const Tensor& targets,
+                               int64_t chunk_rows, int64_t ignore_index, std::vector<double> transform,
+                               bool recompute) {
+    ctx->set_materialize_grads(false);
+    const int64_t N = h.size(0), H = h.size(1), V = W.size(0);
+    const auto f32_rows = h.options().dtype(at::kFloat);
+    Tensor logp = at::empty({N}, f32_rows), lse = at::empty({N}, f32_rows), entropy = at::empty({N}, f32_rows);
+    const size_t kept = recompute ? 0 : g_api.score_state_bytes(N, H, V, chunk_rows);
+    Tensor state = kept ? bytes(kept, h) : Tensor();
+    Tensor ws = bytes(g_api.score_workspace_bytes(N, H, V, 0), h);
+    const Transform tf(transform);
+    check("flce_score", g_api.score(bf16(h), bf16(W), static_cast<const int64_t*>(data(targets)), N, H, V, 0,
+                                    ignore_index, tf.get(), f32(logp), f32(lse), f32(entropy), nullptr, nullptr,
+                                    data(state), data(ws), ws.numel(), stream()));
+    ctx->save_for_backward({h, W, targets, lse, entropy, state});
+    ctx->saved_data["rows"] = chunk_rows;
+    ctx->saved_data["ignore"] = ignore_index;
+    ctx->saved_data["transform"] = std::move(transform);
+    return {logp, entropy};
+  }
+
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const bool need_h = ctx->needs_input_grad(0), need_W = ctx->needs_input_grad(1);
+    if ((!grads[0].defined() && !grads[1].defined()) || !(need_h || need_W)) return variable_list(7);
+    const variable_list saved = ctx->get_saved_variables();
+    const Tensor &h = saved[0], &W = saved[1], &targets = saved[2], &lse = saved[3], &entropy = saved[4],
+                 &state = saved[5];
+    const int64_t N = h.size(0), H = h.size(1), V = W.size(0), rows = ctx->saved_data["rows"].toInt();
+    auto vector = [](const Tensor& g) { return g.defined() ? g.to(at::kFloat).contiguous() : g; };
+    const Tensor ga = vector(grads[0]), ge = vector(grads[1]);
+    Tensor dH = need_h ? at::empty({N, H}, h.options()) : Tensor();
+    Tensor dW = need_W ? at::empty({V, H}, W.options()) : Tensor();
+    Tensor ws = bytes(g_api.score_backward_workspace_bytes(N, H, V, rows, FLCE_BF16), h);
+    const std::vector<double> v = ctx->saved_data["transform"].toDoubleVector();
+    const Transform tf(v);
+    check("flce_score_backward",
+          g_api.score_backward(bf16(h), bf16(W), static_cast<const int64_t*>(data(targets)), f32(lse), f32(entropy),
+                               f32(ga), f32(ge), data(state), bf16(dH), data(dW), FLCE_BF16, N, H, V, rows,
+                               ctx->saved_data["ignore"].toInt(), tf.get(), data(ws), ws.numel(), stream()));
+    variable_list out = first_order({dH, dW}, {h, W, grads[0], grads[1]});
+    out.resize(7);
+    return out;
+  }
+};
+
+std::vector<Tensor> score(const Tensor& h, const Tensor& W, const Tensor& targets, int64_t chunk_rows,
+                          int64_t ignore_index, at::ArrayRef<double> transform, bool recompute) {
+  return Score::apply(h, W, targets, chunk_rows, ignore_index, transform.vec(), recompute);
+}
+
+}  // namespace
+
+TORCH_LIBRARY(flce, m) {
+  m.def("bind(int[] entry_points) -> ()", &bind);
+  m.def("layer_norm(Tensor x, Tensor weight, Tensor? bias, Tensor? residual, float eps, float weight_offset) -> Tensor[]",
+        &layer_norm);
+  m.def("score(Tensor h, Tensor W, Tensor targets, int chunk_rows, int ignore_index, float[] transform, bool recompute)"
+        " -> Tensor[]", &score);
+}

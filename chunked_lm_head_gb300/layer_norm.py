@@ -2,15 +2,14 @@
 x, or the residual stream with x added to it, and is differentiable.  Every
 arithmetic step runs in libflce's CUDA kernels (include/flce.h states the
 formulas); this module checks tensor properties, allocates outputs and passes
-pointers.
+pointers (the differentiable call leaves the last two to csrc/torch_ops.cpp).
 """
 from __future__ import annotations
 
 import torch
 
 from . import _lib
-from .api import _first_order
-from .norm import _TYPES, _check, _rows_of
+from .norm import _TYPES, _check
 from .score import _elsewhere
 
 
@@ -56,30 +55,6 @@ def layer_norm_forward(x, weight, bias=None, residual=None, eps: float = 1e-5, w
     return {"y": y, "residual": s, "mean": mean, "rstd": rstd}
 
 
-def _norm_grads(dy, s, lds, weight, mean, rstd, ds, weight_offset, need_dx, need_dr, need_dweight, need_dbias, workspace,
-                stream):
-    """(dx, dr, dweight, dbias) of checked tensors on the current device."""
-    N, H = s.shape
-    wide = s.dtype == torch.float32
-    dx = torch.empty_like(dy) if need_dx or (need_dr and not wide) else None
-    dr = torch.empty_like(s, memory_format=torch.contiguous_format) if need_dr and wide else None
-    dw = torch.empty_like(weight) if need_dweight else None
-    db = torch.empty_like(weight) if need_dbias else None
-    ws_bytes = 0
-    if need_dweight or need_dbias:
-        if workspace is None and stream is None:  # torch's allocator keeps it for the next call
-            workspace = torch.empty(_lib.flce_layer_norm_backward_workspace_bytes(N, H), dtype=torch.uint8,
-                                    device=s.device)
-        if workspace is not None:
-            ws_bytes = workspace.numel() * workspace.element_size()
-    elif dx is None and dr is None:
-        return None, None, None, None
-    _lib.check("flce_layer_norm_backward", _lib.flce_layer_norm_backward(
-        dy, s, lds, _TYPES[s.dtype], ds, weight, _TYPES[weight.dtype], weight_offset, mean, rstd, N, H, dx, dr, dw, db,
-        workspace, ws_bytes, stream))
-    return dx if need_dx else None, (dr if wide else dx) if need_dr else None, dw, db
-
-
 def layer_norm_backward(dy, s, weight, mean, rstd, ds=None, weight_offset: float = 0.0, need_dx: bool = True,
                         need_dr: bool = True, need_dweight: bool = True, need_dbias: bool = True,
                         workspace: torch.Tensor | None = None, stream=None):
@@ -102,37 +77,25 @@ def layer_norm_backward(dy, s, weight, mean, rstd, ds=None, weight_offset: float
         with torch.cuda.device(s.device):
             return layer_norm_backward(dy, s, weight, mean, rstd, ds, weight_offset, need_dx, need_dr, need_dweight,
                                        need_dbias, workspace, stream)
-    return _norm_grads(dy, s, lds, weight, mean, rstd, ds, weight_offset, need_dx, need_dr, need_dweight, need_dbias,
-                       workspace, stream)
-
-
-class LayerNormFunction(torch.autograd.Function):
-    """layer_norm with its backward; the stream is returned beside y."""
-
-    @staticmethod
-    def forward(ctx, x, weight, bias, residual, eps, weight_offset):
-        ctx.set_materialize_grads(False)
-        y, s, stats = _norm(x, weight, bias, residual, eps, weight_offset, True, None)
-        ctx.save_for_backward(x if s is None else s, weight, stats)
-        ctx.weight_offset = weight_offset
-        return y if s is None else (y, s)
-
-    @staticmethod
-    def backward(ctx, dy, ds=None):
-        s, weight, stats = ctx.saved_tensors
-        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
-        if dy is None:  # only the stream was used
-            if ds is None:
-                return (None,) * 6
-            return ds.to(torch.bfloat16) if need_x else None, None, None, ds if need_r else None, None, None
-        N, H = s.shape
-        mean = stats.data_ptr() if N else None  # (the backward runs on the device of its tensors)
-        dx, dr, dw, db = _norm_grads(_rows_of(dy), s, s.stride(0) if N > 1 else H, weight, mean, mean and mean + 4 * N,
-                                     None if ds is None else _rows_of(ds), ctx.weight_offset, need_x, need_r, need_w,
-                                     need_b, None, None)
-        if torch.is_grad_enabled():
-            dx, dw, db, dr = _first_order((dx, dw, db, dr), (s, weight, dy, ds))
-        return dx, dw, db, dr, None, None
+    N, H = s.shape
+    wide = s.dtype == torch.float32
+    dx = torch.empty_like(dy) if need_dx or (need_dr and not wide) else None
+    dr = torch.empty_like(s, memory_format=torch.contiguous_format) if need_dr and wide else None
+    dw = torch.empty_like(weight) if need_dweight else None
+    db = torch.empty_like(weight) if need_dbias else None
+    ws_bytes = 0
+    if need_dweight or need_dbias:
+        if workspace is None and stream is None:  # torch's allocator keeps it for the next call
+            workspace = torch.empty(_lib.flce_layer_norm_backward_workspace_bytes(N, H), dtype=torch.uint8,
+                                    device=s.device)
+        if workspace is not None:
+            ws_bytes = workspace.numel() * workspace.element_size()
+    elif dx is None and dr is None:
+        return None, None, None, None
+    _lib.check("flce_layer_norm_backward", _lib.flce_layer_norm_backward(
+        dy, s, lds, _TYPES[s.dtype], ds, weight, _TYPES[weight.dtype], weight_offset, mean, rstd, N, H, dx, dr, dw, db,
+        workspace, ws_bytes, stream))
+    return dx if need_dx else None, (dr if wide else dx) if need_dr else None, dw, db
 
 
 def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, weight_offset: float = 0.0):
@@ -143,7 +106,15 @@ def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, weight_of
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or
                                     (bias is not None and bias.requires_grad) or
                                     (residual is not None and residual.requires_grad)):
-        return LayerNormFunction.apply(x, weight, bias, residual, eps, weight_offset)
+        _check_all(x, weight, bias, residual)
+        if _elsewhere(x):
+            with torch.cuda.device(x.device):
+                return layer_norm(x, weight, bias, residual, eps, weight_offset)
+        try:
+            out = (_lib._TORCH_OPS or _lib.torch_ops())[0](x, weight, bias, residual, eps, weight_offset)
+        except RuntimeError as e:
+            raise _lib.torch_error(e) from None
+        return out[0] if residual is None else tuple(out)
     y, s, _ = _norm(x, weight, bias, residual, eps, weight_offset, False, None)
     return y if s is None else (y, s)
 

@@ -5,14 +5,15 @@ and the entropy, differentiable in both; ``top_logprobs`` the K likeliest words
 of each row with their log-probabilities.  ``score_forward`` and
 ``score_backward`` are the calls below them.  Every arithmetic step runs in
 libflce's CUDA kernels (include/flce.h states the formulas); this module checks
-tensor properties, allocates outputs and passes pointers.
+tensor properties, allocates outputs and passes pointers (the differentiable call
+leaves the last two to csrc/torch_ops.cpp).
 """
 from __future__ import annotations
 
 import torch
 
 from . import _lib
-from .api import IGNORE_INDEX, _first_order
+from .api import IGNORE_INDEX
 from .topk import _DW, _workspace
 
 
@@ -76,20 +77,6 @@ def score_forward(h, W, targets=None, k: int = 0, ignore_index: int = IGNORE_IND
     return {"logp": logp, "lse": lse, "entropy": entropy, "ids": ids, "logprobs": words, "state": state}
 
 
-def _grads(h, W, targets, lse, entropy, grad_logp, grad_entropy, chunk_rows, ignore_index, transform, need_dH, need_dW,
-           workspace, stream, dW_dtype, state):
-    """score_backward of checked tensors on the current device."""
-    (N, H), V, dev = h.shape, W.shape[0], h.device
-    dH = torch.empty_like(h) if need_dH else None
-    dW = torch.empty((V, H), dtype=dW_dtype, device=dev) if need_dW else None
-    kind = _DW[dW_dtype]
-    ws, ws_bytes = _workspace(workspace, _lib.flce_score_backward_workspace_bytes(N, H, V, chunk_rows, kind), stream, dev)
-    _lib.check("flce_score_backward", _lib.flce_score_backward(
-        h, W, targets, lse, entropy, grad_logp, grad_entropy, state, dH, dW, kind, N, H, V, chunk_rows, ignore_index,
-        transform, ws, ws_bytes, stream))
-    return dH, dW
-
-
 def score_backward(h, W, targets, lse, entropy, grad_logp=None, grad_entropy=None, chunk_rows: int = 256,
                    ignore_index: int = IGNORE_INDEX, transform=None, need_dH: bool = True, need_dW: bool = True,
                    workspace: torch.Tensor | None = None, stream=None, dW_dtype=torch.float32, state=None):
@@ -114,36 +101,14 @@ def score_backward(h, W, targets, lse, entropy, grad_logp=None, grad_entropy=Non
         with torch.cuda.device(dev):
             return score_backward(h, W, targets, lse, entropy, grad_logp, grad_entropy, chunk_rows, ignore_index,
                                   transform, need_dH, need_dW, workspace, stream, dW_dtype, state)
-    return _grads(h, W, targets, lse, entropy, grad_logp, grad_entropy, chunk_rows, ignore_index, transform, need_dH,
-                  need_dW, workspace, stream, dW_dtype, state)
-
-
-class SelectiveLogSoftmaxEntropy(torch.autograd.Function):
-    """selective_log_softmax_entropy with its backward, from kept logits where the
-    rows fit chunk_rows, else recomputing them."""
-
-    @staticmethod
-    def forward(ctx, h, W, targets, chunk_rows, ignore_index, transform, recompute):
-        ctx.set_materialize_grads(False)  # no zeros for an output without a gradient
-        out = score_forward(h, W, targets, 0, ignore_index, transform, keep_rows=0 if recompute else chunk_rows)
-        ctx.save_for_backward(h, W, targets, out["lse"], out["entropy"], out["state"])
-        ctx.chunk_rows, ctx.ignore_index, ctx.transform = chunk_rows, ignore_index, transform
-        return out["logp"], out["entropy"]
-
-    @staticmethod
-    def backward(ctx, grad_logp, grad_entropy):
-        need_h, need_W = ctx.needs_input_grad[:2]
-        if (grad_logp is None and grad_entropy is None) or not (need_h or need_W):
-            return (None,) * 7
-        h, W, targets, lse, entropy, state = ctx.saved_tensors
-        ga = None if grad_logp is None else grad_logp.float().contiguous()
-        ge = None if grad_entropy is None else grad_entropy.float().contiguous()
-        # (the backward runs on the device of its tensors)
-        dH, dW = _grads(h, W, targets, lse, entropy, ga, ge, ctx.chunk_rows, ctx.ignore_index, ctx.transform, need_h,
-                        need_W, None, None, W.dtype, state)
-        if torch.is_grad_enabled():
-            dH, dW = _first_order((dH, dW), (h, W, grad_logp, grad_entropy))
-        return (dH, dW) + (None,) * 5
+    dH = torch.empty_like(h) if need_dH else None
+    dW = torch.empty((V, H), dtype=dW_dtype, device=dev) if need_dW else None
+    ws, ws_bytes = _workspace(workspace, _lib.flce_score_backward_workspace_bytes(N, H, V, chunk_rows, _DW[dW_dtype]),
+                              stream, dev)
+    _lib.check("flce_score_backward", _lib.flce_score_backward(
+        h, W, targets, lse, entropy, grad_logp, grad_entropy, state, dH, dW, _DW[dW_dtype], N, H, V, chunk_rows,
+        ignore_index, transform, ws, ws_bytes, stream))
+    return dH, dW
 
 
 def selective_log_softmax_entropy(h, W, targets, chunk_rows: int = 256, ignore_index: int = IGNORE_INDEX,
@@ -161,7 +126,17 @@ def selective_log_softmax_entropy(h, W, targets, chunk_rows: int = 256, ignore_i
     if not torch.is_grad_enabled() or not (h.requires_grad or W.requires_grad):
         out = score_forward(h, W, targets, 0, ignore_index, transform)
         return out["logp"], out["entropy"]
-    return SelectiveLogSoftmaxEntropy.apply(h, W, targets, chunk_rows, ignore_index, transform, recompute)
+    _check(h, W, targets)
+    if _elsewhere(h):
+        with torch.cuda.device(h.device):
+            return selective_log_softmax_entropy(h, W, targets, chunk_rows, ignore_index, transform, recompute)
+    tf = _lib.make_transform(transform)
+    try:
+        return tuple((_lib._TORCH_OPS or _lib.torch_ops())[1](
+            h, W, targets, chunk_rows, ignore_index,
+            [] if tf is None else [tf.scale_multiply, tf.scale_divide, tf.softcap, tf.temperature], recompute))
+    except RuntimeError as e:
+        raise _lib.torch_error(e) from None
 
 
 def top_logprobs(h, W, k: int, targets=None, ignore_index: int = IGNORE_INDEX, transform=None,
