@@ -235,8 +235,8 @@ _TORCH_ENTRIES = ("flce_layer_norm", "flce_layer_norm_backward", "flce_layer_nor
 
 
 def torch_ops():
-    """(layer_norm, score): the differentiable calls as PyTorch operators
-    (csrc/torch_ops.cpp), bound to this library's entry points."""
+    """(layer_norm, score, top) as PyTorch operators (csrc/torch_ops.cpp), bound to
+    this library's entry points."""
     global _TORCH_OPS
     if _TORCH_OPS is None:
         import torch
@@ -244,8 +244,15 @@ def torch_ops():
         torch.ops.load_library(_build.build_torch_ops() if not os.path.exists(_build.TORCH_LIB_PATH)
                                else _build.TORCH_LIB_PATH)
         torch.ops.flce.bind([ctypes.cast(getattr(lib, name), _c_vp).value for name in _TORCH_ENTRIES])
-        _TORCH_OPS = (torch.ops.flce.layer_norm.default, torch.ops.flce.score.default)
+        ops = torch.ops.flce
+        _TORCH_OPS = (ops.layer_norm.default, ops.score.default, ops.top.default)
     return _TORCH_OPS
+
+
+def transform_list(tf) -> list:
+    """A logit transform as the operators take it."""
+    t = make_transform(tf)
+    return [] if t is None else [t.scale_multiply, t.scale_divide, t.softcap, t.temperature]
 
 
 def torch_error(e: RuntimeError) -> RuntimeError:

@@ -788,12 +788,20 @@ __device__ __forceinline__ void mma_commit_all(uint32_t bar) {
     umma_commit_pair_mc(bar, 0x3);  // the barrier at this offset in both CTAs
 }
 
-// tanh as 1 - 2 / (1 + e^2x), by the SFU's exponential and reciprocal: off by at
-// most 2^-21.5 absolutely (both are good to 2^-22, the quotient is at most 2),
-// which a soft-capped logit, cap tanh(z / cap), has anyway from a z of its size.
-// A fifth of tanhf's instructions.
-__device__ __forceinline__ float cap_tanh(float x) {
-  return fmaf(-1.f, __fdividef(2.f, 1.f + ex2_approx(2.f * kLog2e * x)), 1.f);
+// u = b tanh(a z) of two soft-capped logits, tanh x = 1 - 2 / (1 + e^2x) by the SFU's
+// exponential and reciprocal: off by at most b 2^-21.5 (both are good to 2^-22, the
+// quotient is at most 2), which a u of its size has anyway from its z.  A fifth of
+// tanhf's instructions.  An infinite z, which tanh would hide, becomes NaN (0 z).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 soft_cap2(float2 z, float a, float b) {
+  const float2 x = mul2(z, both(2.f * kLog2e * a));
+  const float2 e = add2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), both(1.f));
+  const float2 u = fma2(make_float2(rcp_approx(e.x), rcp_approx(e.y)), both(-2.f * b), both(b));
+  return fma2(z, both(0.f), u);
 }
 
 // v[j] for a run-time j in [0, 32) without dynamic register indexing (which
@@ -1282,6 +1290,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
             // where m is the row's maximum, and nothing cancels (lse - sum p x
             // would, a log-sum-exp of 20 against an entropy near 0).
             const int nc = min(32, p.V - col0);  // columns of the chunk (32, but in the last tile)
+            float top_key = -INFINITY;
             run_abs = fmaxf(fmaxf(run_abs, fmaxf(fabsf(v[0]), fabsf(v[8]))), fmaxf(fabsf(v[16]), fabsf(v[24])));
             if (kScore == SCORE_TOP && p.z != nullptr) {
               if (row_ok) {
@@ -1301,6 +1310,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                 m2 = fmaxf(m2, less);
               }
               // two chunks' records leave together
+              top_key = m1;
               if ((c & 1) == 0) {
                 rec_even = make_float2(m1, m2);
                 rec_third = m3;
@@ -1311,9 +1321,12 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
               }
             }
             if (p.tf_softcap) {
-              // (an infinite logit, which tanh would hide, becomes NaN: 0 z)
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], 0.f, p.tf_b * cap_tanh(p.tf_a * v[j]));
+              for (int j = 0; j < 32; j += 2) {
+                const float2 u = soft_cap2(make_float2(v[j], v[j + 1]), p.tf_a, p.tf_b);
+                v[j] = u.x;
+                v[j + 1] = u.y;
+              }
             }
             if (nc < 32) {
 #pragma unroll
@@ -1321,8 +1334,13 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                 if (j >= nc) v[j] = -INFINITY;
             }
             float cm = v[0];
+            if (kScore == SCORE_TOP && p.z == nullptr) {
+              // any reference near the maximum does: the record's
+              cm = p.tf_softcap && top_key > -INFINITY ? soft_cap2(both(top_key), p.tf_a, p.tf_b).x : top_key;
+            } else {
 #pragma unroll
-            for (int j = 1; j < 32; ++j) cm = fmaxf(cm, v[j]);
+              for (int j = 1; j < 32; ++j) cm = fmaxf(cm, v[j]);
+            }
             const float nm = fmaxf(run_m, cm * l2a);
             // the exponentials' reference: the row's maximum so far, or (kept
             // logits) the chunk's own
@@ -1335,9 +1353,18 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                 const float2 x = fma2(make_float2(v[j], v[j + 1]), both(l2a), both(-ref));
                 const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                 a = add2(a, w);
-                // (a logit of -infinity has no share: 0, not 0 times infinity)
-                e = fma2(w, make_float2(fmaxf(x.x, -1000.f), fmaxf(x.y, -1000.f)), e);
+                e = fma2(w, x, e);
                 if constexpr (MODE == MODE_FUSED_FWD) pk[j / 2] = pack_f16x2(x.x, x.y);
+              }
+              if (e.x + e.y != e.x + e.y) {
+                // a logit of -infinity (or a column past the vocabulary) has no
+                // share: 0, not 0 times infinity.  (A NaN stays one, in a)
+                e = both(0.f);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  const float x = fmaf(v[j], l2a, -ref);
+                  e.x = fmaf(ex2_approx(x), fmaxf(x, -1000.f), e.x);
+                }
               }
               if constexpr (MODE == MODE_FUSED_FWD) {
                 // from the chunk's reference to the row's (a chunk without a
@@ -1353,8 +1380,11 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
               run_ent = fmaf(fmaf(up, run_s, run_ent), r, -(e.x + e.y));
               run_s = fmaf(run_s, r, a.x + a.y);
               run_m = nm;
-            } else if (cm != cm) {
-              run_s = cm;  // NaN throughout, without a maximum so far
+            } else {
+              // without a maximum so far: NaN, or nothing
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (v[j] != v[j]) run_s = v[j];
             }
             if constexpr (MODE == MODE_FUSED_FWD) {
               // the logits, log2 relative to the chunk's largest, in fp16: exact
@@ -1559,7 +1589,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE>(EW), 1)
                     for (int e = 0; e < 2; ++e) {
                       float x, slope = lin_a;
                       if (p.tf_softcap) {
-                        const float th = cap_tanh(p.tf_a * v[j + e]);
+                        const float th = soft_cap2(both(v[j + e]), p.tf_a, 1.f).x;
                         x = fmaf(p.tf_b * th, kLog2e, nl2);
                         slope = p.tf_d * (1.f - th * th);
                       } else {

@@ -49,6 +49,18 @@ __device__ __forceinline__ ScorePart score_join(const ScorePart& a, const ScoreP
   return o;
 }
 
+// A warp's partials joined, in a fixed order; the same in all lanes.
+__device__ __forceinline__ ScorePart score_join_warp(ScorePart a, int lane) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const ScorePart b{__shfl_xor_sync(0xffffffffu, a.m, off), __shfl_xor_sync(0xffffffffu, a.s, off),
+                      __shfl_xor_sync(0xffffffffu, a.c, off), __shfl_xor_sync(0xffffffffu, a.top, off)};
+    // (the lower lane's first, in both)
+    a = (lane & off) ? score_join(b, a) : score_join(a, b);
+  }
+  return a;
+}
+
 // A row's S partials joined by a warp, in a fixed order; the same in all lanes.
 // (Eight of a lane's are read at once: the joins wait on one another.)
 __device__ __forceinline__ ScorePart score_join_row(const float4* part, int S, int lane) {
@@ -62,21 +74,14 @@ __device__ __forceinline__ ScorePart score_join_row(const float4* part, int S, i
     for (int e = 0; e < 8; ++e)
       if (s0 + 32 * e < S) a = score_join(a, ScorePart{q[e].x, q[e].y, q[e].z, q[e].w});
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const ScorePart b{__shfl_xor_sync(0xffffffffu, a.m, off), __shfl_xor_sync(0xffffffffu, a.s, off),
-                      __shfl_xor_sync(0xffffffffu, a.c, off), __shfl_xor_sync(0xffffffffu, a.top, off)};
-    // (the lower lane's first, in both)
-    a = (lane & off) ? score_join(b, a) : score_join(a, b);
-  }
-  return a;
+  return score_join_warp(a, lane);
 }
 
 // (lse, entropy); NaN where the row has a logit that is NaN or +infinity (with a
 // soft-cap, any infinity), or none above -infinity.
 __device__ __forceinline__ float2 score_of(const ScorePart& a) {
   const float nan = __int_as_float(0x7fc00000);
-  if (!(a.s > 0.f) || !(fabsf(a.m) < INFINITY)) return make_float2(nan, nan);
+  if (!(a.s > 0.f && a.s < INFINITY) || !(fabsf(a.m) < INFINITY)) return make_float2(nan, nan);
   const float l2 = log2f(a.s);
   // m ln 2 + log S with ln 2 in two parts
   const float lse = fmaf(a.m, kLn2, fmaf(a.m, kLn2Low, l2 * kLn2));
@@ -160,19 +165,19 @@ __device__ __forceinline__ float2 two_add(float2 x, float2 y) {
 // sum_k h_k w_k of a bf16 row with NW others by a warp, each as a rounded value
 // and what the rounding leaves out: products of bf16 are exact in fp32, each step
 // of the sum hands its rounding error to a second sum.  The same in all lanes.
-// 1,024 elements of each are read at once: a word's row is somewhere else in
+// 256 G elements of each are read at once: a word's row is somewhere else in
 // memory each time.
-template <int NW>
+template <int NW, int G>
 __device__ __forceinline__ void exact_dots(const uint16_t* __restrict__ h, const uint16_t* const (&w)[NW], int H,
                                            int lane, float2 (&out)[NW]) {
   float2 hi[NW], lo[NW];
 #pragma unroll
   for (int i = 0; i < NW; ++i) hi[i] = lo[i] = both(0.f);
   const float2 minus = both(-1.f);
-  for (int k0 = lane * 8; k0 < H; k0 += 1024) {
-    Raw8<uint16_t> a[4], b[NW][4];
+  for (int k0 = lane * 8; k0 < H; k0 += 256 * G) {
+    Raw8<uint16_t> a[G], b[NW][G];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < G; ++g) {
       const int k = k0 + 256 * g;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
@@ -187,7 +192,7 @@ __device__ __forceinline__ void exact_dots(const uint16_t* __restrict__ h, const
         a[g].zero();
     }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < G; ++g) {
       if (k0 - lane * 8 + 256 * g >= H) break;  // (the whole warp)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) score_select_kernel(const
   __shared__ int found, kept_words, whole_chunks;
   __shared__ float best_k;
   __shared__ float2 target_z;
-  __shared__ ScorePart row_part;
+  __shared__ ScorePart parts[T / 32], row_part;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int K = p.out.k;
   const int j = blockIdx.x;
@@ -301,20 +306,31 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) score_select_kernel(const
   };
   const uint16_t* h = p.h + i * p.H;
   float top = -INFINITY;
-#pragma unroll 4
-  for (int c = t; c < units; c += T) top = fmaxf(top, unit(c).x);
-  if (warp == 0) {
-    const ScorePart w = score_join_row(p.part + static_cast<idx_t>(j) * p.S, p.S, lane);
-    if (lane == 0) {
-      row_part = w;
-      found = kept_words = whole_chunks = 0;
+  // the row's partials, joined by warps and then by the first
+  {
+    ScorePart w{-INFINITY, 0.f, 0.f, 0.f};
+    const float4* part = p.part + static_cast<idx_t>(j) * p.S;
+    for (int s = t; s < p.S; s += T) {
+      const float4 q = part[s];
+      w = score_join(w, ScorePart{q.x, q.y, q.z, q.w});
     }
+    w = score_join_warp(w, lane);
+    if (lane == 0) parts[warp] = w;
   }
+#pragma unroll(T == 256 ? 4 : 8)
+  for (int c = t; c < units; c += T) top = fmaxf(top, unit(c).x);
+  if (t == 0) found = kept_words = whole_chunks = 0;
   const uint32_t mine = ordered(top);
   uint32_t prefix = 0;
 #pragma unroll 1
-  for (uint32_t bit = 0x80000000u; bit >= 0x8000u; bit >>= 1)
+  for (uint32_t bit = 0x80000000u; bit >= 0x8000u; bit >>= 1) {
     if (__syncthreads_count(mine >= (prefix | bit)) >= K) prefix |= bit;
+    if (bit == 0x80000000u && warp == 0) {
+      const ScorePart w =
+          score_join_warp(lane < T / 32 ? parts[lane] : ScorePart{-INFINITY, 0.f, 0.f, 0.f}, lane);
+      if (lane == 0) row_part = w;
+    }
+  }
   const ScorePart whole = row_part;
   const float2 r = score_of(whole);
   if (r.x != r.x) {
@@ -361,7 +377,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) score_select_kernel(const
       const long long v1 = e + 1 < total ? word[e + 1] : e + 1 < end ? tgt : v0;
       const uint16_t* const w[2] = {p.W + v0 * p.H, p.W + v1 * p.H};
       float2 z[2];
-      exact_dots<2>(h, w, p.H, lane, z);
+      exact_dots<2, T == 256 ? 4 : 6>(h, w, p.H, lane, z);
       if (lane < 2 && e + lane < end) (e + lane < total ? val[e + lane] : target_z) = lane == 0 ? z[0] : z[1];
     }
     __syncthreads();

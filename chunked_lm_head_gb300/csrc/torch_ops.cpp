@@ -1,7 +1,7 @@
-// The differentiable calls of the layer norm and of the scores as PyTorch operators
-// (torch.ops.flce): a training step on few rows is bound by its host work, and of
-// an autograd node in Python 100 us of 250 run on the engine's own thread, whose
-// caches are cold.  Marshalling only, as the ctypes binding: the arithmetic runs
+// The layer norm and the scores as PyTorch operators (torch.ops.flce).  A call on few
+// rows is bound by its host work: a training step of 1,003 x 1,000 took 248 us with
+// its autograd node in Python, 100 of them on the engine's own thread, whose caches
+// are cold, and takes 177 this way.  Marshalling only, as the ctypes binding: the arithmetic runs
 // behind include/flce.h, whose entry points `bind` takes from the library that the
 // binding has loaded.  The callers in Python have checked the tensors.
 #include <c10/cuda/CUDAStream.h>
@@ -105,26 +105,41 @@ variable_list first_order(variable_list grads, const variable_list& inputs) {
 
 int64_t row_stride(const Tensor& x) { return x.size(0) > 1 ? x.stride(0) : x.size(1); }
 
+// y, and with a residual the stream; stats [2,N] (mean, rstd) where they are wanted.
+variable_list run_layer_norm(const Tensor& x, const Tensor& weight, const Tensor& b, const Tensor& r, double eps,
+                             double weight_offset, Tensor* stats) {
+  const int64_t N = x.size(0), H = x.size(1);
+  Tensor y = at::empty({N, H}, x.options());
+  Tensor s = r.defined() ? at::empty({N, H}, r.options()) : Tensor();
+  if (stats) *stats = at::empty({2, N}, x.options().dtype(at::kFloat));
+  float* mean = stats ? f32(*stats) : nullptr;
+  check("flce_layer_norm",
+        g_api.layer_norm(bf16(x), row_stride(x), data(r), r.defined() ? row_stride(r) : 0, r.defined() ? kind(r) : 0,
+                         data(weight), data(b), kind(weight), static_cast<float>(weight_offset), static_cast<float>(eps),
+                         N, H, bf16(y), data(s), mean, mean ? mean + N : nullptr, stream()));
+  return r.defined() ? variable_list{y, s} : variable_list{y};
+}
+
+bool wanted(std::initializer_list<const Tensor*> inputs) {
+  if (!at::GradMode::is_enabled()) return false;
+  for (const Tensor* t : inputs)
+    if (t->defined() && t->requires_grad()) return true;
+  return false;
+}
+
 struct LayerNorm : Function<LayerNorm> {
   static variable_list forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight,
                                const std::optional<Tensor>& bias, const std::optional<Tensor>& residual, double eps,
                                double weight_offset) {
     ctx->set_materialize_grads(false);
-    const int64_t N = x.size(0), H = x.size(1);
     const Tensor b = bias.value_or(Tensor()), r = residual.value_or(Tensor());
-    Tensor y = at::empty({N, H}, x.options());
-    Tensor s = r.defined() ? at::empty({N, H}, r.options()) : Tensor();
-    Tensor stats = at::empty({2, N}, x.options().dtype(at::kFloat));  // mean, rstd
-    float* mean = f32(stats);
-    check("flce_layer_norm",
-          g_api.layer_norm(bf16(x), row_stride(x), data(r), r.defined() ? row_stride(r) : 0, r.defined() ? kind(r) : 0,
-                           data(weight), data(b), kind(weight), static_cast<float>(weight_offset),
-                           static_cast<float>(eps), N, H, bf16(y), data(s), mean, mean ? mean + N : nullptr, stream()));
-    ctx->save_for_backward({r.defined() ? s : x, weight, stats});
+    Tensor stats;
+    variable_list out = run_layer_norm(x, weight, b, r, eps, weight_offset, &stats);
+    ctx->save_for_backward({r.defined() ? out[1] : x, weight, stats});
     ctx->saved_data["offset"] = weight_offset;
     ctx->saved_data["bias"] = b.defined();
     ctx->saved_data["residual"] = r.defined();
-    return r.defined() ? variable_list{y, s} : variable_list{y};
+    return out;
   }
 
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
@@ -164,6 +179,8 @@ struct LayerNorm : Function<LayerNorm> {
 
 std::vector<Tensor> layer_norm(const Tensor& x, const Tensor& weight, const std::optional<Tensor>& bias,
                                const std::optional<Tensor>& residual, double eps, double weight_offset) {
+  const Tensor b = bias.value_or(Tensor()), r = residual.value_or(Tensor());
+  if (!wanted({&x, &weight, &b, &r})) return run_layer_norm(x, weight, b, r, eps, weight_offset, nullptr);
   return LayerNorm::apply(x, weight, bias, residual, eps, weight_offset);
 }
 
@@ -178,26 +195,45 @@ struct Transform {
   const flce_logit_transform* get() const { return given ? &t : nullptr; }
 };
 
+// flce_score with k words; logp is undefined without targets, ids and words without
+// words, state where none is kept (keep_rows 0, or it does not pay).
+struct Scores {
+  Tensor logp, lse, entropy, ids, words, state;
+};
+Scores run_score(const Tensor& h, const Tensor& W, const Tensor& targets, int64_t k, int64_t ignore_index,
+                 at::ArrayRef<double> transform, int64_t keep_rows) {
+  const int64_t N = h.size(0), H = h.size(1), V = W.size(0);
+  const auto f32_rows = h.options().dtype(at::kFloat);
+  Scores o;
+  o.lse = at::empty({N}, f32_rows);
+  o.entropy = at::empty({N}, f32_rows);
+  if (targets.defined()) o.logp = at::empty({N}, f32_rows);
+  if (k > 0) {
+    o.ids = at::empty({N, k}, h.options().dtype(at::kLong));
+    o.words = at::empty({N, k}, f32_rows);
+  }
+  const size_t kept = keep_rows > 0 ? g_api.score_state_bytes(N, H, V, keep_rows) : 0;
+  if (kept) o.state = bytes(kept, h);
+  Tensor ws = bytes(g_api.score_workspace_bytes(N, H, V, k), h);
+  const Transform tf(transform);
+  check("flce_score", g_api.score(bf16(h), bf16(W), static_cast<const int64_t*>(data(targets)), N, H, V, k, ignore_index,
+                                  tf.get(), f32(o.logp), f32(o.lse), f32(o.entropy),
+                                  static_cast<int64_t*>(data(o.ids)), f32(o.words), data(o.state), data(ws), ws.numel(),
+                                  stream()));
+  return o;
+}
+
 struct Score : Function<Score> {
   static variable_list forward(AutogradContext* ctx, const Tensor& h, const Tensor& W, const Tensor& targets,
                                int64_t chunk_rows, int64_t ignore_index, std::vector<double> transform,
                                bool recompute) {
     ctx->set_materialize_grads(false);
-    const int64_t N = h.size(0), H = h.size(1), V = W.size(0);
-    const auto f32_rows = h.options().dtype(at::kFloat);
-    Tensor logp = at::empty({N}, f32_rows), lse = at::empty({N}, f32_rows), entropy = at::empty({N}, f32_rows);
-    const size_t kept = recompute ? 0 : g_api.score_state_bytes(N, H, V, chunk_rows);
-    Tensor state = kept ? bytes(kept, h) : Tensor();
-    Tensor ws = bytes(g_api.score_workspace_bytes(N, H, V, 0), h);
-    const Transform tf(transform);
-    check("flce_score", g_api.score(bf16(h), bf16(W), static_cast<const int64_t*>(data(targets)), N, H, V, 0,
-                                    ignore_index, tf.get(), f32(logp), f32(lse), f32(entropy), nullptr, nullptr,
-                                    data(state), data(ws), ws.numel(), stream()));
-    ctx->save_for_backward({h, W, targets, lse, entropy, state});
+    Scores o = run_score(h, W, targets, 0, ignore_index, transform, recompute ? 0 : chunk_rows);
+    ctx->save_for_backward({h, W, targets, o.lse, o.entropy, o.state});
     ctx->saved_data["rows"] = chunk_rows;
     ctx->saved_data["ignore"] = ignore_index;
     ctx->saved_data["transform"] = std::move(transform);
-    return {logp, entropy};
+    return {o.logp, o.entropy};
   }
 
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
@@ -226,7 +262,20 @@ struct Score : Function<Score> {
 
 std::vector<Tensor> score(const Tensor& h, const Tensor& W, const Tensor& targets, int64_t chunk_rows,
                           int64_t ignore_index, at::ArrayRef<double> transform, bool recompute) {
+  if (!wanted({&h, &W})) {
+    Scores o = run_score(h, W, targets, 0, ignore_index, transform, 0);
+    return {o.logp, o.entropy};
+  }
   return Score::apply(h, W, targets, chunk_rows, ignore_index, transform.vec(), recompute);
+}
+
+// ids, words, lse, entropy, and with targets logp
+std::vector<Tensor> top(const Tensor& h, const Tensor& W, int64_t k, const std::optional<Tensor>& targets,
+                        int64_t ignore_index, at::ArrayRef<double> transform) {
+  Scores o = run_score(h, W, targets.value_or(Tensor()), k, ignore_index, transform, 0);
+  std::vector<Tensor> out{o.ids, o.words, o.lse, o.entropy};
+  if (o.logp.defined()) out.push_back(o.logp);
+  return out;
 }
 
 }  // namespace
@@ -237,4 +286,5 @@ TORCH_LIBRARY(flce, m) {
         &layer_norm);
   m.def("score(Tensor h, Tensor W, Tensor targets, int chunk_rows, int ignore_index, float[] transform, bool recompute)"
         " -> Tensor[]", &score);
+  m.def("top(Tensor h, Tensor W, int k, Tensor? targets, int ignore_index, float[] transform) -> Tensor[]", &top);
 }

@@ -2,7 +2,7 @@
 x, or the residual stream with x added to it, and is differentiable.  Every
 arithmetic step runs in libflce's CUDA kernels (include/flce.h states the
 formulas); this module checks tensor properties, allocates outputs and passes
-pointers (the differentiable call leaves the last two to csrc/torch_ops.cpp).
+pointers (``layer_norm`` leaves the last two to csrc/torch_ops.cpp).
 """
 from __future__ import annotations
 
@@ -24,34 +24,24 @@ def _check_all(x, weight, bias, residual):
     return ld
 
 
-def _norm(x, weight, bias, residual, eps, weight_offset, need_stats, stream):
-    """(y, stream or None, stats): stats [2,N] the rows' mean and rstd, or None."""
-    if _elsewhere(x):
-        with torch.cuda.device(x.device):
-            return _norm(x, weight, bias, residual, eps, weight_offset, need_stats, stream)
-    ldx, ldr = _check_all(x, weight, bias, residual)
-    N, H = x.shape
-    y = torch.empty_like(x)  # contiguous, also for rows out of a wider buffer
-    s = None if residual is None else torch.empty_like(residual)
-    stats = mean = rstd = None
-    if need_stats:
-        stats = torch.empty((2, N), dtype=torch.float32, device=x.device)
-        if N:
-            mean = stats.data_ptr()
-            rstd = mean + 4 * N
-    _lib.check("flce_layer_norm", _lib.flce_layer_norm(
-        x, ldx, residual, ldr, 0 if residual is None else _TYPES[residual.dtype], weight, bias, _TYPES[weight.dtype],
-        weight_offset, eps, N, H, y, s, mean, rstd, stream))
-    return y, s, stats
-
-
 def layer_norm_forward(x, weight, bias=None, residual=None, eps: float = 1e-5, weight_offset: float = 0.0, stream=None,
                        need_stats: bool = True):
     """dict(y[N,H] bf16, residual[N,H] or None, mean[N], rstd[N] f32 or None) on
     device.  The stream s = round(x + residual) comes back as ``residual``, in the
     residual's type; y = (s - mean) rstd (weight + weight_offset) + bias."""
-    y, s, stats = _norm(x, weight, bias, residual, eps, weight_offset, need_stats, stream)
-    mean, rstd = (None, None) if stats is None else stats.unbind(0)
+    ldx, ldr = _check_all(x, weight, bias, residual)
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return layer_norm_forward(x, weight, bias, residual, eps, weight_offset, stream, need_stats)
+    N, H = x.shape
+    y = torch.empty_like(x)  # contiguous, also for rows out of a wider buffer
+    s = None if residual is None else torch.empty_like(residual)
+    mean = rstd = None
+    if need_stats:
+        mean, rstd = torch.empty((2, N), dtype=torch.float32, device=x.device).unbind(0)
+    _lib.check("flce_layer_norm", _lib.flce_layer_norm(
+        x, ldx, residual, ldr, 0 if residual is None else _TYPES[residual.dtype], weight, bias, _TYPES[weight.dtype],
+        weight_offset, eps, N, H, y, s, mean, rstd, stream))
     return {"y": y, "residual": s, "mean": mean, "rstd": rstd}
 
 
@@ -103,20 +93,15 @@ def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, weight_of
     residual's type, y = (s - mean(s)) (var(s) + eps)^(-1/2) (weight +
     weight_offset) + bias in bf16.  x [N,H] bf16; residual [N,H] bf16 or fp32;
     weight and bias [H] of one type, bf16 or fp32; differentiable in all four."""
-    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or
-                                    (bias is not None and bias.requires_grad) or
-                                    (residual is not None and residual.requires_grad)):
-        _check_all(x, weight, bias, residual)
-        if _elsewhere(x):
-            with torch.cuda.device(x.device):
-                return layer_norm(x, weight, bias, residual, eps, weight_offset)
-        try:
-            out = (_lib._TORCH_OPS or _lib.torch_ops())[0](x, weight, bias, residual, eps, weight_offset)
-        except RuntimeError as e:
-            raise _lib.torch_error(e) from None
-        return out[0] if residual is None else tuple(out)
-    y, s, _ = _norm(x, weight, bias, residual, eps, weight_offset, False, None)
-    return y if s is None else (y, s)
+    _check_all(x, weight, bias, residual)
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return layer_norm(x, weight, bias, residual, eps, weight_offset)
+    try:
+        out = (_lib._TORCH_OPS or _lib.torch_ops())[0](x, weight, bias, residual, eps, weight_offset)
+    except RuntimeError as e:
+        raise _lib.torch_error(e) from None
+    return out[0] if residual is None else tuple(out)
 
 
 class LayerNorm(torch.nn.Module):

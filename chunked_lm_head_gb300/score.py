@@ -5,8 +5,8 @@ and the entropy, differentiable in both; ``top_logprobs`` the K likeliest words
 of each row with their log-probabilities.  ``score_forward`` and
 ``score_backward`` are the calls below them.  Every arithmetic step runs in
 libflce's CUDA kernels (include/flce.h states the formulas); this module checks
-tensor properties, allocates outputs and passes pointers (the differentiable call
-leaves the last two to csrc/torch_ops.cpp).
+tensor properties, allocates outputs and passes pointers (the first two calls leave
+the last two to csrc/torch_ops.cpp).
 """
 from __future__ import annotations
 
@@ -123,27 +123,34 @@ def selective_log_softmax_entropy(h, W, targets, chunk_rows: int = 256, ignore_i
     backward saves their product; recompute=True keeps nothing."""
     if targets is None:
         raise ValueError("targets are needed")
-    if not torch.is_grad_enabled() or not (h.requires_grad or W.requires_grad):
-        out = score_forward(h, W, targets, 0, ignore_index, transform)
-        return out["logp"], out["entropy"]
     _check(h, W, targets)
     if _elsewhere(h):
         with torch.cuda.device(h.device):
             return selective_log_softmax_entropy(h, W, targets, chunk_rows, ignore_index, transform, recompute)
-    tf = _lib.make_transform(transform)
     try:
-        return tuple((_lib._TORCH_OPS or _lib.torch_ops())[1](
-            h, W, targets, chunk_rows, ignore_index,
-            [] if tf is None else [tf.scale_multiply, tf.scale_divide, tf.softcap, tf.temperature], recompute))
+        return tuple((_lib._TORCH_OPS or _lib.torch_ops())[1](h, W, targets, chunk_rows, ignore_index,
+                                                             _lib.transform_list(transform), recompute))
     except RuntimeError as e:
         raise _lib.torch_error(e) from None
 
 
 def top_logprobs(h, W, k: int, targets=None, ignore_index: int = IGNORE_INDEX, transform=None,
                  workspace: torch.Tensor | None = None, stream=None):
-    """score_forward with k words: the alternatives of a sampled token, or the
-    lists (ids, logprobs, and a log-sum-exp of 0) that topk_distill_loss takes
-    of a teacher.  Not differentiable."""
+    """score_forward with k words, dict(ids, logprobs, lse, entropy, logp): the
+    alternatives of a sampled token, or the lists (ids, logprobs, and a log-sum-exp
+    of 0) that topk_distill_loss takes of a teacher.  Not differentiable."""
     if k < 1:
         raise ValueError("k must be at least 1")
-    return score_forward(h, W, targets, k, ignore_index, transform, workspace, stream)
+    if workspace is not None or stream is not None or _elsewhere(h):
+        out = score_forward(h, W, targets, k, ignore_index, transform, workspace, stream)
+        del out["state"]
+        return out
+    _check(h, W, targets)
+    if k > W.shape[0]:
+        raise ValueError("k must be between 0 and the vocabulary")
+    try:
+        out = (_lib._TORCH_OPS or _lib.torch_ops())[2](h, W, k, targets, ignore_index, _lib.transform_list(transform))
+    except RuntimeError as e:
+        raise _lib.torch_error(e) from None
+    return {"ids": out[0], "logprobs": out[1], "lse": out[2], "entropy": out[3],
+            "logp": None if targets is None else out[4]}
