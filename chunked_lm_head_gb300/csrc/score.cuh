@@ -405,6 +405,14 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) score_select_kernel(const
       }
     __syncthreads();
   };
+  auto zero_row = [&] {
+    bool any = false;
+    for (int k = t * 8; k < p.H; k += T * 8) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(h + k));
+      any |= ((x.x | x.y | x.z | x.w) & 0x7fff7fffu) != 0u;
+    }
+    return __syncthreads_or(any) == 0;
+  };
 #pragma unroll 4
   for (int c = t; c < units; c += T) {
     const float2 q = unit(c);
@@ -449,6 +457,14 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) score_select_kernel(const
       listed = kept_words;
     }
     settle(0, listed);
+  } else if (zero_row()) {
+    // (a row of padding, of which a batch may hold many: nothing to sum)
+    for (int e = t; e < K; e += T) {
+      val[e] = make_float2(0.f, 0.f);
+      word[e] = e;
+    }
+    if (t == 0) target_z = make_float2(0.f, 0.f);
+    __syncthreads();
   } else {
     // kept: words at the list's front that are settled; total: those in the list
     int kept = 0, total = 0;

@@ -112,12 +112,15 @@ ScoreLayout score_layout(int64_t N, int64_t H, int64_t V, int64_t k, const Score
 }
 
 // How far a record or logit of the forward can be off the row's exact logits,
-// relative to their largest magnitude: each of H / 16 steps cuts its running sum
-// by less than one unit of its last place, 2^-23 of it; the running sum may be 4
-// times the row's largest logit (and the few-row forward's rounded sums are off
-// by less); the column in a record's low bits changes it by 2^-18.
+// relative to their largest magnitude.  Each of H / 16 steps cuts its running sum
+// by less than one unit of its last place, 2^-23 of it (the few-row forward's
+// rounded sums are off by less).  The running sum is at most |h| |w|, which is
+// sqrt(H) / 4 times the row's largest logit where that is as large as the largest
+// of some 30,000 products of random directions (4 |h| |w| / sqrt(H)), and 4 times
+// is allowed for at least.  The column in a record's low bits changes it by 2^-18.
 float score_slack(int64_t H) {
-  return static_cast<float>(4.0 * static_cast<double>(ceil_div(H, UMMA_K)) / 8388608.0 + 1.0 / 131072.0);
+  const double steps = static_cast<double>(ceil_div(H, UMMA_K));
+  return static_cast<float>(std::max(4.0, std::sqrt(static_cast<double>(H)) / 4.0) * steps / 8388608.0 + 1.0 / 131072.0);
 }
 
 flce_status score_rows(const ScorePlan& q, bool kLong, const ScoreRows& rows, const float4* part, const float2* rec,

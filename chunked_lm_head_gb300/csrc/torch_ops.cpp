@@ -103,6 +103,10 @@ variable_list first_order(variable_list grads, const variable_list& inputs) {
   return grads;
 }
 
+// gradients of a node's inputs: as many as it may have (those past the last input
+// are undefined, and dropped)
+constexpr size_t kInputs = 16;
+
 int64_t row_stride(const Tensor& x) { return x.size(0) > 1 ? x.stride(0) : x.size(1); }
 
 // y, and with a residual the stream; stats [2,N] (mean, rstd) where they are wanted.
@@ -151,8 +155,10 @@ struct LayerNorm : Function<LayerNorm> {
     const bool need_b = has_b && ctx->needs_input_grad(2), need_r = has_r && ctx->needs_input_grad(has_b ? 3 : 2);
     const Tensor ds0 = grads.size() > 1 ? grads[1] : Tensor();
     if (!grads[0].defined()) {  // only the stream was used
-      if (!ds0.defined()) return variable_list(6);
-      return {need_x ? ds0.to(at::kBFloat16) : Tensor(), Tensor(), Tensor(), need_r ? ds0 : Tensor(), Tensor(), Tensor()};
+      if (!ds0.defined()) return variable_list(kInputs);
+      variable_list out{need_x ? ds0.to(at::kBFloat16) : Tensor(), Tensor(), Tensor(), need_r ? ds0 : Tensor()};
+      out.resize(kInputs);
+      return out;
     }
     const Tensor dy = rows_of(grads[0]), ds = rows_of(ds0);
     const int64_t N = s.size(0), H = s.size(1);
@@ -172,7 +178,7 @@ struct LayerNorm : Function<LayerNorm> {
                                       ws.defined() ? ws.numel() : 0, stream()));
     variable_list out{need_x ? dx : Tensor(), dw, db, need_r ? (wide ? dr : dx) : Tensor()};
     out = first_order(std::move(out), {s, weight, grads[0], ds0});
-    out.resize(6);
+    out.resize(kInputs);
     return out;
   }
 };
@@ -238,7 +244,7 @@ struct Score : Function<Score> {
 
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
     const bool need_h = ctx->needs_input_grad(0), need_W = ctx->needs_input_grad(1);
-    if ((!grads[0].defined() && !grads[1].defined()) || !(need_h || need_W)) return variable_list(7);
+    if ((!grads[0].defined() && !grads[1].defined()) || !(need_h || need_W)) return variable_list(kInputs);
     const variable_list saved = ctx->get_saved_variables();
     const Tensor &h = saved[0], &W = saved[1], &targets = saved[2], &lse = saved[3], &entropy = saved[4],
                  &state = saved[5];
@@ -255,7 +261,7 @@ struct Score : Function<Score> {
                                f32(ga), f32(ge), data(state), bf16(dH), data(dW), FLCE_BF16, N, H, V, rows,
                                ctx->saved_data["ignore"].toInt(), tf.get(), data(ws), ws.numel(), stream()));
     variable_list out = first_order({dH, dW}, {h, W, grads[0], grads[1]});
-    out.resize(7);
+    out.resize(kInputs);
     return out;
   }
 };

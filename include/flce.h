@@ -745,7 +745,9 @@ FLCE_API size_t flce_layer_norm_backward_workspace_bytes(int64_t N, int64_t H);
  *   entropy  = -sum_v p_v log p_v     (natural units)
  *   ids      = the k words of largest z in descending order, ties to the lowest
  *              index (of equal sums; the order is that of the sums of h W^T to
- *              about 2^-45, not of the tensor cores' fp32 ones)
+ *              about 2^-45, not of the tensor cores' fp32 ones, so long as these
+ *              are off by no more than they can be where |h| |w| is at most
+ *              max(16, sqrt(H)) / 4 times the row's largest logit)
  *   logprobs = u_ids - lse.
  *   targets  [N] int64 or NULL.  A row whose target is ignore_index is skipped:
  *            its outputs are 0 and its ids -1.  A target outside [0,V) gives a

@@ -122,6 +122,18 @@ def test_equal_logits_go_to_the_lowest_index(N, V, K):
     assert _lib.flce_device_status() == 0
 
 
+@pytest.mark.parametrize("N,V,K", [(700, 120000, 20), (3, 120000, 20), (700, 2500, 128)])
+def test_rows_of_padding(N, V, K):
+    """Most rows zero (also with -0): their words are the first, and they cost no sums."""
+    h, W, t, _, _ = make(N, 256, V, seed=26)
+    h[1:] = 0
+    h[2, 5] = -0.0
+    r = R.reference(h, W, t, K)
+    out = flce.top_logprobs(h, W, K, t)
+    R.check(out, h, W, t, r, K)
+    assert torch.equal(out["ids"][1:], torch.arange(K, device="cuda").expand(N - 1, K))
+
+
 @pytest.mark.parametrize("N", [1, 3, 140])
 @pytest.mark.parametrize("V,K", [(40000, 50), (2000, 50)])
 def test_words_that_are_neighbours(N, V, K):
@@ -269,6 +281,19 @@ def test_kept_and_recomputed_through_autograd():
         with torch.no_grad():
             R.check_grads(*grads, h, W, t, r, ga, ge, kept=kept)
         assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+@pytest.mark.parametrize("N,H,chunk", [(20, 64, 256), (200, 512, 256), (300, 64, 128), (400, 512, 128)])
+def test_no_counted_row_has_no_gradient(N, H, chunk):
+    h, W, t, ga, ge = make(N, H, 3001, seed=27)
+    t[:] = R.IGNORE
+    h.requires_grad_(True)
+    W.requires_grad_(True)
+    logp, entropy = flce.selective_log_softmax_entropy(h, W, t, chunk_rows=chunk)
+    assert not bool(logp.any()) and not bool(entropy.any())
+    dH, dW = torch.autograd.grad((logp, entropy), (h, W), (ga, ge))
+    assert not bool(dH.any()) and not bool(dW.any())
+    assert _lib.flce_device_status() == 0
 
 
 def test_likely_targets_keep_their_gradient():
