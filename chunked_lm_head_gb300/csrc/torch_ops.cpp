@@ -4,8 +4,10 @@
 // are cold, and takes 177 this way.  Marshalling only, as the ctypes binding: the arithmetic runs
 // behind include/flce.h, whose entry points `bind` takes from the library that the
 // binding has loaded.  The callers in Python have checked the tensors.
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/variable.h>
 #include <torch/library.h>
 
 #include <string>
@@ -124,11 +126,24 @@ variable_list run_layer_norm(const Tensor& x, const Tensor& weight, const Tensor
   return r.defined() ? variable_list{y, s} : variable_list{y};
 }
 
+// Whether a graph is to be built.  A leaf that an eager graph still holds passes its
+// gradient on the stream of that graph; where that is the default one and this call
+// is being captured, the backward's wait between the two would end the capture and
+// the process with it, so the call is refused while that can be told.
 bool wanted(std::initializer_list<const Tensor*> inputs) {
   if (!at::GradMode::is_enabled()) return false;
-  for (const Tensor* t : inputs)
-    if (t->defined() && t->requires_grad()) return true;
-  return false;
+  bool any = false;
+  for (const Tensor* t : inputs) any |= t->defined() && t->requires_grad();
+  if (!any || c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return any;
+  for (const Tensor* t : inputs) {
+    if (!t->defined() || !t->requires_grad() || !t->is_leaf()) continue;
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
+    const auto on = node ? node->stream() : std::nullopt;
+    TORCH_CHECK(!on || *on != c10::cuda::getDefaultCUDAStream(on->device_index()).unwrap(),
+                "an eager graph of a leaf of this call is alive: drop it (the losses and outputs made of it) before "
+                "the call is captured");
+  }
+  return true;
 }
 
 struct LayerNorm : Function<LayerNorm> {

@@ -92,7 +92,10 @@ def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, weight_of
     """y, or (y, stream) with a residual: the stream s = round(x + residual) in the
     residual's type, y = (s - mean(s)) (var(s) + eps)^(-1/2) (weight +
     weight_offset) + bias in bf16.  x [N,H] bf16; residual [N,H] bf16 or fp32;
-    weight and bias [H] of one type, bf16 or fp32; differentiable in all four."""
+    weight and bias [H] of one type, bf16 or fp32; differentiable in all four.
+
+    Captured into a CUDA graph, a call whose leaves an eager graph still holds is
+    refused: PyTorch's backward could not be captured beside it."""
     _check_all(x, weight, bias, residual)
     if _elsewhere(x):
         with torch.cuda.device(x.device):

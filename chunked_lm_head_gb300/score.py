@@ -120,7 +120,10 @@ def selective_log_softmax_entropy(h, W, targets, chunk_rows: int = 256, ignore_i
 
     chunk_rows bounds the rows of dlogits that the backward holds.  A call of at
     most that many rows keeps its logits until then, 2 bytes each, and the
-    backward saves their product; recompute=True keeps nothing."""
+    backward saves their product; recompute=True keeps nothing.
+
+    Captured into a CUDA graph, a call whose leaves an eager graph still holds is
+    refused: PyTorch's backward could not be captured beside it."""
     if targets is None:
         raise ValueError("targets are needed")
     _check(h, W, targets)

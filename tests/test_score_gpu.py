@@ -428,6 +428,34 @@ def test_capture_and_replay(N, H):
     assert _lib.flce_device_status() == 0
 
 
+def test_a_capture_beside_a_live_eager_graph_is_refused():
+    h, W, t, ga, ge = make(150, 64, 5001, seed=28)
+    h.requires_grad_(True)
+    W.requires_grad_(True)
+    w = torch.ones(64, device="cuda", dtype=BF16, requires_grad=True)
+
+    def step():
+        logp, entropy = flce.selective_log_softmax_entropy(flce.layer_norm(h, w), W, t)
+        return torch.autograd.grad((logp, entropy), (h, W, w), (ga, ge))
+
+    want = step()
+    for alive in (lambda: flce.layer_norm(h, w.detach()), lambda: flce.layer_norm(h.detach(), w),
+                  lambda: flce.selective_log_softmax_entropy(h.detach(), W, t)):
+        held = alive()
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises(RuntimeError, match="eager graph of a leaf"):
+            with torch.cuda.graph(graph):
+                step()
+        del held, graph
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert _lib.flce_device_status() == 0
+
+
 def test_a_callers_workspace():
     h, W, t, ga, ge = make(200, 64, 9001, seed=19)
     ws = torch.full((_lib.flce_score_workspace_bytes(200, 64, 9001, 5),), 255, dtype=torch.uint8, device="cuda")
