@@ -378,8 +378,9 @@ static flce_status backward_impl(const flce_bf16* h, const flce_bf16* W, const i
   // ignored rows cost nothing in the three backward GEMMs.  Their dH rows are
   // zeroed up front.  A problem of one row tile gains nothing from it (its
   // GEMMs cover one tile of rows whatever the count), so it skips the listing
-  // and gathering launches.
-  const bool compact = compact_on() && N > tm;
+  // and gathering launches.  (The scores' does not: an ignored row's h may hold
+  // anything, also NaN, and is kept out of dW.)
+  const bool compact = compact_on() && (N > tm || score != nullptr);
   int* cidx = reinterpret_cast<int*>(wb + L.idx);
   int* cblk = reinterpret_cast<int*>(wb + L.blk);
   int* ccount = reinterpret_cast<int*>(wb + L.count);

@@ -370,7 +370,7 @@ KeepBwdPlan keep_bwd_plan(int64_t N, int64_t H, int64_t V, int workers, int tm) 
   const size_t d_rows = static_cast<size_t>(k.fp.lo > 0 ? 2 * k.fp.lo : N);
   k.D = take(d_rows * k.fp.ldD * 2);
   k.dh_part = take(k.fp.b.dh_f32 ? static_cast<size_t>(k.fp.b.dh_splits) * k.fp.R * H * 4 : 0);
-  k.hc = take(N > kKeepCompactRows ? static_cast<size_t>(N) * H * 2 : 0);
+  k.hc = take(static_cast<size_t>(N) * H * 2);
   k.total = o;
   return k;
 }
@@ -392,15 +392,14 @@ flce_status score_backward_kept(const flce_bf16* h, const flce_bf16* W, const in
   const bool kLong = std::max<long long>(N, 2 * fp.lo) * fp.ldD >= INT_MAX || N * H >= INT_MAX || V * H >= INT_MAX ||
                      static_cast<long long>(fp.b.dh_splits) * fp.R * H >= INT_MAX;
   if (compact && dH) FLCE_CUDA_TRY(cudaMemsetAsync(dH, 0, static_cast<size_t>(N) * H * 2, st));
-  if (compact) {
-    const flce_status sg = gather_rows(h, H, idx, count, Ni, 0, N, hc, st);
-    if (sg != FLCE_OK) return sg;
-  }
   {
     ProfScope ps(K_DLOGITS, st);
     const long long runs = ceil_div(fp.ldD, TOPK_DL_COLS);
     const int steps = static_cast<int>(std::max<long long>(1, std::min<long long>(4, runs * N / (16LL * device_sms()))));
     ScoreDlogits d{};
+    d.h = h;
+    d.hc = dW != nullptr || sc.dW16 != nullptr ? hc : nullptr;
+    d.H = static_cast<int>(H);
     d.E = reinterpret_cast<const uint16_t*>(state + K.E);
     d.mx = reinterpret_cast<const float*>(state + K.mx);
     d.D = D;
@@ -434,7 +433,7 @@ flce_status score_backward_kept(const flce_bf16* h, const flce_bf16* W, const in
   FLCE_CUDA_TRY(cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_device_error));
   const int d_rows = fp.lo > 0 ? static_cast<int>(2 * fp.lo) : Ni;
   CUtensorMap W_mn, B_dw, dW_map, dhp_map, D_k, D_mn;
-  if (!make_map(&W_mn, W, H, V, H, 64, BK) || !make_map(&B_dw, compact ? hc : h, H, N, H, 64, BK) ||
+  if (!make_map(&W_mn, W, H, V, H, 64, BK) || !make_map(&B_dw, hc, H, N, H, 64, BK) ||
       !make_map(&D_k, D, fp.ldD, d_rows, fp.ldD, BK, BM) || !make_map(&D_mn, D, fp.ldD, d_rows, fp.ldD, 64, BK))
     return FLCE_ERR_CUDA;
   if (dW && !make_map_t(&dW_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dW, H, V, H, 32, 32)) return FLCE_ERR_CUDA;

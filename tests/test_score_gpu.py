@@ -283,6 +283,27 @@ def test_kept_and_recomputed_through_autograd():
         assert all(torch.equal(a, b) for a, b in zip(grads, again))
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("N,H", [(2, 64), (20, 512), (128, 64), (129, 64), (200, 512), (256, 1096), (300, 64), (700, 512)])
+def test_what_ignored_rows_hold_goes_nowhere(N, H, value):
+    h, W, t, ga, ge = make(N, H, 3001, seed=29, mask=0.3)
+    t[N // 2] = R.IGNORE
+    h2 = h.clone()
+    h2[t == R.IGNORE] = value
+
+    def step(x, chunk, recompute):
+        x, y = x.detach().requires_grad_(True), W.detach().requires_grad_(True)
+        out = flce.selective_log_softmax_entropy(x, y, t, chunk_rows=chunk, recompute=recompute)
+        top = flce.top_logprobs(x.detach(), y.detach(), 5, t)
+        return [o.detach() for o in out] + [top[k] for k in ("ids", "logprobs", "lse", "entropy", "logp")] + list(
+            torch.autograd.grad(out, (x, y), (ga, ge)))
+
+    for chunk, recompute in ((128, True), (256, False), (256, True), (1024, False)):
+        for a, b in zip(step(h, chunk, recompute), step(h2, chunk, recompute)):
+            assert torch.equal(a, b), (chunk, recompute)
+    assert _lib.flce_device_status() == 0
+
+
 @pytest.mark.parametrize("N,H,chunk", [(20, 64, 256), (200, 512, 256), (300, 64, 128), (400, 512, 128)])
 def test_no_counted_row_has_no_gradient(N, H, chunk):
     h, W, t, ga, ge = make(N, H, 3001, seed=27)
