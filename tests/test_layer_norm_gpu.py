@@ -256,3 +256,33 @@ def test_module():
     y.float().sum().backward()
     assert m.weight.grad.shape == (256,) and torch.equal(m.bias.grad, torch.full_like(m.bias, 5.0))
     assert flce.LayerNorm(256, bias=False).bias is None
+
+
+@pytest.mark.parametrize("residual", [None, BF16], ids=["none", "bf16"])
+def test_rows_past_32_bit_offsets(residual):
+    """N H beyond 2^31: the last rows as a call of their own gives them."""
+    N, H, n = 1045000, 2064, 37
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(n, H, generator=g, device="cuda").bfloat16()
+    dy = torch.randn(n, H, generator=g, device="cuda").bfloat16()
+    w = torch.randn(H, generator=g, device="cuda")
+    many = torch.zeros(N, H, device="cuda", dtype=BF16)
+    many[-n:] = x
+    dys = torch.zeros(N, H, device="cuda", dtype=BF16)
+    dys[-n:] = dy
+    r = None if residual is None else many.clone()
+    a = flce.layer_norm_forward(many, w, None, r, eps=EPS)
+    b = flce.layer_norm_forward(x, w, None, None if r is None else x, eps=EPS)
+    for k in ("y", "residual", "mean", "rstd"):
+        if a[k] is not None:
+            assert torch.equal(a[k][-n:], b[k]), k
+    assert not bool(a["y"][:1000].any())
+    sa, sb = (many, x) if r is None else (a["residual"], b["residual"])
+    ga = flce.layer_norm_backward(dys, sa, w, a["mean"], a["rstd"])
+    gb = flce.layer_norm_backward(dy, sb, w, b["mean"], b["rstd"])
+    assert torch.equal(ga[0][-n:], gb[0]) and not bool(ga[0][:1000].any())
+    _, dweight, dbias = R.backward(dy, None, sb, w, EPS, 0.0)
+    _, bw, bb = R.backward_bounds(dy, None, sb, w, EPS, 0.0)
+    assert_within(ga[2], dweight, 1.01 * dweight.abs() * R.half_step(F32) + bw, "dw")
+    assert_within(ga[3], dbias, 1.01 * dbias.abs() * R.half_step(F32) + bb, "db")
+    assert _lib.flce_device_status() == 0

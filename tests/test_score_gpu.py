@@ -552,3 +552,23 @@ def test_a_head_past_32_bit_offsets():
         out = flce.top_logprobs(h[:n].contiguous(), W, 16)
         assert torch.equal(out["ids"], want[:n])
         assert float((out["lse"].double() - z[:n].logsumexp(1)).abs().max()) < 1e-4
+
+
+@pytest.mark.parametrize("recompute", [False, True])
+def test_kept_logits_past_32_bit_offsets(recompute):
+    """N V beyond 2^31, gradients of the last rows alone."""
+    N, H, V, n = 16400, 512, 131104, 200
+    h, W, t, ga, ge = make(N, H, V, seed=30)
+    ga[:-n] = 0
+    ge[:-n] = 0
+    h.requires_grad_(True)
+    W.requires_grad_(True)
+    out = flce.selective_log_softmax_entropy(h, W, t, chunk_rows=N, recompute=recompute)
+    dH, dW = torch.autograd.grad(out, (h, W), (ga, ge))
+    assert _lib.flce_device_status() == 0
+    with torch.no_grad():
+        end = [x[-n:].contiguous() for x in (h, t, out[0], out[1], ga, ge, dH)]
+        r = R.reference(end[0], W, end[1])
+        R.check(dict(logp=end[2], entropy=end[3]), end[0], W, end[1], r)
+        R.check_grads(end[6], dW, end[0], W, end[1], r, end[4], end[5], kept=not recompute)
+        assert not bool(dH[:-n].any())
