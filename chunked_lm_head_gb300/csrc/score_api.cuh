@@ -58,6 +58,37 @@ bool keep_pays(int64_t N, int64_t H, int64_t chunk_rows) {
          (H >= kKeepMinHidden || N <= BM);
 }
 
+// Whether a call lists the rows that count and leaves the others out.
+bool score_skips(int64_t N, bool keep, bool gemv) {
+  return keep ? N > kKeepCompactRows : !gemv && N >= skip_min_rows();
+}
+
+// The forward's splits where the device alone knows how many row tiles it has:
+// planned for all of them, six row tiles in 12 splits of 11 column tiles keep 72 of
+// 76 pairs busy, and five keep 60 as long.  So the splits are those that do best
+// over every count from half the row tiles on (a unit costs a tenth of a tile beside
+// its tiles: its partials, and its targets).  1,501 rows, a quarter masked, x 1,096 x
+// 32,003: 86 us, 90 with the splits for all rows.
+void plan_counted(FwdPlan& f, long long rows, int workers, size_t partials_cap) {
+  if (opt(FLCE_OPT_FWD_SPLITS) > 0) return;
+  const long long fit = std::max(1LL, static_cast<long long>(partials_cap) / (8 * std::max(1LL, rows)));
+  const int smax = static_cast<int>(std::min<long long>(std::min(f.n_tiles, 256), fit));
+  double best = 1e300;
+  for (int s = 1; s <= smax; ++s) {
+    const int tps = static_cast<int>(ceil_div(f.n_tiles, s)), se = static_cast<int>(ceil_div(f.n_tiles, tps));
+    double cost = 0.;
+    for (int m = (f.m_tiles + 1) / 2; m <= f.m_tiles; ++m)
+      cost += static_cast<double>(ceil_div(static_cast<long long>(m) * se, workers)) * (tps + 0.1) / m;
+    if (cost < best) {
+      best = cost;
+      f.S = se;
+      f.tps = tps;
+    }
+  }
+  f.units = f.m_tiles * f.S;
+  f.grid = std::min(f.units, workers);
+}
+
 struct ScorePlan {
   bool gemv = false, dense = false, keep = false;
   long long rows = 0;  // of a launch
@@ -79,6 +110,7 @@ ScorePlan score_plan(int64_t N, int64_t H, int64_t V, int64_t k, bool keep, int 
   }
   // (a row has kScoreParts partials of 16 bytes to a split: four times the 8 that the cap counts)
   q.f = plan_forward(q.rows, H, V, workers, tm, kFwdPartialsCap / 4);
+  if (score_skips(N, keep, q.gemv)) plan_counted(q.f, q.rows, workers, kFwdPartialsCap / 4);
   q.S = q.gemv ? topk_gemv_ctas(V) : kScoreParts * q.f.S;
   return q;
 }
@@ -101,7 +133,7 @@ ScoreLayout score_layout(int64_t N, int64_t H, int64_t V, int64_t k, const Score
   L.rec = take(k > 0 && !q.dense ? rows * q.ld * 8 : 0);
   L.rec3 = take(k > 0 && !q.dense ? rows * q.ld * 4 : 0);
   L.bad = take(256);
-  if (q.keep ? N > kKeepCompactRows : !q.gemv && N >= skip_min_rows()) {
+  if (score_skips(N, q.keep, q.gemv)) {
     L.idx = take(n * 4);
     L.blk = take(static_cast<size_t>(ceil_div(N, COMPACT_ROWS_PER_BLOCK)) * 4);
     L.count = take(256);
