@@ -9,6 +9,8 @@ namespace {
 // the K words share costs 32 products, so the records serve while chunks are
 // many: about K^3 / 6 / chunks^2 of them are shared.  Below 4 K chunks (K / 96
 // shared ones) the logits are held, at 4 bytes instead of 3/8 byte a column.
+// (512 x 1,024, logits / records: 64 / 72 us at 3.9 K chunks, K 64, and 111 / 142, K
+// 128; 164 / 126 at 7.8 K chunks, K 128, and 152 / 97 at 10 K.)
 bool score_dense(int64_t V, int64_t k) { return ceil_div(V, 32) < 4 * k; }
 
 constexpr size_t kScoreBlockBytes = size_t(256) << 20;  // of records or logits held at once
@@ -45,17 +47,25 @@ KeepLayout keep_layout(int64_t N, int64_t V) {
   return L;
 }
 
-// At short rows of h the product costs no more than reading what was kept; but at
-// most 128 rows are kept at any size, since only their dlogits from kept logits
-// take two bf16 parts (fused_lo_rows), and one entry often holds most of so few
-// rows' gradients.
+// At short rows of h the product costs no more than writing and reading what was
+// kept.  Forward and backward with kept logits, and without (us):
+//   rows x vocabulary      H  64        256        384        512        1,024
+//     256 x 151,936        144 / 156  154 / 167  178 / 192  190 / 213  265 / 310
+//     512 x 151,936        227 / 215  235 / 228
+//   1,024 x 151,936        350 / 328  374 / 355  436 / 427
+//   2,048 x 151,936                   648 / 630             830 / 870
+//   4,096 x  32,000                   331 / 329             409 / 436  615 / 706
+// So from 512 on, and up to one tile of rows, which are not compacted and whose
+// backward is bound by its launches.  (At most 128 rows are kept in any case: only
+// their dlogits from kept logits take two bf16 parts, fused_lo_rows, and one entry
+// often holds most of so few rows' gradients.)
 constexpr int64_t kKeepMinHidden = 512;
 
 // Whether a call of these sizes keeps its logits: they fit the caller's dlogits
 // budget (chunk_rows x V), and reading them costs less than their product again.
 bool keep_pays(int64_t N, int64_t H, int64_t chunk_rows) {
   return N > 0 && N <= kKeepMaxRows && N <= round_up(std::max<int64_t>(1, chunk_rows), BM) &&
-         (H >= kKeepMinHidden || N <= BM);
+         (H >= kKeepMinHidden || N <= kKeepCompactRows);
 }
 
 // Whether a call lists the rows that count and leaves the others out.
@@ -88,6 +98,12 @@ void plan_counted(FwdPlan& f, long long rows, int workers, size_t partials_cap) 
   f.units = f.m_tiles * f.S;
   f.grid = std::min(f.units, workers);
 }
+
+// CTA group of the score forwards.  Up to 128 rows each CTA takes a tile of its
+// own: half of a pair's 256 rows would be empty, and its products cost as much as
+// reading W (33 x 1,536 x 151,936: 98 us, pairs 111; 128 x 4,096: 205 and 211, with
+// words 225 and 240).  The backward keeps the pairs (33 x 1,536: 205 us, 232 without).
+int score_group(int64_t N) { return N <= BM ? 1 : cta_group(); }
 
 struct ScorePlan {
   bool gemv = false, dense = false, keep = false;
@@ -191,6 +207,8 @@ flce_status score_rows(const ScorePlan& q, bool kLong, const ScoreRows& rows, co
     return launch_dependent(kern, dim3(static_cast<unsigned>(rows.rows)), threads, 0, st, p);
   };
   // with a row to an SM, or fewer, a row's latency counts: more warps to its words
+  // (152 rows x 2,048 x 151,936, K 64: 150 us, 170 with 256 threads; 777 x 1,096 x
+  // 32,003, K 37: 138 with 512 threads, 107)
   const bool few = rows.rows <= device_sms();
   auto of = [&](auto dense) -> cudaError_t {
     constexpr bool D = decltype(dense)::value;
@@ -233,7 +251,7 @@ extern "C" {
 
 size_t flce_score_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k) {
   if (!topk_sizes_ok(N, H, V) || k < 0 || k > SCORE_MAX_K || k > V) return 0;
-  const int cg = cta_group();
+  const int cg = score_group(N);
   const int workers = device_workers(cg);
   auto of = [&](bool keep) {
     return score_layout(N, H, V, k, score_plan(N, H, V, k, keep, workers, BM * cg)).total;
@@ -264,7 +282,7 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
     return FLCE_ERR_UNSUPPORTED;
   if (N == 0) return FLCE_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int cg = cta_group(), tm = BM * cg;
+  const int cg = score_group(N), tm = BM * cg;
   const int workers = device_workers(cg);
   const bool keep = state != nullptr;
   const ScorePlan q = score_plan(N, H, V, k, keep, workers, tm);

@@ -69,7 +69,7 @@ def test_sizes():
     s = _lib.flce_score_state_bytes
     assert 0 < s(4096, 1024, 20000, 4096) <= 4096 * (20256 * 2.25 + 16) + 4096
     assert s(4096, 1024, 20000, 3968) == 0 and s(4096, 64, 20000, 4096) == 0 and s(0, 1024, 20000, 4096) == 0
-    assert s(128, 64, 20000, 128) > 0 and s(129, 64, 20000, 256) == 0
+    assert s(128, 64, 20000, 128) > 0 and s(256, 64, 20000, 256) > 0 and s(257, 64, 20000, 512) == 0
     assert s(40000, 1024, 20000, 40000) == 0 and s(5, 1024, 20000, 1) > 0 and s(-1, 1024, 20000, 4096) == 0
 
 
