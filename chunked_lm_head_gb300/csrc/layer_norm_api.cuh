@@ -22,6 +22,9 @@ cudaError_t launch_layer_warps(const LayerParams& p, cudaStream_t st) {
 
 // The shapes of launch_norm_as: a warp to a row where the row fits its
 // registers, else groups of two vectors to a thread, past 8,192 elements four.
+// Warps and groups (us): 65,536 x 256 23 / 29, x 1,024 53 / 70, x 2,560 113 / 164,
+// 32,768 x 4,096 107 / 131; with a bf16 residual x 256 29 / 33, x 512 47 / 47, x
+// 1,024 87 / 86.
 // Three CTAs of 512 threads to an SM with a bf16 stream (16,384 x 4,096 with a
 // residual 88 us, 16,384 x 6,144 126: two CTAs 105 and 135, four 90 and 131), two
 // with fp32 (125 us; three 127, four 135).
