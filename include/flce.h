@@ -750,8 +750,8 @@ FLCE_API size_t flce_layer_norm_backward_workspace_bytes(int64_t N, int64_t H);
  *              max(16, sqrt(H)) / 4 times the row's largest logit)
  *   logprobs = u_ids - lse.
  *   targets  [N] int64 or NULL.  A row whose target is ignore_index is skipped:
- *            its outputs are 0 and its ids -1.  A target outside [0,V) gives a
- *            NaN logp (or FLCE_ERR_BAD_TARGET as in flce_forward).
+ *            its outputs are 0 and its ids -1, whatever its h holds.  A target
+ *            outside [0,V) gives a NaN logp (or FLCE_ERR_BAD_TARGET as in flce_forward).
  *   k        0, or 1 .. min(128, V) (above 128: FLCE_ERR_UNSUPPORTED).
  *   out_logp (needs targets), out_lse, out_entropy [N] fp32, each may be NULL;
  *   out_ids [N,k] int64 and out_logprobs [N,k] fp32: NULL exactly when k is 0,
@@ -774,7 +774,7 @@ FLCE_API flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const in
 FLCE_API size_t flce_score_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k);
 /* Bytes of the state where keeping it pays: the rows fit the backward's dlogits
  * budget (N <= chunk_rows rounded up to 128, and 32,768) and the product costs
- * more than reading them (H >= 512; or, for the gradients' precision, N <= 128).
+ * more than reading them (H >= 512 or N <= 256).
  * Else 0: pass no state. */
 FLCE_API size_t flce_score_state_bytes(int64_t N, int64_t H, int64_t V, int64_t chunk_rows);
 
@@ -787,7 +787,8 @@ FLCE_API size_t flce_score_state_bytes(int64_t N, int64_t H, int64_t V, int64_t 
  * block by block as in flce_backward (chunk_rows bounds the dlogits held at
  * once).  lse, entropy [N] from flce_score; g_logp,
  * g_entropy [N] fp32, each may be NULL (zero).  Rows whose target is
- * ignore_index have no gradient; a target outside [0,V) has no one-hot term.
+ * ignore_index have no gradient and no share in dW, also where their h is not
+ * finite (with FLCE_OPT_COMPACT = 0 and no state it has to be); a target outside [0,V) has no one-hot term.
  *   dH [N,H] bf16, dW [V,H] of dW_type (FLCE_F32 or FLCE_BF16); either may be
  *   NULL, not both.
  * Workspace: flce_score_backward_workspace_bytes (with a state, of the chunk_rows
