@@ -21,8 +21,17 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libflce.so")
+
+
+def _torch_version() -> str | None:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None  # the C library alone
+
+
 # (its name carries the PyTorch it was compiled against)
-TORCH_LIB_PATH = os.path.join(BUILD_DIR, f"flce_torch-{importlib.metadata.version('torch')}.so")
+TORCH_LIB_PATH = os.path.join(BUILD_DIR, f"flce_torch-{_torch_version()}.so")
 TORCH_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
 SOURCES = ["flce.cu"]
 HEADERS = ["ptx.cuh", "gemm.cuh", "small_kernels.cuh", "host_common.cuh", "options.cuh", "plan.cuh",
@@ -91,7 +100,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     when up to date); returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     ops = None
-    if force or not torch_ops_up_to_date():
+    if _torch_version() is not None and (force or not torch_ops_up_to_date()):
         ops_tmp = TORCH_LIB_PATH + f".tmp{os.getpid()}"
         ops = _start_torch_ops(ops_tmp)
     try:

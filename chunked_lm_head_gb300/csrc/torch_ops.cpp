@@ -3,7 +3,8 @@
 // its autograd node in Python, 100 of them on the engine's own thread, whose caches
 // are cold, and takes 177 this way.  Marshalling only, as the ctypes binding: the arithmetic runs
 // behind include/flce.h, whose entry points `bind` takes from the library that the
-// binding has loaded.  The callers in Python have checked the tensors.
+// binding has loaded.  The callers in Python check the tensors, and say what is wrong
+// with them; here only what the kernels' reads and writes rest on is checked again.
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
@@ -51,6 +52,17 @@ void bind(at::IntArrayRef a) {
   take(g_api.score_backward_workspace_bytes, a[7]);
   take(g_api.status_string, a[8]);
 }
+
+// Tensors whose addresses a kernel may take: of one type, on x's device, rows
+// without gaps but for a row stride.
+void expect(const Tensor& t, const Tensor& x, bool type, at::IntArrayRef shape, bool rows = false) {
+  if (!t.defined()) return;
+  TORCH_CHECK(t.is_cuda() && t.device() == x.device() && type && t.sizes() == shape &&
+                  (t.is_contiguous() || (rows && t.stride(1) == 1 && t.stride(0) >= t.size(1))),
+              "flce: an argument has another device, type, shape or layout than the operator takes");
+}
+bool is_bf16(const Tensor& t) { return t.defined() && t.scalar_type() == at::kBFloat16; }
+bool is_parameter(const Tensor& t) { return t.defined() && (t.scalar_type() == at::kFloat || is_bf16(t)); }
 
 void check(const char* fn, flce_status s) {
   TORCH_CHECK(s == FLCE_OK, fn, " failed: ", g_api.status_string(s));
@@ -114,7 +126,12 @@ int64_t row_stride(const Tensor& x) { return x.size(0) > 1 ? x.stride(0) : x.siz
 // y, and with a residual the stream; stats [2,N] (mean, rstd) where they are wanted.
 variable_list run_layer_norm(const Tensor& x, const Tensor& weight, const Tensor& b, const Tensor& r, double eps,
                              double weight_offset, Tensor* stats) {
+  TORCH_CHECK(x.dim() == 2 && g_api.layer_norm, "flce: a matrix is expected, and bound entry points");
   const int64_t N = x.size(0), H = x.size(1);
+  expect(x, x, is_bf16(x), {N, H}, true);
+  expect(r, x, is_parameter(r), {N, H}, true);
+  expect(weight, x, is_parameter(weight), {H});
+  expect(b, x, b.defined() && b.scalar_type() == weight.scalar_type(), {H});
   Tensor y = at::empty({N, H}, x.options());
   Tensor s = r.defined() ? at::empty({N, H}, r.options()) : Tensor();
   if (stats) *stats = at::empty({2, N}, x.options().dtype(at::kFloat));
@@ -223,7 +240,11 @@ struct Scores {
 };
 Scores run_score(const Tensor& h, const Tensor& W, const Tensor& targets, int64_t k, int64_t ignore_index,
                  at::ArrayRef<double> transform, int64_t keep_rows) {
+  TORCH_CHECK(h.dim() == 2 && W.dim() == 2 && k >= 0 && g_api.score, "flce: matrices are expected, and bound entry points");
   const int64_t N = h.size(0), H = h.size(1), V = W.size(0);
+  expect(h, h, is_bf16(h), {N, H});
+  expect(W, h, is_bf16(W), {V, H});
+  expect(targets, h, targets.defined() && targets.scalar_type() == at::kLong, {N});
   const auto f32_rows = h.options().dtype(at::kFloat);
   Scores o;
   o.lse = at::empty({N}, f32_rows);

@@ -53,6 +53,17 @@ def test_backward_refusals(kw, want):
     assert bwd(**kw) == want
 
 
+def test_operators_check_what_the_kernels_rest_on():
+    """torch.ops.flce refuses what its callers here would not pass on."""
+    norm, score, top = _lib.torch_ops()
+    x, t = torch.zeros(3, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int64)
+    for call in (lambda: score(x, x, t, 256, -100, [], False), lambda: top(x, x, 2, None, -100, []),
+                 lambda: norm(x, x[0], None, None, 1e-5, 0.0), lambda: score(x[0], x, t, 256, -100, [], False),
+                 lambda: norm(x[0], x[0], None, None, 1e-5, 0.0)):
+        with pytest.raises(RuntimeError, match="flce: "):
+            call()
+
+
 def test_sizes():
     f = _lib.flce_score_workspace_bytes
     assert f(-1, 64, 1000, 4) == 0 and f(4, 64, 1000, 129) == 0 and f(4, 64, 100, 101) == 0 and f(4, 64, 100, -1) == 0
