@@ -102,8 +102,23 @@ void plan_counted(FwdPlan& f, long long rows, int workers, size_t partials_cap) 
 // CTA group of the score forwards.  Up to 128 rows each CTA takes a tile of its
 // own: half of a pair's 256 rows would be empty, and its products cost as much as
 // reading W (33 x 1,536 x 151,936: 98 us, pairs 111; 128 x 4,096: 205 and 211, with
-// words 225 and 240).  The backward keeps the pairs (33 x 1,536: 205 us, 232 without).
-int score_group(int64_t N) { return N <= BM ? 1 : cta_group(); }
+// words 225 and 240).  So too where pairs' tiles hold so much more than the rows that
+// their waves are more than 1.15 times as many; a tile takes 1.1 times a pair's (us,
+// CTAs / pairs: 300 x 4,096 x 128,256 271 / 302, 384 rows 275 / 308; 256 x 2,048 x
+// 151,936 135 / 125, 900 380 / 352; 600 x 4,096 x 32,000 134 / 117) -- but not where
+// rows start inside a 128-byte line, whose loads are slower, and CTAs make half as
+// many again for a product (384 x 1,096 x 151,936 136 / 133, with 1,088 100 / 109; 777
+// x 1,096 x 32,003 70 / 60).  The backward keeps the pairs (33 x 1,536: 205 us, 232
+// without).
+int score_group(int64_t N, int64_t H, int64_t V) {
+  if (N <= BM || cta_group() == 1) return 1;
+  if (H % 64 != 0) return 2;
+  const long long n = ceil_div(V, BN);
+  return 1.15 * static_cast<double>(ceil_div(ceil_div(N, BM) * n, device_workers(1))) <
+                 static_cast<double>(ceil_div(ceil_div(N, 2 * BM) * n, device_workers(2)))
+             ? 1
+             : 2;
+}
 
 struct ScorePlan {
   bool gemv = false, dense = false, keep = false;
@@ -251,7 +266,7 @@ extern "C" {
 
 size_t flce_score_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t k) {
   if (!topk_sizes_ok(N, H, V) || k < 0 || k > SCORE_MAX_K || k > V) return 0;
-  const int cg = score_group(N);
+  const int cg = score_group(N, H, V);
   const int workers = device_workers(cg);
   auto of = [&](bool keep) {
     return score_layout(N, H, V, k, score_plan(N, H, V, k, keep, workers, BM * cg)).total;
@@ -282,7 +297,7 @@ flce_status flce_score(const flce_bf16* h, const flce_bf16* W, const int64_t* ta
     return FLCE_ERR_UNSUPPORTED;
   if (N == 0) return FLCE_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int cg = score_group(N), tm = BM * cg;
+  const int cg = score_group(N, H, V), tm = BM * cg;
   const int workers = device_workers(cg);
   const bool keep = state != nullptr;
   const ScorePlan q = score_plan(N, H, V, k, keep, workers, tm);
