@@ -257,9 +257,10 @@ cudaError_t launch_listed(int cg, bool kLong, const CUtensorMap& a, const CUtens
 // A launch with the scores' epilogue: MODE_FWD, MODE_FUSED_FWD, MODE_DLOGITS or
 // MODE_PIPE.
 // Two column parts (partial slots): the forwards' 8 epilogue warps.  4,096 x 512 x
-// 151,936 with entropy 414 us, with kept logits 481 and under a soft-cap 575, where 4
-// warps take 431, 576 and 799; from a hidden size of 1,024 on the two are within 3 %
-// (4,096: 2,751 and 2,698, with words 3,177 and 3,220).
+// 151,936 with entropy 414 us, with kept logits 481 and under a soft-cap 575, with
+// words 728, where 4 warps take 431, 576, 799 and 920; at a hidden size of 1,024, with
+// words under a soft-cap, 1,025 and 1,221.  From there on the two are within 3 %
+// (4,096: 2,751 and 2,698, with words 3,083 and 3,019).
 constexpr int kScoreParts = 2;
 template <int MODE, int kScore>
 cudaError_t launch_scored(int cg, bool kLong, const Maps& m, const GemmParams& p, int workers, cudaStream_t st) {

@@ -572,3 +572,22 @@ def test_kept_logits_past_32_bit_offsets(recompute):
         R.check(dict(logp=end[2], entropy=end[3]), end[0], W, end[1], r)
         R.check_grads(end[6], dW, end[0], W, end[1], r, end[4], end[5], kept=not recompute)
         assert not bool(dH[:-n].any())
+
+
+@pytest.mark.parametrize("tf", [None, TFS[2]], ids=["none", "softcap"])
+@pytest.mark.parametrize("N,H,V", [(300, 512, 20011), (384, 512, 20000), (270, 1024, 33001)])
+def test_a_third_row_tile(N, H, V, tf):
+    """Rows that fill one tile of a pair and little of the next, some of them ignored:
+    forward, words, and gradients from kept and recomputed logits."""
+    h, W, t, ga, ge = make(N, H, V, seed=31, mask=0.1)
+    r = R.reference(h, W, t, 20, tf)
+    R.check(flce.score_forward(h, W, t, transform=tf), h, W, t, r, tf=tf)
+    R.check(flce.top_logprobs(h, W, 20, t, transform=tf), h, W, t, r, 20, tf=tf)
+    for keep in (0, 512):
+        o = flce.score_forward(h, W, t, transform=tf, keep_rows=keep)
+        assert (o["state"] is not None) == (keep > 0)
+        R.check(o, h, W, t, r, tf=tf)
+        dH, dW = flce.score_backward(h, W, t, o["lse"], o["entropy"], ga, ge, chunk_rows=512, transform=tf,
+                                     dW_dtype=BF16, state=o["state"])
+        R.check_grads(dH, dW, h, W, t, r, ga, ge, tf, kept=keep > 0)
+    assert _lib.flce_device_status() == 0
